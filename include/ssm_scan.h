@@ -421,6 +421,152 @@ int ssm_ssd_state_update(int64_t batch, int64_t nheads, int64_t headdim, int64_t
                          const float* dt_bias, int softplus, void* y, void* stream);
 
 /*
+ * The gated delta rule: the multi-head state update of ssm_ssd_scan_fwd with
+ * the same gate (Delta, A, dt_bias) and state layout, where a token replaces
+ * what the state holds at its key instead of adding to it. Per batch b, head h
+ * (keys and queries of head h / (nheads / nkheads)), state S (headdim x
+ * dstate, fp32):
+ *
+ *   Delta    = softplus(dt[b,t,h] + dt_bias[h])   (or no softplus)
+ *   beta     = sigmoid(beta[b,t,h])               (or beta as it is)
+ *   k, q     = k / sqrt(|k|^2 + 1e-6), q likewise (qk_norm; or as they are)
+ *   S        = exp(Delta * A[h]) * S
+ *   u[p]     = beta * (v[b,t,h,p] - sum_n S[p][n] k[n])
+ *   S[p][n]  = S[p][n] + u[p] * k[n]
+ *   y[b,t,h,p] = scale * sum_n S[p][n] q[n]
+ *
+ * starting from h0[b,h] (or zero) and ending in h_last[b,h].
+ *   q, k     : (batch, seqlen, nkheads, dstate) io_dtype, nheads a multiple of nkheads
+ *   v, y     : (batch, seqlen, nheads, headdim) io_dtype
+ *   dt, beta : (batch, seqlen, nheads)          io_dtype
+ *   A        : (nheads) fp32, not positive (A * Delta is a log decay);
+ *   dt_bias  : (nheads) fp32, nullable
+ *   h0, h_last : (batch, nheads, headdim, dstate) fp32, nullable; 16-byte aligned
+ * dstate 32, 64, 128 or 256; any headdim; q and k aligned to four elements.
+ */
+
+/*
+ * ssm_gated_delta_fwd -- the gated delta rule over a sequence. bf16 io with
+ * dstate 64 or 128, headdim a multiple of 16, at least 32 tokens and 16-byte
+ * aligned q, k, v and y runs chunk by chunk (64 tokens) on the tensor cores,
+ * every product on the state's path in two fp16 pieces per fp32 operand, so
+ * that h_last is as exact as fp32 arithmetic; other calls run token by token
+ * in fp32. y may be NULL when h_last is given; h_last may be h0.
+ * workspace: at least ssm_gated_delta_workspace_bytes(...) bytes of device
+ * memory, 16-byte aligned (may be NULL when that is 0), used as scratch only;
+ * not by two calls that can run at the same time. seqlen == 0 writes only
+ * h_last. No output may overlap an input or the workspace.
+ */
+size_t ssm_gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,
+                                       int64_t nkheads, int64_t headdim, int64_t dstate,
+                                       int io_dtype);
+int ssm_gated_delta_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkheads,
+                        int64_t headdim, int64_t dstate, int io_dtype, const void* q,
+                        const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, int softplus, int beta_sigmoid,
+                        int qk_norm, float scale, const float* h0, void* y, float* h_last,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ssm_gated_delta_update -- one decode step of the gated delta rule on a
+ * carried state (batch, nheads, headdim, dstate) fp32, updated in place; q, k
+ * (batch, nkheads, dstate), v, y (batch, nheads, headdim), dt, beta (batch,
+ * nheads). fp32 or bf16 io, arithmetic in fp32. y must not overlap the state
+ * or an input.
+ */
+int ssm_gated_delta_update(int64_t batch, int64_t nheads, int64_t nkheads, int64_t headdim,
+                           int64_t dstate, int io_dtype, float* state, const void* q,
+                           const void* k, const void* v, const void* dt, const float* A,
+                           const void* beta, const float* dt_bias, int softplus,
+                           int beta_sigmoid, int qk_norm, float scale, void* y, void* stream);
+
+/*
+ * ssm_gated_delta_bwd -- gradients of
+ *   sum dy * y + sum dh_last * h_last
+ * with y, h_last as ssm_gated_delta_fwd computes them from the same inputs
+ * (states are recomputed chunk by chunk into the workspace, not stored by the
+ * forward call). Writes (overwrites)
+ *   dq, dk      : (batch, seqlen, nkheads, dstate) bf16, summed over the heads
+ *                 that share them, through the unit-length scaling
+ *   dv          : (batch, seqlen, nheads, headdim) bf16
+ *   ddt, dbeta  : (batch, seqlen, nheads) bf16, of the raw dt and beta
+ *   dA, ddt_bias: (nheads) fp32, nullable;  dh0: the state's shape, fp32, nullable
+ * bf16 io, dstate 64 or 128, headdim a multiple of 16 up to 128 (else
+ * SSM_ERR_UNSUPPORTED). dh_last nullable (zero). Tensors with a dstate or
+ * headdim axis 16-byte aligned. workspace: ssm_gated_delta_bwd_workspace_bytes
+ * (about 8 * headdim * dstate / 64 bytes per token and head), 16-byte aligned.
+ * Sums run in a fixed order. No output may overlap an input, another output
+ * or the workspace.
+ */
+size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,
+                                           int64_t nkheads, int64_t headdim, int64_t dstate,
+                                           int io_dtype);
+int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkheads,
+                        int64_t headdim, int64_t dstate, int io_dtype, const void* q,
+                        const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, int softplus, int beta_sigmoid,
+                        int qk_norm, float scale, const float* h0, const void* dy,
+                        const float* dh_last, void* dq, void* dk, void* dv, void* ddt,
+                        void* dbeta, float* dA, float* ddt_bias, float* dh0, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * ssm_gated_delta_status -- synchronise `stream`, then report whether a CTA of
+ * a chunked gated delta rule call on the current device gave up a bounded wait
+ * (2 s, or SSM_SCAN_WAIT_LIMIT_NS nanoseconds) since the last call of this
+ * function: SSM_OK, or SSM_ERR_TIMEOUT (that call's outputs are then
+ * incomplete). Cleared by this call. For testing this path,
+ * SSM_DELTA_TEST_STALL=1 makes the first CTA wait for data that never arrives.
+ */
+int ssm_gated_delta_status(void* stream);
+
+/*
+ * ssm_gated_norm_fwd -- the norm before and after a block: RMSNorm over each of
+ * `groups` equal groups of a row, with the residual sum in front of it and the
+ * SiLU gate on either side:
+ *
+ *   h = residual + residual_scale * x   (h = x without a residual)
+ *   y = RMSNorm(h * SiLU(z)) * w        (z given, norm_before_gate = 0)
+ *   y = RMSNorm(h) * w * SiLU(z)        (z given, norm_before_gate != 0)
+ *   y = RMSNorm(h) * w                  (z NULL)
+ *   RMSNorm(u) = u / sqrt(mean over the group of u^2 + eps)
+ *
+ *   x, z, y         : (rows, dim) io_dtype, z nullable
+ *   residual, h_out : (rows, dim) residual_dtype (bf16 or fp32; fp32 with fp32
+ *                     io), both or neither; h_out (h, rounded once) may be residual
+ *   w               : (dim) fp32
+ * Statistics and sums are fp32. dim a multiple of groups, at most 49152 per
+ * group. Groups of whole 16-byte units with 16-byte aligned bases take vector
+ * accesses, others one element per access. Returns SSM_OK or SSM_ERR_*.
+ */
+int ssm_gated_norm_fwd(int64_t rows, int64_t dim, int64_t groups, int io_dtype,
+                       int residual_dtype, const void* x, const void* residual,
+                       float residual_scale, const void* z, int norm_before_gate, const float* w,
+                       float eps, void* y, void* h_out, void* stream);
+
+/*
+ * ssm_gated_norm_bwd -- gradients of sum dy * y + sum dh * h for
+ * ssm_gated_norm_fwd, from h (h_out of the forward call, h_dtype; x itself,
+ * io_dtype, without a residual):
+ *   dx        : (rows, dim) io_dtype, residual_scale times the gradient of h
+ *               (pass residual_scale = 1 without a residual)
+ *   dresidual : (rows, dim) h_dtype, the gradient of h, nullable
+ *   dz        : (rows, dim) io_dtype, exactly when z is given
+ *   dw        : (dim) fp32, nullable, summed over the rows in a fixed order
+ * dy (rows, dim) io_dtype; dh (rows, dim) h_dtype, the gradient that reaches h
+ * by the residual stream, nullable. workspace: with dw, at least
+ * ssm_gated_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned.
+ * No output may overlap an input, another output or the workspace.
+ */
+size_t ssm_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups,
+                                          int io_dtype);
+int ssm_gated_norm_bwd(int64_t rows, int64_t dim, int64_t groups, int io_dtype, int h_dtype,
+                       const void* h, float residual_scale, const void* z, int norm_before_gate,
+                       const float* w, float eps, const void* dy, const void* dh, void* dx,
+                       void* dresidual, void* dz, float* dw, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
  * ssm_scan_status -- synchronise `stream`, then report whether every CTA of
  * the last ssm_scan_fwd call that used this workspace (with these sizes)
  * finished normally: SSM_OK, or SSM_ERR_TIMEOUT if a bounded wait inside a

@@ -114,6 +114,30 @@ def lib() -> ctypes.CDLL:
         L.ssm_ssd_scan_fwd.restype = ctypes.c_int
         L.ssm_ssd_scan_fwd.argtypes = [_I64] * 5 + [ctypes.c_int] + [_VP] * 7 + \
             [ctypes.c_int, _VP, _VP, _VP, _VP]
+        L.ssm_gated_delta_workspace_bytes.restype = ctypes.c_size_t
+        L.ssm_gated_delta_workspace_bytes.argtypes = [_I64] * 6 + [ctypes.c_int]
+        L.ssm_gated_delta_fwd.restype = ctypes.c_int
+        L.ssm_gated_delta_fwd.argtypes = [_I64] * 6 + [ctypes.c_int] + [_VP] * 7 + \
+            [ctypes.c_int] * 3 + [ctypes.c_float] + [_VP] * 4 + [ctypes.c_size_t, _VP]
+        L.ssm_gated_delta_update.restype = ctypes.c_int
+        L.ssm_gated_delta_update.argtypes = [_I64] * 5 + [ctypes.c_int] + [_VP] * 8 + \
+            [ctypes.c_int] * 3 + [ctypes.c_float, _VP, _VP]
+        L.ssm_gated_delta_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.ssm_gated_delta_bwd_workspace_bytes.argtypes = [_I64] * 6 + [ctypes.c_int]
+        L.ssm_gated_delta_bwd.restype = ctypes.c_int
+        L.ssm_gated_delta_bwd.argtypes = [_I64] * 6 + [ctypes.c_int] + [_VP] * 7 + \
+            [ctypes.c_int] * 3 + [ctypes.c_float] + [_VP] * 12 + [ctypes.c_size_t, _VP]
+        L.ssm_gated_delta_status.restype = ctypes.c_int
+        L.ssm_gated_delta_status.argtypes = [_VP]
+        L.ssm_gated_norm_fwd.restype = ctypes.c_int
+        L.ssm_gated_norm_fwd.argtypes = [_I64] * 3 + [ctypes.c_int] * 2 + \
+            [_VP, _VP, ctypes.c_float, _VP, ctypes.c_int, _VP, ctypes.c_float, _VP, _VP, _VP]
+        L.ssm_gated_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.ssm_gated_norm_bwd_workspace_bytes.argtypes = [_I64] * 3 + [ctypes.c_int]
+        L.ssm_gated_norm_bwd.restype = ctypes.c_int
+        L.ssm_gated_norm_bwd.argtypes = [_I64] * 3 + [ctypes.c_int] * 2 + \
+            [_VP, ctypes.c_float, _VP, ctypes.c_int, _VP, ctypes.c_float] + [_VP] * 7 + \
+            [ctypes.c_size_t, _VP]
         _lib = L
     return _lib
 
@@ -561,3 +585,224 @@ def ssm_ssd_state_update(state, x, dt, A, B, C, D=None, dt_bias=None, softplus=T
         raise SsmError(rc, "ssm_ssd_state_update", with_detail=True)
     return y
 
+
+
+def _delta_sizes(q, v, tokens):
+    """(batch, L, heads, key heads, headdim, dstate) of v (batch[, L], heads,
+    headdim) and q (batch[, L], key heads, dstate)."""
+    if q.dim() != 3 + tokens or v.dim() != 3 + tokens:
+        raise ValueError("q and v must be (batch, seqlen, heads, width)" if tokens
+                         else "q and v must be (batch, heads, width)")
+    L = v.shape[1] if tokens else 1
+    return v.shape[0], L, v.shape[-2], q.shape[-2], v.shape[-1], q.shape[-1]
+
+
+def _delta_inputs(q, k, v, dt, A, beta, dt_bias, tokens):
+    """Checked pointers of a gated delta rule call's inputs, in the C order."""
+    B, L, H, Hk, P, N = _delta_sizes(q, v, tokens)
+    dev = v.device
+    bl = (B, L) if tokens else (B,)
+    return [_ptr(q, "q", v.dtype, bl + (Hk, N), dev), _ptr(k, "k", v.dtype, bl + (Hk, N), dev),
+            _ptr(v, "v", v.dtype, bl + (H, P)), _ptr(dt, "dt", v.dtype, bl + (H,), dev),
+            _ptr(A, "A", torch.float32, (H,), dev), _ptr(beta, "beta", v.dtype, bl + (H,), dev),
+            _ptr(dt_bias, "dt_bias", torch.float32, (H,), dev)]
+
+
+def gated_delta_workspace_bytes(batch, seqlen, nheads, nkheads, headdim, dstate,
+                                dtype=torch.bfloat16) -> int:
+    return int(lib().ssm_gated_delta_workspace_bytes(batch, seqlen, nheads, nkheads, headdim,
+                                                     dstate, _io_code(dtype)))
+
+
+def gated_delta_bwd_workspace_bytes(batch, seqlen, nheads, nkheads, headdim, dstate,
+                                    dtype=torch.bfloat16) -> int:
+    return int(lib().ssm_gated_delta_bwd_workspace_bytes(batch, seqlen, nheads, nkheads, headdim,
+                                                         dstate, _io_code(dtype)))
+
+
+def ssm_gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, softplus=True, beta_sigmoid=True,
+                        qk_norm=True, scale=None, h0=None, y=None, h_last=None, workspace=None,
+                        return_last_state=True, stream=None):
+    """The gated delta rule over a sequence through ssm_gated_delta_fwd of
+    libssmscan.so: q, k (batch, L, key heads, dstate), v (batch, L, heads,
+    headdim), dt, beta (batch, L, heads), all float32 or all bfloat16; A and
+    dt_bias (heads,), h0 (batch, heads, headdim, dstate) float32. ``scale``
+    defaults to dstate ** -0.5. Returns (y, h_last); h_last is None when not
+    requested, and may be given (it may be h0)."""
+    sizes = _delta_sizes(q, v, True)
+    B, L, H, Hk, P, N = sizes
+    dev = v.device
+    io = _io_code(v.dtype)
+    ins = _delta_inputs(q, k, v, dt, A, beta, dt_bias, True)
+    ph0 = _ptr(h0, "h0", torch.float32, (B, H, P, N), dev)
+    if y is None:
+        y = torch.empty((B, L, H, P), dtype=v.dtype, device=dev)
+    py = _ptr(y, "y", v.dtype, (B, L, H, P), dev)
+    if h_last is None and return_last_state:
+        h_last = torch.empty((B, H, P, N), dtype=torch.float32, device=dev)
+    ph = _ptr(h_last, "h_last", torch.float32, (B, H, P, N), dev)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = gated_delta_workspace_bytes(*sizes, v.dtype)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        pws = _ptr(workspace, "workspace", None, None, dev)
+        rc = lib().ssm_gated_delta_fwd(*sizes, io, *ins, 1 if softplus else 0,
+                                       1 if beta_sigmoid else 0, 1 if qk_norm else 0,
+                                       N ** -0.5 if scale is None else scale, ph0, py, ph, pws,
+                                       workspace.numel() * workspace.element_size(),
+                                       _stream_ptr(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gated_delta_fwd", with_detail=True)
+    return y, h_last
+
+
+def ssm_gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, softplus=True,
+                           beta_sigmoid=True, qk_norm=True, scale=None, y=None, stream=None):
+    """One decode step of the gated delta rule through ssm_gated_delta_update
+    of libssmscan.so: updates the float32 state (batch, heads, headdim, dstate)
+    in place and returns y (batch, heads, headdim) in v's dtype; q, k (batch,
+    key heads, dstate), v (batch, heads, headdim), dt, beta (batch, heads)."""
+    B, _, H, Hk, P, N = _delta_sizes(q, v, False)
+    dev = v.device
+    ins = _delta_inputs(q, k, v, dt, A, beta, dt_bias, False)
+    ps = _ptr(state, "state", torch.float32, (B, H, P, N), dev)
+    if y is None:
+        y = torch.empty((B, H, P), dtype=v.dtype, device=dev)
+    py = _ptr(y, "y", v.dtype, (B, H, P), dev)
+    with torch.cuda.device(dev):
+        rc = lib().ssm_gated_delta_update(B, H, Hk, P, N, _io_code(v.dtype), ps, *ins,
+                                          1 if softplus else 0, 1 if beta_sigmoid else 0,
+                                          1 if qk_norm else 0,
+                                          N ** -0.5 if scale is None else scale, py,
+                                          _stream_ptr(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gated_delta_update", with_detail=True)
+    return y
+
+
+def ssm_gated_delta_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, softplus=True, beta_sigmoid=True,
+                        qk_norm=True, scale=None, h0=None, dh_last=None, workspace=None,
+                        want_dA=True, want_ddt_bias=True, want_dh0=True, stream=None):
+    """Gradients of sum(dy * y) + sum(dh_last * h_last) through
+    ssm_gated_delta_bwd of libssmscan.so (bfloat16; inputs as for
+    ssm_gated_delta_fwd, dh_last may be None). Returns a dict: dq, dk, dv, ddt,
+    dbeta in bfloat16, dA, ddt_bias (heads,) and dh0 in float32 (None when not
+    asked for)."""
+    sizes = _delta_sizes(q, v, True)
+    B, L, H, Hk, P, N = sizes
+    dev = v.device
+    f32 = torch.float32
+    io = _io_code(v.dtype)
+    ins = _delta_inputs(q, k, v, dt, A, beta, dt_bias, True)
+    ph0 = _ptr(h0, "h0", f32, (B, H, P, N), dev)
+    pdy = _ptr(dy, "dy", v.dtype, (B, L, H, P), dev)
+    pdh = _ptr(dh_last, "dh_last", f32, (B, H, P, N), dev)
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "ddt": torch.empty_like(dt), "dbeta": torch.empty_like(beta),
+         "dA": torch.empty((H,), dtype=f32, device=dev) if want_dA else None,
+         "ddt_bias": torch.empty((H,), dtype=f32, device=dev) if want_ddt_bias else None,
+         "dh0": torch.empty((B, H, P, N), dtype=f32, device=dev) if want_dh0 else None}
+    outs = [t.data_ptr() if t is not None else None for t in g.values()]
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = gated_delta_bwd_workspace_bytes(*sizes, v.dtype)
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        pws = _ptr(workspace, "workspace", None, None, dev)
+        rc = lib().ssm_gated_delta_bwd(*sizes, io, *ins, 1 if softplus else 0,
+                                       1 if beta_sigmoid else 0, 1 if qk_norm else 0,
+                                       N ** -0.5 if scale is None else scale, ph0, pdy, pdh,
+                                       *outs, pws, workspace.numel() * workspace.element_size(),
+                                       _stream_ptr(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gated_delta_bwd", with_detail=True)
+    return g
+
+
+def ssm_gated_delta_status(device=None, stream=None):
+    """Synchronise the stream and return 0, or -5 if a CTA of a chunked gated
+    delta rule call on the device gave up a bounded wait since the last call
+    (the flag is then cleared)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    with torch.cuda.device(dev):
+        return int(lib().ssm_gated_delta_status(_stream_ptr(stream, dev)))
+
+
+def gated_norm_bwd_workspace_bytes(rows, dim, groups=1, dtype=torch.bfloat16) -> int:
+    return int(lib().ssm_gated_norm_bwd_workspace_bytes(rows, dim, groups, _io_code(dtype)))
+
+
+def _norm_rows(x):
+    dim = x.shape[-1]
+    return (x.numel() // dim if dim else 0), dim
+
+
+def ssm_gated_norm_fwd(x, w, z=None, norm_before_gate=False, residual=None, residual_scale=1.0,
+                       groups=1, eps=1e-5, y=None, h=None, stream=None):
+    """The norm before and after a block through ssm_gated_norm_fwd of
+    libssmscan.so: RMSNorm over groups of the last axis of x (..., dim), fp32
+    weights w (dim,), the SiLU gate z (x's shape and type) before the norm or
+    after it (``norm_before_gate``), and residual + residual_scale * x in front
+    of it (residual of x's shape, x's type or float32). Returns (y, h): h is
+    the sum (``h`` may be given, and may be residual), or x without a residual."""
+    if x.dim() < 1:
+        raise ValueError("x must be (..., dim)")
+    rows, dim = _norm_rows(x)
+    dev, shape = x.device, tuple(x.shape)
+    px = _ptr(x, "x", x.dtype, shape)
+    pz = _ptr(z, "z", x.dtype, shape, dev)
+    pw = _ptr(w, "w", torch.float32, (dim,), dev)
+    pres = _ptr(residual, "residual", None, shape, dev)
+    rio = _io_code(residual.dtype if residual is not None else x.dtype)
+    if y is None:
+        y = torch.empty_like(x)
+    py = _ptr(y, "y", x.dtype, shape, dev)
+    if residual is None and h is not None:
+        raise ValueError("h is an output only with a residual")
+    if residual is not None and h is None:
+        h = torch.empty_like(residual)
+    ph = _ptr(h, "h", residual.dtype if residual is not None else None, shape, dev)
+    with torch.cuda.device(dev):
+        rc = lib().ssm_gated_norm_fwd(rows, dim, groups, _io_code(x.dtype), rio, px, pres,
+                                      residual_scale, pz, 1 if norm_before_gate else 0, pw, eps,
+                                      py, ph, _stream_ptr(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gated_norm_fwd", with_detail=True)
+    return y, (x if residual is None else h)
+
+
+def ssm_gated_norm_bwd(h, w, dy, z=None, norm_before_gate=False, dh=None, residual=False,
+                       residual_scale=1.0, groups=1, eps=1e-5, workspace=None, want_dw=True,
+                       stream=None):
+    """Gradients of sum(dy * y) + sum(dh * h) through ssm_gated_norm_bwd of
+    libssmscan.so, from the h that ssm_gated_norm_fwd returned (x itself without
+    a residual). ``residual``: whether there was one (dresidual is returned,
+    and dx is residual_scale times it). Returns a dict: dx, dz (dy's type),
+    dresidual (h's type), dw (dim,) float32; what does not apply is None."""
+    if h.dim() < 1:
+        raise ValueError("h must be (..., dim)")
+    if not residual and (h.dtype != dy.dtype or residual_scale != 1.0):
+        raise ValueError("without a residual h has dy's type and residual_scale is 1")
+    rows, dim = _norm_rows(h)
+    dev, shape = h.device, tuple(h.shape)
+    ph = _ptr(h, "h", None, shape)
+    pw = _ptr(w, "w", torch.float32, (dim,), dev)
+    pdy = _ptr(dy, "dy", None, shape, dev)
+    pz = _ptr(z, "z", dy.dtype, shape, dev)
+    pdh = _ptr(dh, "dh", h.dtype, shape, dev)
+    g = {"dx": torch.empty_like(dy), "dz": torch.empty_like(dy) if z is not None else None,
+         "dresidual": torch.empty_like(h) if residual else None,
+         "dw": torch.empty((dim,), dtype=torch.float32, device=dev) if want_dw else None}
+    P = {k: (v.data_ptr() if v is not None else None) for k, v in g.items()}
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = gated_norm_bwd_workspace_bytes(rows, dim, groups, dy.dtype) if want_dw else 0
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        pws = _ptr(workspace, "workspace", None, None, dev)
+        rc = lib().ssm_gated_norm_bwd(rows, dim, groups, _io_code(dy.dtype), _io_code(h.dtype), ph,
+                                      residual_scale, pz, 1 if norm_before_gate else 0, pw, eps,
+                                      pdy, pdh, P["dx"], P["dresidual"], P["dz"], P["dw"], pws,
+                                      workspace.numel() * workspace.element_size(),
+                                      _stream_ptr(stream, dev))
+    if rc != 0:
+        raise SsmError(rc, "ssm_gated_norm_bwd", with_detail=True)
+    return g

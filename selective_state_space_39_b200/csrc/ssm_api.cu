@@ -12,6 +12,8 @@
 #include "../../include/ssm_scan.h"
 #include "ssm_bwd_internal.h"
 #include "ssm_conv_internal.h"
+#include "ssm_delta_internal.h"
+#include "ssm_norm_internal.h"
 #include "ssm_seqpar_internal.h"
 #include "ssm_ssd_decode_internal.h"
 #include "ssm_ssd_internal.h"
@@ -913,6 +915,437 @@ int ssm_compose_carries(int64_t rank, int64_t batch, int64_t dim, int64_t dstate
   p.dsum_all = dsum_all;
   p.h_in = h_in;
   return cuda_status(launch_compose(p, static_cast<cudaStream_t>(stream)), "compose launch");
+}
+
+// ---- gated delta rule ---------------------------------------------------------
+
+// The sizes of a call; `chunked`: whether the chunk kernels hold it (bf16 io and
+// the sizes of delta_chunk_supported).
+struct DeltaDims {
+  int64_t batch, seqlen, nheads, nkheads, headdim, dstate;
+  int io;
+};
+
+// Tokens from which the chunk kernels are taken; shorter sequences go token by
+// token, without a workspace.
+constexpr int64_t kDeltaMinChunked = 32;
+
+static int delta_dims_status(const DeltaDims& d) {
+  if (d.io != SSM_DTYPE_F32 && d.io != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
+  if (d.batch < 0 || d.seqlen < 0 || d.nheads < 0 || d.nkheads < 0 || d.headdim < 0 ||
+      d.dstate <= 0)
+    return SSM_ERR_INVALID_ARG;
+  if (!delta_step_dstate_supported((int)std::min<int64_t>(d.dstate, 1 << 20)))
+    return fail(SSM_ERR_UNSUPPORTED, "gated delta rule: dstate 32, 64, 128 or 256 only");
+  if (d.batch > 65535 || d.nheads > 32768 || d.headdim > (1 << 16) || d.seqlen > (1 << 30))
+    return SSM_ERR_UNSUPPORTED;
+  if (too_large({d.batch, d.seqlen, d.nheads, d.headdim}) ||
+      too_large({d.batch, d.seqlen, d.nkheads, d.dstate}) ||
+      too_large({d.batch, d.nheads, d.headdim, d.dstate, 16}))  // at most 2^31 state rows
+    return SSM_ERR_UNSUPPORTED;
+  if (d.nheads > 0 && (d.nkheads == 0 || d.nheads % d.nkheads != 0))
+    return fail(SSM_ERR_INVALID_ARG, "gated delta rule: nheads must be a multiple of nkheads");
+  return SSM_OK;
+}
+
+static bool delta_chunked(const DeltaDims& d) {
+  return d.io == SSM_DTYPE_BF16 && d.seqlen >= kDeltaMinChunked &&
+         delta_chunk_supported((int)d.dstate, (int)d.headdim);
+}
+
+struct DeltaWs {
+  size_t kq, head, state, dstate, r, doto, dotv, dotu, part, bytes;
+};
+static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
+  DeltaWs w{};
+  const size_t nc = (size_t)((d.seqlen + kDeltaChunk - 1) / kDeltaChunk);
+  const size_t bc = (size_t)d.batch * nc, state = (size_t)d.nheads * d.headdim * d.dstate * 4;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  w.kq = take(bc * d.nkheads * 2 * kDeltaChunk * d.dstate * 2);
+  w.head = take(bc * d.nheads * (bwd ? kDeltaHeadBwd : kDeltaHeadFwd));
+  if (bwd) {
+    const size_t dots = bc * d.nheads * (d.headdim / 16) * kDeltaChunk * 4;
+    w.state = take((size_t)d.batch * (nc + 1) * state);
+    w.dstate = take(bc * state);
+    w.r = take((size_t)d.batch * d.seqlen * d.nheads * d.headdim * 2);
+    w.doto = take(dots);
+    w.dotv = take(dots);
+    w.dotu = take(dots);
+    w.part = take(bc * d.nheads * 2 * 4);
+  }
+  w.bytes = off;
+  return w;
+}
+
+static DeltaParams delta_params(const DeltaDims& d, const void* q, const void* k, const void* v,
+                                const void* dt, const float* A, const void* beta,
+                                const float* dt_bias, int softplus, int beta_sigmoid,
+                                int qk_norm, float scale) {
+  DeltaParams p{};
+  p.batch = (int)d.batch;
+  p.nheads = (int)d.nheads;
+  p.nkheads = (int)d.nkheads;
+  p.headdim = (int)d.headdim;
+  p.dstate = (int)d.dstate;
+  p.seqlen = d.seqlen;
+  p.softplus = softplus ? 1 : 0;
+  p.beta_sigmoid = beta_sigmoid ? 1 : 0;
+  p.qk_norm = qk_norm ? 1 : 0;
+  p.scale = scale;
+  p.q = q; p.k = k; p.v = v; p.dt = dt; p.beta = beta;
+  p.A = A; p.dt_bias = dt_bias;
+  return p;
+}
+
+static DeltaChunkParams delta_chunk_params(const DeltaParams& dp, const DeltaDims& d, bool bwd,
+                                           void* workspace) {
+  DeltaChunkParams p{};
+  const DeltaWs w = delta_ws(d, bwd);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.d = dp;
+  p.nchunks = (int)((d.seqlen + kDeltaChunk - 1) / kDeltaChunk);
+  p.head_bytes = bwd ? kDeltaHeadBwd : kDeltaHeadFwd;
+  p.ws_kq = ws + w.kq;
+  p.ws_head = ws + w.head;
+  p.wait_limit_ns = (uint64_t)std::max(1L, env_long("SSM_SCAN_WAIT_LIMIT_NS",
+                                                    (long)kDefaultWaitLimitNs));
+  p.test_stall = env_long("SSM_DELTA_TEST_STALL", 0) != 0 ? 1 : 0;
+  if (bwd) {
+    p.ws_state = reinterpret_cast<float*>(ws + w.state);
+    p.ws_dstate = reinterpret_cast<float*>(ws + w.dstate);
+    p.ws_r = reinterpret_cast<uint16_t*>(ws + w.r);
+    p.ws_doto = reinterpret_cast<float*>(ws + w.doto);
+    p.ws_dotv = reinterpret_cast<float*>(ws + w.dotv);
+    p.ws_dotu = reinterpret_cast<float*>(ws + w.dotu);
+    p.ws_part = reinterpret_cast<float*>(ws + w.part);
+  }
+  return p;
+}
+
+struct Buf {
+  const void* p;
+  size_t n;
+};
+// Whether one of the outputs overlaps an input or another output.
+static bool any_overlap(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+  for (const Buf* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Buf& i : ins)
+      if (overlap(o->p, o->n, i.p, i.n)) return true;
+    for (const Buf* q = outs.begin(); q != o; ++q)
+      if (overlap(o->p, o->n, q->p, q->n)) return true;
+  }
+  return false;
+}
+
+size_t ssm_gated_delta_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,
+                                       int64_t nkheads, int64_t headdim, int64_t dstate,
+                                       int io_dtype) {
+  const DeltaDims d{batch, seqlen, nheads, nkheads, headdim, dstate, io_dtype};
+  if (delta_dims_status(d) != SSM_OK || !delta_chunked(d)) return 0;
+  return delta_ws(d, false).bytes;
+}
+
+int ssm_gated_delta_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkheads,
+                        int64_t headdim, int64_t dstate, int io_dtype, const void* q,
+                        const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, int softplus, int beta_sigmoid,
+                        int qk_norm, float scale, const float* h0, void* y, float* h_last,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  const DeltaDims d{batch, seqlen, nheads, nkheads, headdim, dstate, io_dtype};
+  const int st = delta_dims_status(d);
+  if (st != SSM_OK) return st;
+  if (batch == 0 || nheads == 0 || headdim == 0) return SSM_OK;
+  if (seqlen > 0 && (!q || !k || !v || !dt || !A || !beta || (!y && !h_last)))
+    return SSM_ERR_INVALID_ARG;
+  const size_t es = io_bytes(io_dtype);
+  if ((q && !aligned(q, 4 * es)) || (k && !aligned(k, 4 * es)) || (v && !aligned(v, es)) ||
+      (dt && !aligned(dt, es)) || (beta && !aligned(beta, es)) || (y && !aligned(y, es)) ||
+      !aligned(A, 4) || (dt_bias && !aligned(dt_bias, 4)) || (h0 && !aligned(h0, 16)) ||
+      (h_last && !aligned(h_last, 16)))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_fwd: misaligned pointer");
+  const size_t nqk = (size_t)batch * seqlen * nkheads * dstate * es;
+  const size_t nv = (size_t)batch * seqlen * nheads * headdim * es;
+  const size_t ng = (size_t)batch * seqlen * nheads * es, nh = (size_t)nheads * 4;
+  const size_t ns = (size_t)batch * nheads * headdim * dstate * 4;
+  if (any_overlap({{y, nv}, {h_last, ns}}, {{q, nqk}, {k, nqk}, {v, nv}, {dt, ng}, {beta, ng},
+                                            {A, nh}, {dt_bias, nh}}) ||
+      overlap(y, nv, h0, ns) || (h_last != h0 && overlap(h_last, ns, h0, ns)))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_fwd: an output overlaps an input");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (seqlen == 0) {
+    if (!h_last || h_last == h0) return SSM_OK;
+    return cuda_status(h0 ? cudaMemcpyAsync(h_last, h0, ns, cudaMemcpyDeviceToDevice, s)
+                          : cudaMemsetAsync(h_last, 0, ns, s),
+                       "ssm_gated_delta_fwd: empty sequence");
+  }
+  DeltaParams p = delta_params(d, q, k, v, dt, A, beta, dt_bias, softplus, beta_sigmoid, qk_norm,
+                               scale);
+  p.h0 = h0;
+  p.y = y;
+  p.h_last = h_last;
+  if (delta_chunked(d)) {
+    const size_t need = delta_ws(d, false).bytes;
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+      return fail(SSM_ERR_WORKSPACE,
+                  "ssm_gated_delta_fwd: workspace missing, too small or unaligned");
+    if (any_overlap({{workspace, need}}, {{q, nqk}, {k, nqk}, {v, nv}, {dt, ng}, {beta, ng},
+                                          {A, nh}, {dt_bias, nh}, {h0, ns}, {y, nv}, {h_last, ns}}))
+      return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_fwd: the workspace overlaps a tensor");
+    // the chunk kernels copy whole 16-byte units; other bases go token by token
+    if (aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && (!y || aligned(y, 16))) {
+      const DeltaChunkParams cp = delta_chunk_params(p, d, false, workspace);
+      cudaError_t e = launch_delta_prep(cp, false, s);
+      if (e == cudaSuccess) e = launch_delta_chunk_fwd(cp, false, s);
+      return cuda_status(e, "gated delta rule launch (chunks)");
+    }
+  }
+  return cuda_status(launch_delta_step(p, io_dtype == SSM_DTYPE_BF16, s),
+                     "gated delta rule launch");
+}
+
+int ssm_gated_delta_update(int64_t batch, int64_t nheads, int64_t nkheads, int64_t headdim,
+                           int64_t dstate, int io_dtype, float* state, const void* q,
+                           const void* k, const void* v, const void* dt, const float* A,
+                           const void* beta, const float* dt_bias, int softplus,
+                           int beta_sigmoid, int qk_norm, float scale, void* y, void* stream) {
+  const DeltaDims d{batch, 1, nheads, nkheads, headdim, dstate, io_dtype};
+  const int st = delta_dims_status(d);
+  if (st != SSM_OK) return st;
+  if (batch == 0 || nheads == 0 || headdim == 0) return SSM_OK;
+  if (!state || !y) return SSM_ERR_INVALID_ARG;
+  return ssm_gated_delta_fwd(batch, 1, nheads, nkheads, headdim, dstate, io_dtype, q, k, v, dt, A,
+                             beta, dt_bias, softplus, beta_sigmoid, qk_norm, scale, state, y,
+                             state, nullptr, 0, stream);
+}
+
+int ssm_gated_delta_status(void* stream) {
+  int v = 0;
+  const cudaError_t e = delta_chunk_status(static_cast<cudaStream_t>(stream), &v);
+  if (e != cudaSuccess) return fail(SSM_ERR_CUDA, "ssm_gated_delta_status", e);
+  return v ? fail(SSM_ERR_TIMEOUT, "a CTA of the gated delta rule gave up a bounded wait")
+           : SSM_OK;
+}
+
+static int delta_bwd_status(const DeltaDims& d) {
+  const int st = delta_dims_status(d);
+  if (st != SSM_OK) return st;
+  if (d.io != SSM_DTYPE_BF16 || (d.dstate != 64 && d.dstate != 128) || d.headdim % 16 != 0 ||
+      d.headdim > 128)
+    return fail(SSM_ERR_UNSUPPORTED, "ssm_gated_delta_bwd: bf16 io, dstate 64 or 128 and "
+                                     "headdim a multiple of 16 up to 128 only");
+  return SSM_OK;
+}
+
+size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,
+                                           int64_t nkheads, int64_t headdim, int64_t dstate,
+                                           int io_dtype) {
+  const DeltaDims d{batch, seqlen, nheads, nkheads, headdim, dstate, io_dtype};
+  if (delta_bwd_status(d) != SSM_OK) return 0;
+  return delta_ws(d, true).bytes;
+}
+
+int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t nkheads,
+                        int64_t headdim, int64_t dstate, int io_dtype, const void* q,
+                        const void* k, const void* v, const void* dt, const float* A,
+                        const void* beta, const float* dt_bias, int softplus, int beta_sigmoid,
+                        int qk_norm, float scale, const float* h0, const void* dy,
+                        const float* dh_last, void* dq, void* dk, void* dv, void* ddt,
+                        void* dbeta, float* dA, float* ddt_bias, float* dh0, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const DeltaDims d{batch, seqlen, nheads, nkheads, headdim, dstate, io_dtype};
+  const int st = delta_bwd_status(d);
+  if (st != SSM_OK) return st;
+  if (nheads == 0) return SSM_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t es = 2, nh = (size_t)nheads * 4;
+  if ((dA && !aligned(dA, 4)) || (ddt_bias && !aligned(ddt_bias, 4)))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_bwd: misaligned pointer");
+  const size_t nqk = (size_t)batch * seqlen * nkheads * dstate * es;
+  const size_t nv = (size_t)batch * seqlen * nheads * headdim * es;
+  const size_t ng = (size_t)batch * seqlen * nheads * es;
+  const size_t ns = (size_t)batch * nheads * headdim * dstate * 4;
+  const bool none = batch == 0 || seqlen == 0 || headdim == 0;
+  if (!none && (!q || !k || !v || !dt || !A || !beta || !dy || !dq || !dk || !dv || !ddt || !dbeta))
+    return SSM_ERR_INVALID_ARG;
+  const void* rows[] = {q, k, v, dy, dq, dk, dv, h0, dh_last, dh0};
+  const void* gates[] = {dt, beta, ddt, dbeta};
+  for (const void* x : rows)
+    if (x && !aligned(x, 16))
+      return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_bwd: misaligned pointer");
+  for (const void* x : gates)
+    if (x && !aligned(x, es))
+      return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_bwd: misaligned pointer");
+  if (!aligned(A, 4) || (dt_bias && !aligned(dt_bias, 4)))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_bwd: misaligned pointer");
+  if (any_overlap({{dq, nqk}, {dk, nqk}, {dv, nv}, {ddt, ng}, {dbeta, ng}, {dA, nh},
+                   {ddt_bias, nh}, {dh0, ns}},
+                  {{q, nqk}, {k, nqk}, {v, nv}, {dt, ng}, {beta, ng}, {A, nh}, {dt_bias, nh},
+                   {h0, ns}, {dy, nv}, {dh_last, ns}}))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_bwd: an output overlaps an input or another");
+  if (none) {  // no token: the state's gradient passes through, the others are zero
+    cudaError_t e = dA ? cudaMemsetAsync(dA, 0, nh, s) : cudaSuccess;
+    if (e == cudaSuccess && ddt_bias) e = cudaMemsetAsync(ddt_bias, 0, nh, s);
+    if (e == cudaSuccess && dh0 && ns)
+      e = dh_last ? cudaMemcpyAsync(dh0, dh_last, ns, cudaMemcpyDeviceToDevice, s)
+                  : cudaMemsetAsync(dh0, 0, ns, s);
+    return cuda_status(e, "ssm_gated_delta_bwd: empty sequence");
+  }
+  const size_t need = delta_ws(d, true).bytes;
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(SSM_ERR_WORKSPACE, "ssm_gated_delta_bwd: workspace missing, too small or unaligned");
+  if (any_overlap({{workspace, need}},
+                  {{q, nqk}, {k, nqk}, {v, nv}, {dt, ng}, {beta, ng}, {A, nh}, {dt_bias, nh},
+                   {h0, ns}, {dy, nv}, {dh_last, ns}, {dq, nqk}, {dk, nqk}, {dv, nv}, {ddt, ng},
+                   {dbeta, ng}, {dA, nh}, {ddt_bias, nh}, {dh0, ns}}))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_bwd: the workspace overlaps a tensor");
+  DeltaParams p = delta_params(d, q, k, v, dt, A, beta, dt_bias, softplus, beta_sigmoid, qk_norm,
+                               scale);
+  p.h0 = h0;
+  DeltaChunkParams cp = delta_chunk_params(p, d, true, workspace);
+  cp.dy = static_cast<const uint16_t*>(dy);
+  cp.dh_last = dh_last;
+  cp.dq = static_cast<uint16_t*>(dq);
+  cp.dk = static_cast<uint16_t*>(dk);
+  cp.dv = static_cast<uint16_t*>(dv);
+  cp.ddt = static_cast<uint16_t*>(ddt);
+  cp.dbeta = static_cast<uint16_t*>(dbeta);
+  cp.dA = dA;
+  cp.ddt_bias = ddt_bias;
+  cp.dh0 = dh0;
+  cudaError_t e = launch_delta_prep(cp, true, s);
+  if (e == cudaSuccess) e = launch_delta_chunk_fwd(cp, true, s);
+  if (e == cudaSuccess) e = launch_delta_chunk_rev(cp, s);
+  if (e == cudaSuccess) e = launch_delta_grad(cp, s);
+  return cuda_status(e, "gated delta rule backward launch");
+}
+
+// ---- norm before and after a block ------------------------------------------
+
+static int norm_types(int io, int h) {
+  if (io == SSM_DTYPE_F32) return h == SSM_DTYPE_F32 ? 2 : -1;
+  return h == SSM_DTYPE_F32 ? 1 : 0;
+}
+
+static int norm_status(int64_t rows, int64_t dim, int64_t groups, int io, int h) {
+  if ((io != SSM_DTYPE_F32 && io != SSM_DTYPE_BF16) || (h != SSM_DTYPE_F32 && h != SSM_DTYPE_BF16))
+    return SSM_ERR_UNSUPPORTED;
+  if (rows < 0 || dim < 0 || groups <= 0) return SSM_ERR_INVALID_ARG;
+  if (norm_types(io, h) < 0)
+    return fail(SSM_ERR_UNSUPPORTED, "gated norm: fp32 io needs an fp32 residual");
+  if (dim % groups != 0)
+    return fail(SSM_ERR_INVALID_ARG, "gated norm: dim must be a multiple of groups");
+  if (groups > 65535 || dim > (1 << 24) || dim / groups > 49152 ||
+      (double)rows * (double)groups > 2147483647.0 || too_large({rows, dim}))
+    return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+static NormParams norm_params(int64_t rows, int64_t dim, int64_t groups, const void* z,
+                              int norm_before_gate, const float* w, float eps, float scale) {
+  NormParams p{};
+  p.rows = rows;
+  p.dim = (int)dim;
+  p.groups = (int)groups;
+  p.width = (int)(dim / groups);
+  p.gate = !z ? kGateNone : norm_before_gate ? kGateLast : kGateFirst;
+  p.eps = eps;
+  p.residual_scale = scale;
+  p.z = z;
+  p.w = w;
+  return p;
+}
+
+// 16-byte accesses: row groups of whole units and aligned bases.
+static bool norm_vec(int64_t width, int io, std::initializer_list<const void*> ptrs) {
+  if (width % (io == SSM_DTYPE_BF16 ? 8 : 4) != 0) return false;
+  for (const void* q : ptrs)
+    if (q && !aligned(q, 16)) return false;
+  return true;
+}
+
+int ssm_gated_norm_fwd(int64_t rows, int64_t dim, int64_t groups, int io_dtype,
+                       int residual_dtype, const void* x, const void* residual,
+                       float residual_scale, const void* z, int norm_before_gate, const float* w,
+                       float eps, void* y, void* h_out, void* stream) {
+  const int hd = residual ? residual_dtype : io_dtype;
+  const int st = norm_status(rows, dim, groups, io_dtype, hd);
+  if (st != SSM_OK) return st;
+  if (rows == 0 || dim == 0) return SSM_OK;
+  if (!x || !w || !y || (residual && !h_out) || (!residual && h_out)) return SSM_ERR_INVALID_ARG;
+  const size_t es = io_bytes(io_dtype), hs = io_bytes(hd), n = (size_t)rows * dim;
+  if (!aligned(x, es) || !aligned(y, es) || (z && !aligned(z, es)) || !aligned(w, 4) ||
+      (residual && !aligned(residual, hs)) || (h_out && !aligned(h_out, hs)))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_norm_fwd: misaligned pointer");
+  const size_t nw = (size_t)dim * 4;
+  if (any_overlap({{y, n * es}, {h_out, n * hs}}, {{x, n * es}, {z, n * es}, {w, nw}}) ||
+      overlap(y, n * es, residual, n * hs) ||
+      (h_out != residual && overlap(h_out, n * hs, residual, n * hs)))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_norm_fwd: an output overlaps an input");
+  NormParams p = norm_params(rows, dim, groups, z, norm_before_gate, w, eps, residual_scale);
+  p.x = x;
+  p.residual = residual;
+  p.y = y;
+  p.h_out = h_out;
+  return cuda_status(launch_norm_fwd(p, norm_types(io_dtype, hd),
+                                     norm_vec(dim / groups, io_dtype, {x, residual, z, w, y, h_out}),
+                                     static_cast<cudaStream_t>(stream)),
+                     "gated norm launch");
+}
+
+size_t ssm_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups,
+                                          int io_dtype) {
+  if (norm_status(rows, dim, groups, io_dtype, SSM_DTYPE_F32) != SSM_OK || rows == 0) return 0;
+  return sizeof(float) * (size_t)norm_bwd_slices(rows, (int)dim, (int)groups) * dim;
+}
+
+int ssm_gated_norm_bwd(int64_t rows, int64_t dim, int64_t groups, int io_dtype, int h_dtype,
+                       const void* h, float residual_scale, const void* z, int norm_before_gate,
+                       const float* w, float eps, const void* dy, const void* dh, void* dx,
+                       void* dresidual, void* dz, float* dw, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const int st = norm_status(rows, dim, groups, io_dtype, h_dtype);
+  if (st != SSM_OK) return st;
+  if (dim == 0) return SSM_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t nw = (size_t)dim * 4;
+  if (dw && !aligned(dw, 4))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_norm_bwd: misaligned pointer");
+  if (rows == 0)
+    return dw ? cuda_status(cudaMemsetAsync(dw, 0, nw, s), "ssm_gated_norm_bwd: no rows") : SSM_OK;
+  if (!h || !w || !dy || !dx || (z && !dz) || (!z && dz)) return SSM_ERR_INVALID_ARG;
+  const size_t es = io_bytes(io_dtype), hs = io_bytes(h_dtype), n = (size_t)rows * dim;
+  if (!aligned(h, hs) || !aligned(dy, es) || (z && !aligned(z, es)) || !aligned(w, 4) ||
+      !aligned(dx, es) || (dz && !aligned(dz, es)) || (dh && !aligned(dh, hs)) ||
+      (dresidual && !aligned(dresidual, hs)))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_norm_bwd: misaligned pointer");
+  if (any_overlap({{dx, n * es}, {dresidual, n * hs}, {dz, n * es}, {dw, nw}},
+                  {{h, n * hs}, {z, n * es}, {w, nw}, {dy, n * es}, {dh, n * hs}}))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_norm_bwd: an output overlaps an input or another");
+  const size_t need = ssm_gated_norm_bwd_workspace_bytes(rows, dim, groups, io_dtype);
+  if (dw && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(SSM_ERR_WORKSPACE, "ssm_gated_norm_bwd: workspace missing, too small or unaligned");
+  if (dw && any_overlap({{workspace, need}},
+                        {{dx, n * es}, {dresidual, n * hs}, {dz, n * es}, {dw, nw}, {h, n * hs},
+                         {z, n * es}, {w, nw}, {dy, n * es}, {dh, n * hs}}))
+    return fail(SSM_ERR_INVALID_ARG, "ssm_gated_norm_bwd: the workspace overlaps a tensor");
+  NormParams p = norm_params(rows, dim, groups, z, norm_before_gate, w, eps, residual_scale);
+  p.h = h;
+  p.dy = dy;
+  p.dh = dh;
+  p.dx = dx;
+  p.dresidual = dresidual;
+  p.dz = dz;
+  p.dw = dw;
+  p.ws = static_cast<float*>(workspace);
+  return cuda_status(
+      launch_norm_bwd(p, norm_types(io_dtype, h_dtype),
+                      norm_vec(dim / groups, io_dtype, {h, z, w, dy, dh, dx, dresidual, dz}), s),
+      "gated norm backward launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,122 @@
+// ssm_delta.cuh -- device helpers of the gated delta rule: the gates, warp
+// MMAs and their fragment loads, and the two-piece fp16 form of fp32 operands.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "ssm_delta_internal.h"
+#include "ssm_device.cuh"
+
+namespace ssm {
+
+// Delta of one token: softplus with the library's cut, in fp32 functions whose
+// error is a few units in the last place (one call per token and head).
+__device__ __forceinline__ float delta_step_size(float raw, int softplus) {
+  return (softplus && raw <= kSoftplusCut) ? log1pf(expf(raw)) : raw;
+}
+__device__ __forceinline__ float delta_beta(float raw, int sigmoid) {
+  return sigmoid ? 1.f / (1.f + expf(-raw)) : raw;
+}
+
+// ------------------------------------------------------ fragments and MMAs --
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte unit `c` of row `row` in a tile with RB-byte rows: the
+// unit's low three bits are xored with the row's, so that the eight rows of an
+// ldmatrix at one column lie in eight different bank groups.
+template <int RB>
+__device__ __forceinline__ uint32_t swz(int row, int c) {
+  return (uint32_t)(row * RB + ((c ^ (row & 7)) << 4));
+}
+
+// ------------------------------------- fp32 operands as two pieces of fp16 --
+// x s = hi + lo with hi, lo fp16 and s a power of two that brings the largest
+// magnitude of the row to [2^14, 2^15): the two pieces carry 22 bits of every
+// element within 2^16 of the largest, and smaller ones to 2^-40 of the
+// largest, so products keep fp32's accuracy at two MMAs (three where both
+// operands have two pieces; the dropped lo lo is 2^-24 of the product).
+// bf16 operands (k, q) are one exact fp16 piece under a row scale of their own.
+struct RowScale {
+  float s, inv;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t e) {  // e: biased exponent of the maximum
+  e = e < 15u ? 15u : e;
+  RowScale r;
+  r.s = __uint_as_float((268u - e) << 23);
+  r.inv = __uint_as_float((e - 14u) << 23);
+  return r;
+}
+__device__ __forceinline__ uint32_t exponent_of(float m) { return __float_as_uint(m) >> 23; }
+// Largest magnitude of fragment rows g (m0) and g + 8 (m1), over the quad.
+template <int T>
+__device__ __forceinline__ void row_max(const float (&x)[T][4], float& m0, float& m1) {
+  m0 = m1 = 0.f;
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    m0 = fmaxf(m0, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
+    m1 = fmaxf(m1, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, uint32_t& lo) {
+  x *= s;
+  y *= s;
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = h2_bits(h);
+  lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
+}
+// A fragments (16 rows x 16 of k) of accumulator tiles c0 (k 0..7) and c1 (k 8..15).
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], float s0,
+                                        float s1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split2(c0[0], c0[1], s0, hi[0], lo[0]);
+  split2(c0[2], c0[3], s1, hi[1], lo[1]);
+  split2(c1[0], c1[1], s0, hi[2], lo[2]);
+  split2(c1[2], c1[3], s1, hi[3], lo[3]);
+}
+__device__ __forceinline__ void half_a(const float (&c0)[4], const float (&c1)[4], float s0,
+                                       float s1, uint32_t (&hi)[4]) {
+  hi[0] = h2_bits(__floats2half2_rn(c0[0] * s0, c0[1] * s0));
+  hi[1] = h2_bits(__floats2half2_rn(c0[2] * s1, c0[3] * s1));
+  hi[2] = h2_bits(__floats2half2_rn(c1[0] * s0, c1[1] * s0));
+  hi[3] = h2_bits(__floats2half2_rn(c1[2] * s1, c1[3] * s1));
+}
+
+}  // namespace ssm

@@ -1,0 +1,442 @@
+// ssm_delta_grad.cu -- gradients of the gated delta rule that need no further
+// walk over the sequence (bf16 io, sm_100a): dq, dk, dbeta, ddt, dA, ddt_bias
+// from each chunk's entering state S, the adjoint dS of its leaving state, and
+// the residuals r, dR = dv of the two passes over the chunks.
+//
+// With W_ij = (dy_i . u_j) e^(G_i - G_j) (j <= i) and
+// N_ij = -(dv_i . u_j) e^(G_i - G_j) (j < i):
+//   dq_i = e^(G_i) S dy_i + sum_j W_ij k_j
+//   dk_j = e^(G_end - G_j) dS u_j - e^(G_j) S dv_j + sum_i W_ij q_i + sum_i (N + N^T)_ji k_i
+//   dbeta_j = du_j . r_j - sum_(i>j) (k_i . k_j) e^(G_i - G_j) (dv_i . r_j)
+// and, since a decay scales every later use of the state, the log decays'
+// gradients need no matrix at all:
+//   dg_t = sum_(i >= t in the chunk) (dy_i . y_i - dv_i . v_i) + <S_end, dS_end>
+// whose row products the two passes took in fp32. One CTA per chunk and key
+// head adds its value heads in order, so dq and dk are written once, through
+// x / |x| when q and k were scaled to unit length. Operands are bf16 (q, k, dy
+// exactly; S, dS, r, dv and the weights rounded once), sums fp32: the outputs
+// are bf16 themselves.
+//
+// Bound: the states' traffic (S, dS and the next S in fp32, 192 KB per chunk
+// and head of 128 x 128) beside about 5 M bf16 MACs per chunk and head.
+#include "ssm_delta.cuh"
+
+namespace ssm {
+
+namespace {
+
+constexpr int kC = kDeltaChunk;
+constexpr int kThreads = 256;
+constexpr int kWs = kC * 2 + 16;  // row stride (bytes) of the 64 x 64 tiles
+
+struct GradLayout {
+  int xs, ps;  // row strides (bytes) of the dstate-wide and headdim-wide tiles
+  int k, q, s, ds, dy, r, dr, w1, w2, ns, f, bytes;
+};
+enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfDelta, kfSig, kfCol, kfRow = kfCol + 4, kfRed = kfRow + 4, kfCount = kfRed + 1 };
+
+__host__ __device__ inline GradLayout grad_layout(int N, int P) {
+  GradLayout g;
+  g.xs = N * 2 + 16;
+  g.ps = P * 2 + 16;
+  int at = 0;
+  g.k = at; at += kC * g.xs;
+  g.q = at; at += kC * g.xs;
+  g.s = at; at += P * g.xs;
+  g.ds = at; at += P * g.xs;
+  g.dy = at; at += kC * g.ps;
+  g.r = at; at += kC * g.ps;
+  g.dr = at; at += kC * g.ps;
+  g.w1 = at; at += kC * kWs;
+  g.w2 = at; at += kC * kWs;
+  g.ns = at; at += kC * kWs;
+  g.f = at; at += kfCount * kC * 4;
+  g.bytes = at;
+  return g;
+}
+
+__device__ __forceinline__ void st16(unsigned char* p, float v) {
+  *reinterpret_cast<uint16_t*>(p) = f32_to_bf16(v);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaChunkParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int T = N / 16;  // n-tiles of a warp's half of dstate
+  const DeltaParams& d = p.d;
+  const int P = d.headdim;
+  const GradLayout g = grad_layout(N, P);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int mi = warp & 3, half = warp >> 2;
+  const int c = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
+  const int rep = d.nheads / d.nkheads;
+  const int64_t t0 = (int64_t)c * kC;
+  const int valid = (int)min((int64_t)kC, d.seqlen - t0);
+  const size_t bc = (size_t)b * p.nchunks + c;
+  const size_t row0 = (size_t)b * d.seqlen + t0;
+  float* F = reinterpret_cast<float*>(smem + g.f);
+  const uint32_t sm = smem_u32(smem);
+  // fragment addressing: A rows (m) with k contiguous; B rows n (nt); rows k (tr)
+  const int a_row = lane & 15, a_u = lane >> 4;
+  const int nt_row = (lane & 7) + ((lane & 16) >> 1), nt_u = (lane >> 3) & 1;
+  const int tr_row = (lane & 7) + (lane & 8), tr_u = lane >> 4;
+  const int r0 = mi * 16 + (lane >> 2), r1 = r0 + 8;
+
+  // ---- raw k and q, and 1 / (|x|^2 + eps)
+  constexpr int LPR = N / 8;
+  for (int w = 0; w < 2; ++w) {
+    const uint16_t* src = static_cast<const uint16_t*>(w ? d.q : d.k);
+    for (int i = tid; i < kC * LPR; i += kThreads) {
+      const int row = i / LPR, u = i % LPR;
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (row < valid)
+        raw = *reinterpret_cast<const uint4*>(src + ((row0 + row) * d.nkheads + kh) * N + u * 8);
+      *reinterpret_cast<uint4*>(smem + (w ? g.q : g.k) + row * g.xs + u * 16) = raw;
+      const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ss = fmaf(bf16_lo(v[j]), bf16_lo(v[j]), fmaf(bf16_hi(v[j]), bf16_hi(v[j]), ss));
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (u == 0) F[(w ? kfLq : kfLk) * kC + row] = d.qk_norm ? 1.f / (ss + kDeltaQkEps) : 0.f;
+    }
+  }
+  __syncthreads();
+
+  // ---- k k^T (for dbeta): rows of block mi, columns of this warp's half
+  float kk[2][2][4] = {};
+#pragma unroll
+  for (int kt = 0; kt < N / 16; ++kt) {
+    uint32_t a[4];
+    ldsm4(a, sm + g.k + (mi * 16 + a_row) * g.xs + (2 * kt + a_u) * 16);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int jp = 2 * half + x;
+      if (jp > mi) continue;
+      uint32_t bb[4];
+      ldsm4(bb, sm + g.k + (16 * jp + nt_row) * g.xs + (2 * kt + nt_u) * 16);
+      mma_bf16(kk[x][0], a, bb[0], bb[1]);
+      mma_bf16(kk[x][1], a, bb[2], bb[3]);
+    }
+  }
+
+  float tq[T][4] = {}, tk[T][4] = {};
+  for (int hx = 0; hx < rep; ++hx) {
+    const int h = kh * rep + hx;
+    const size_t bch = bc * d.nheads + h;
+    __syncthreads();  // the previous head's tiles are free
+
+    // ---- this head's tiles
+    const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes);
+    if (tid < kC) {
+      F[kfGhi * kC + tid] = sc[kScGhi * kC + tid];
+      F[kfGlo * kC + tid] = sc[kScGlo * kC + tid];
+      F[kfBeta * kC + tid] = sc[kScBeta * kC + tid];
+      F[kfKn * kC + tid] = sc[kScKn * kC + tid];
+      F[kfQn * kC + tid] = sc[kScQn * kC + tid];
+    }
+    const int ppr = P / 8;
+    for (int i = tid; i < 3 * kC * ppr; i += kThreads) {
+      const int w = i / (kC * ppr), j = i - w * kC * ppr, row = j / ppr, u = j - row * ppr;
+      const uint16_t* src = w == 0 ? p.dy : (w == 1 ? p.ws_r : p.dv);
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (row < valid)
+        raw = *reinterpret_cast<const uint4*>(src + ((row0 + row) * d.nheads + h) * P + u * 8);
+      *reinterpret_cast<uint4*>(smem + (w == 0 ? g.dy : (w == 1 ? g.r : g.dr)) + row * g.ps +
+                                u * 16) = raw;
+    }
+    const size_t sz = (size_t)P * N;
+    const size_t at = ((size_t)b * (p.nchunks + 1) + c) * d.nheads + h;
+    const float4* S0 = reinterpret_cast<const float4*>(p.ws_state + at * sz);
+    const float4* S1 = reinterpret_cast<const float4*>(p.ws_state + (at + d.nheads) * sz);
+    const float4* dS = reinterpret_cast<const float4*>(p.ws_dstate + bch * sz);
+    float dot = 0.f;
+    for (int i = tid; i < P * (N / 4); i += kThreads) {
+      const int row = i / (N / 4), u = i - row * (N / 4);
+      const float4 s0 = S0[i], s1 = S1[i], ds = dS[i];
+      dot = fmaf(s1.x, ds.x, fmaf(s1.y, ds.y, fmaf(s1.z, ds.z, fmaf(s1.w, ds.w, dot))));
+      *reinterpret_cast<uint2*>(smem + g.s + row * g.xs + u * 8) =
+          make_uint2(pack_bf16x2(s0.x, s0.y), pack_bf16x2(s0.z, s0.w));
+      *reinterpret_cast<uint2*>(smem + g.ds + row * g.xs + u * 8) =
+          make_uint2(pack_bf16x2(ds.x, ds.y), pack_bf16x2(ds.z, ds.w));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) F[kfRed * kC + warp] = dot;
+    __syncthreads();
+
+    // ---- dy r^T and dv r^T -> W, N + N^T, and the column sums of dbeta
+    float wv[2][2][4] = {}, xv[2][2][4] = {};
+    for (int kt = 0; kt < P / 16; ++kt) {
+      uint32_t a[4], e[4];
+      ldsm4(a, sm + g.dy + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+      ldsm4(e, sm + g.dr + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int jp = 2 * half + x;
+        if (jp > mi) continue;
+        uint32_t bb[4];
+        ldsm4(bb, sm + g.r + (16 * jp + nt_row) * g.ps + (2 * kt + nt_u) * 16);
+        mma_bf16(wv[x][0], a, bb[0], bb[1]);
+        mma_bf16(wv[x][1], a, bb[2], bb[3]);
+        mma_bf16(xv[x][0], e, bb[0], bb[1]);
+        mma_bf16(xv[x][1], e, bb[2], bb[3]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int jp = 2 * half + x;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float cs[2] = {0.f, 0.f};
+        if (jp <= mi) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = q < 2 ? r0 : r1, j = 16 * jp + 8 * y + 2 * (lane & 3) + (q & 1);
+            const float gm = j <= i ? ex2_approx((F[kfGhi * kC + i] - F[kfGhi * kC + j]) +
+                                                 (F[kfGlo * kC + i] - F[kfGlo * kC + j]))
+                                    : 0.f;
+            const float kni = F[kfKn * kC + i], knj = F[kfKn * kC + j];
+            const float gb = gm * F[kfBeta * kC + j];
+            const float w = j <= i ? gb * wv[x][y][q] : 0.f;
+            const float n = j < i ? -gb * xv[x][y][q] : 0.f;
+            if (j < i) cs[q & 1] = fmaf(gm * kni * knj * kk[x][y][q], xv[x][y][q], cs[q & 1]);
+            st16(smem + g.w1 + i * kWs + j * 2, w * knj);
+            st16(smem + g.w2 + i * kWs + j * 2, w * F[kfQn * kC + i]);
+            if (j <= i) {
+              st16(smem + g.ns + i * kWs + j * 2, n * knj);
+              st16(smem + g.ns + j * kWs + i * 2, n * kni);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) cs[q] += __shfl_xor_sync(0xffffffffu, cs[q], o);
+          if (lane < 4) F[(kfCol + mi) * kC + 16 * jp + 8 * y + 2 * lane + q] = cs[q];
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- dq += e^G dy S + W k;  dk += beta e^(G_end - G) r dS - e^G dv S + W^T q + (N + N^T) k
+    const float g0 = F[kfGhi * kC + r0], l0 = F[kfGlo * kC + r0];
+    const float g1 = F[kfGhi * kC + r1], l1 = F[kfGlo * kC + r1];
+    const float ge = F[kfGhi * kC + kC - 1], le = F[kfGlo * kC + kC - 1];
+    const float D0 = ex2_approx(g0 + l0), D1 = ex2_approx(g1 + l1);
+    const float E0 = ex2_approx((ge - g0) + (le - l0)) * F[kfBeta * kC + r0];
+    const float E1 = ex2_approx((ge - g1) + (le - l1)) * F[kfBeta * kC + r1];
+#pragma unroll
+    for (int w = 0; w < 3; ++w) {
+      const int at_a = w == 0 ? g.dy : (w == 1 ? g.r : g.dr), at_b = w == 1 ? g.ds : g.s;
+      float t[T][4] = {};
+      for (int kt = 0; kt < P / 16; ++kt) {
+        uint32_t a[4];
+        ldsm4(a, sm + at_a + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+#pragma unroll
+        for (int j = 0; j < T / 2; ++j) {
+          uint32_t bb[4];
+          ldsm4t(bb, sm + at_b + (16 * kt + tr_row) * g.xs + (half * T + 2 * j + tr_u) * 16);
+          mma_bf16(t[2 * j], a, bb[0], bb[1]);
+          mma_bf16(t[2 * j + 1], a, bb[2], bb[3]);
+        }
+      }
+      const float f0 = w == 0 ? D0 : (w == 1 ? E0 : -D0), f1 = w == 0 ? D1 : (w == 1 ? E1 : -D1);
+#pragma unroll
+      for (int j = 0; j < T; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float& o = w == 0 ? tq[j][q] : tk[j][q];
+          o = fmaf(q < 2 ? f0 : f1, t[j][q], o);
+        }
+    }
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+      uint32_t a[4], e[4], f[4];
+      ldsm4(a, sm + g.w1 + (mi * 16 + a_row) * kWs + (2 * kt + a_u) * 16);
+      ldsm4t(e, sm + g.w2 + (16 * kt + nt_row) * kWs + (2 * mi + nt_u) * 16);
+      ldsm4(f, sm + g.ns + (mi * 16 + a_row) * kWs + (2 * kt + a_u) * 16);
+#pragma unroll
+      for (int j = 0; j < T / 2; ++j) {
+        uint32_t bk[4], bq[4];
+        ldsm4t(bk, sm + g.k + (16 * kt + tr_row) * g.xs + (half * T + 2 * j + tr_u) * 16);
+        ldsm4t(bq, sm + g.q + (16 * kt + tr_row) * g.xs + (half * T + 2 * j + tr_u) * 16);
+        if (kt <= mi) {
+          mma_bf16(tq[2 * j], a, bk[0], bk[1]);
+          mma_bf16(tq[2 * j + 1], a, bk[2], bk[3]);
+        }
+        if (kt >= mi) {
+          mma_bf16(tk[2 * j], e, bq[0], bq[1]);
+          mma_bf16(tk[2 * j + 1], e, bq[2], bq[3]);
+        }
+        mma_bf16(tk[2 * j], f, bk[0], bk[1]);
+        mma_bf16(tk[2 * j + 1], f, bk[2], bk[3]);
+      }
+    }
+
+    // ---- the gates: one token per thread of the first two warps
+    if (tid < kC) {
+      const int sl = P / 16;
+      const float* du = p.ws_dotu + bch * sl * kC + tid;
+      const float* dO = p.ws_doto + bch * sl * kC + tid;
+      const float* dv = p.ws_dotv + bch * sl * kC + tid;
+      float su = 0.f, so = 0.f, sv = 0.f;
+      for (int i = 0; i < sl; ++i) {
+        su += du[i * kC];
+        so += dO[i * kC];
+        sv += dv[i * kC];
+      }
+      float raw = 0.f, beta_raw = 0.f;
+      const size_t gate_at = (row0 + tid) * d.nheads + h;
+      if (tid < valid) {
+        raw = bf16_to_f32(static_cast<const uint16_t*>(d.dt)[gate_at]) +
+              (d.dt_bias ? d.dt_bias[h] : 0.f);
+        beta_raw = bf16_to_f32(static_cast<const uint16_t*>(d.beta)[gate_at]);
+      }
+      float db = su;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) db -= F[(kfCol + i) * kC + tid];
+      if (d.beta_sigmoid) {
+        const float be = delta_beta(beta_raw, 1);
+        db *= be * (1.f - be);
+      }
+      // suffix sums over the chunk's 64 tokens
+      float dg = so - sv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float up = __shfl_down_sync(0xffffffffu, dg, o);
+        if (lane + o < 32) dg += up;
+      }
+      F[(kfRow)*kC + tid] = dg;
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (warp == 0) dg += F[(kfRow)*kC + 32];
+      float end = 0.f;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) end += F[kfRed * kC + i];
+      dg += end;
+      float dA = 0.f, dbias = 0.f;
+      if (tid < valid) {
+        const float step = delta_step_size(raw, d.softplus);
+        // dg = a <S_before, dS'>: after a decay below e^-20 it is less than the
+        // rounding of the sum above (2^-22 of its terms), so it is taken as 0
+        if (step * d.A[h] < -20.f) dg = 0.f;
+        const float sig = (d.softplus && raw <= kSoftplusCut) ? 1.f / (1.f + expf(-raw)) : 1.f;
+        const float ddt = dg * d.A[h] * sig;
+        dA = dg * step;
+        dbias = ddt;
+        p.ddt[gate_at] = f32_to_bf16(ddt);
+        p.dbeta[gate_at] = f32_to_bf16(db);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        dA += __shfl_xor_sync(0xffffffffu, dA, o);
+        dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+      }
+      if (lane == 0) {
+        F[(kfRow + 1) * kC + 2 * warp] = dA;
+        F[(kfRow + 1) * kC + 2 * warp + 1] = dbias;
+      }
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (tid < 2)
+        p.ws_part[bch * 2 + tid] = F[(kfRow + 1) * kC + tid] + F[(kfRow + 1) * kC + 2 + tid];
+    }
+  }
+
+  // ---- through x / |x| (dx = n (t - x (x . t) / |x|^2)), then bf16 rows
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const unsigned char* x = smem + (w ? g.q : g.k);
+    float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const int at = (half * T + j) * 16 + (lane & 3) * 4;
+      const uint32_t x0 = *reinterpret_cast<const uint32_t*>(x + r0 * g.xs + at);
+      const uint32_t x1 = *reinterpret_cast<const uint32_t*>(x + r1 * g.xs + at);
+      const float(&t)[4] = w ? tq[j] : tk[j];
+      d0 = fmaf(bf16_lo(x0), t[0], fmaf(bf16_hi(x0), t[1], d0));
+      d1 = fmaf(bf16_lo(x1), t[2], fmaf(bf16_hi(x1), t[3], d1));
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+      d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+    }
+    if ((lane & 3) == 0) {
+      F[(kfCol + 2 * w + half) * kC + r0] = d0;
+      F[(kfCol + 2 * w + half) * kC + r1] = d1;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const unsigned char* x = smem + (w ? g.q : g.k);
+    const float n0 = F[(w ? kfQn : kfKn) * kC + r0], n1 = F[(w ? kfQn : kfKn) * kC + r1];
+    const float e0 = F[(w ? kfLq : kfLk) * kC + r0] *
+                     (F[(kfCol + 2 * w) * kC + r0] + F[(kfCol + 2 * w + 1) * kC + r0]);
+    const float e1 = F[(w ? kfLq : kfLk) * kC + r1] *
+                     (F[(kfCol + 2 * w) * kC + r1] + F[(kfCol + 2 * w + 1) * kC + r1]);
+    uint16_t* dst = w ? p.dq : p.dk;
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+      const int at = (half * T + j) * 16 + (lane & 3) * 4;
+      const uint32_t x0 = *reinterpret_cast<const uint32_t*>(x + r0 * g.xs + at);
+      const uint32_t x1 = *reinterpret_cast<const uint32_t*>(x + r1 * g.xs + at);
+      const float(&t)[4] = w ? tq[j] : tk[j];
+      if (r0 < valid)
+        *reinterpret_cast<uint32_t*>(dst + ((row0 + r0) * d.nkheads + kh) * N + at / 2) =
+            pack_bf16x2(n0 * (t[0] - bf16_lo(x0) * e0), n0 * (t[1] - bf16_hi(x0) * e0));
+      if (r1 < valid)
+        *reinterpret_cast<uint32_t*>(dst + ((row0 + r1) * d.nkheads + kh) * N + at / 2) =
+            pack_bf16x2(n1 * (t[2] - bf16_lo(x1) * e1), n1 * (t[3] - bf16_hi(x1) * e1));
+    }
+  }
+}
+
+// dA, ddt_bias: the chunks' sums of one head, in a fixed order.
+__global__ void __launch_bounds__(128) delta_grad_reduce(const float* part, int64_t rows, int nheads,
+                                                         float* dA, float* dbias) {
+  __shared__ double sh[2][128];
+  const int h = blockIdx.x, tid = threadIdx.x;
+  double a = 0.0, s = 0.0;
+  for (int64_t i = tid; i < rows; i += 128) {
+    a += part[(i * nheads + h) * 2];
+    s += part[(i * nheads + h) * 2 + 1];
+  }
+  sh[0][tid] = a;
+  sh[1][tid] = s;
+  __syncthreads();
+  for (int o = 64; o > 0; o >>= 1) {
+    if (tid < o) {
+      sh[0][tid] += sh[0][tid + o];
+      sh[1][tid] += sh[1][tid + o];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    if (dA) dA[h] = (float)sh[0][0];
+    if (dbias) dbias[h] = (float)sh[1][0];
+  }
+}
+
+template <int N>
+cudaError_t launch(const DeltaChunkParams& p, cudaStream_t stream) {
+  const int bytes = grad_layout(N, p.d.headdim).bytes;
+  cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<N>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  delta_grad_kernel<N><<<dim3(p.nchunks, p.d.nkheads, p.d.batch), kThreads, bytes, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || (!p.dA && !p.ddt_bias)) return e;
+  delta_grad_reduce<<<p.d.nheads, 128, 0, stream>>>(p.ws_part, (int64_t)p.d.batch * p.nchunks,
+                                                    p.d.nheads, p.dA, p.ddt_bias);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_delta_grad(const DeltaChunkParams& p, cudaStream_t stream) {
+  return p.d.dstate == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+}
+
+}  // namespace ssm

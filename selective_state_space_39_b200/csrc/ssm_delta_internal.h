@@ -1,0 +1,95 @@
+// ssm_delta_internal.h -- parameters of the gated delta rule shared by the C
+// entry points (ssm_api.cu) and its kernels (ssm_delta_step.cu: token by
+// token; ssm_delta_prep.cu, ssm_delta_chunk.cu, ssm_delta_grad.cu: chunk by
+// chunk). Not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ssm {
+
+constexpr int kDeltaChunk = 64;        // tokens per chunk
+constexpr float kDeltaQkEps = 1e-6f;   // |x|^2 + eps under the unit-length scaling
+
+struct DeltaParams {
+  int batch, nheads, nkheads, headdim, dstate;
+  int64_t seqlen;
+  int softplus, beta_sigmoid, qk_norm;
+  float scale;
+  const void* q;         // (batch, seqlen, nkheads, dstate) io
+  const void* k;         // (batch, seqlen, nkheads, dstate) io
+  const void* v;         // (batch, seqlen, nheads, headdim) io
+  const void* dt;        // (batch, seqlen, nheads) io
+  const void* beta;      // (batch, seqlen, nheads) io
+  const float* A;        // (nheads)
+  const float* dt_bias;  // (nheads) or null
+  const float* h0;       // (batch, nheads, headdim, dstate) or null
+  void* y;               // (batch, seqlen, nheads, headdim) io or null
+  float* h_last;         // (batch, nheads, headdim, dstate) or null
+};
+
+// dstate values of the token-by-token kernel (any headdim, fp32 or bf16 io).
+bool delta_step_dstate_supported(int dstate);
+cudaError_t launch_delta_step(const DeltaParams& p, bool bf16, cudaStream_t stream);
+
+// ---- chunk by chunk (bf16 io) ---------------------------------------------
+// Per (batch row, chunk, key head) the workspace holds k and q as fp16 tiles
+// [64][dstate], every row scaled by a power of two; per (batch row, chunk,
+// head) a block of per-token factors and the 64 x 64 tiles of the chunk.
+enum DeltaScal {       // arrays of 64 floats in a head block
+  kScSk = 0,           // e^G kmul: S k16 -> the decayed prediction of v
+  kScU = 1,            // beta 2^-t: (T16 R) -> u
+  kScKend = 2,         // kmul e^(G_end - G): u -> its weight in the end state
+  kScK = 3,            // kmul: k = kmul k16
+  kScSq = 4,           // e^G qmul: S q16 -> y
+  kScP = 5,            // qmul 2^-p: (P16 u) -> y
+  kScEnd = 6,          // [0]: e^G_end
+  kScT = 7,            // 2^-t: (T16 R) -> r
+  kScBeta = 8,
+  kScGhi = 9,          // the running log decay, high and low part
+  kScGlo = 10,
+  kScKn = 11,          // unit-length factor of k
+  kScQn = 12,          // unit-length factor of q, times the readout scale
+  kScCount = 16,
+};
+constexpr int kDeltaScalBytes = kScCount * kDeltaChunk * 4;
+constexpr int kDeltaTile = kDeltaChunk * kDeltaChunk * 2;  // one fp16 64 x 64 tile
+constexpr int kDeltaHeadFwd = kDeltaScalBytes + 3 * kDeltaTile;  // factors, T hi, T lo, P hi
+constexpr int kDeltaHeadBwd = kDeltaScalBytes + 4 * kDeltaTile;  // and P lo
+
+struct DeltaChunkParams {
+  DeltaParams d;
+  int nchunks;
+  int head_bytes;        // kDeltaHeadFwd or kDeltaHeadBwd
+  unsigned char* ws_kq;  // (batch, nchunks, nkheads) x [k16 tile | q16 tile]
+  unsigned char* ws_head;  // (batch, nchunks, nheads) x head block
+  uint64_t wait_limit_ns;
+  int test_stall;
+  int warps;             // consumer warps per CTA of the chunk kernel, 16 rows of headdim each
+  int stages;
+  // backward only
+  const uint16_t* dy;    // (batch, seqlen, nheads, headdim)
+  const float* dh_last;  // or null
+  float* ws_state;       // (batch, nchunks + 1, nheads, headdim, dstate): state before each chunk
+  float* ws_dstate;      // (batch, nchunks, nheads, headdim, dstate): adjoint after each chunk
+  uint16_t* ws_r;        // (batch, seqlen, nheads, headdim): v minus the state's prediction
+  float* ws_doto;        // (batch, nchunks, nheads, headdim/16, 64): dy.y over 16 rows
+  float* ws_dotv;        //   ... dv.v
+  float* ws_dotu;        //   ... du.r
+  float* ws_part;        // (batch, nchunks, nheads, 2): partial dA, ddt_bias
+  uint16_t *dq, *dk, *dv, *ddt, *dbeta;
+  float *dA, *ddt_bias, *dh0;
+};
+
+bool delta_chunk_supported(int dstate, int headdim);
+size_t delta_chunk_smem(const DeltaChunkParams& p, bool reverse);
+cudaError_t launch_delta_prep(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
+cudaError_t launch_delta_chunk_fwd(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
+cudaError_t launch_delta_chunk_rev(const DeltaChunkParams& p, cudaStream_t stream);
+cudaError_t launch_delta_grad(const DeltaChunkParams& p, cudaStream_t stream);
+// Whether a bounded wait gave up since the last call (synchronises the stream).
+cudaError_t delta_chunk_status(cudaStream_t stream, int* timed_out);
+
+}  // namespace ssm
