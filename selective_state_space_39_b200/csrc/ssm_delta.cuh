@@ -61,21 +61,30 @@ __device__ __forceinline__ uint32_t swz(int row, int c) {
   return (uint32_t)(row * RB + ((c ^ (row & 7)) << 4));
 }
 
+// Byte offset inside a 16 x 16 block of a triangular tile (kDeltaTri).
+__device__ __forceinline__ uint32_t tri_at(int row, int half) {
+  return (uint32_t)(row * 32 + ((half ^ ((row >> 2) & 1)) << 4));
+}
+
 // ------------------------------------- fp32 operands as two pieces of fp16 --
 // x s = hi + lo with hi, lo fp16 and s a power of two that brings the largest
-// magnitude of the row to [2^14, 2^15): the two pieces carry 22 bits of every
-// element within 2^16 of the largest, and smaller ones to 2^-40 of the
+// magnitude of the row to [2^14, 2^15) (the carried state: to about 2^6, with
+// room to grow): the two pieces carry 22 bits of every element within 2^16
+// (2^8) of the largest, and smaller ones to 2^-40 (2^-32) of the
 // largest, so products keep fp32's accuracy at two MMAs (three where both
 // operands have two pieces; the dropped lo lo is 2^-24 of the product).
 // bf16 operands (k, q) are one exact fp16 piece under a row scale of their own.
 struct RowScale {
   float s, inv;
 };
-__device__ __forceinline__ RowScale row_scale(uint32_t e) {  // e: biased exponent of the maximum
-  e = e < 15u ? 15u : e;
+// s = 2^(top - e) for a largest magnitude of biased exponent e (top: the
+// exponent it is brought to)
+template <uint32_t top = 14>
+__device__ __forceinline__ RowScale row_scale(uint32_t e) {
+  e = e < 1u + top ? 1u + top : (e > 253u ? 253u : e);
   RowScale r;
-  r.s = __uint_as_float((268u - e) << 23);
-  r.inv = __uint_as_float((e - 14u) << 23);
+  r.s = __uint_as_float((254u + top - e) << 23);
+  r.inv = __uint_as_float((e - top) << 23);
   return r;
 }
 __device__ __forceinline__ uint32_t exponent_of(float m) { return __float_as_uint(m) >> 23; }
@@ -95,13 +104,24 @@ __device__ __forceinline__ void row_max(const float (&x)[T][4], float& m0, float
   }
 }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, uint32_t& lo) {
-  x *= s;
-  y *= s;
+// The pieces of two values that are in range already.
+__device__ __forceinline__ void pieces2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
   const float2 f = __half22float2(h);
+  const float2 d = fma2(f, make_float2(-1.f, -1.f), make_float2(x, y));
   hi = h2_bits(h);
-  lo = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
+  lo = h2_bits(__floats2half2_rn(d.x, d.y));
+}
+__device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, uint32_t& lo) {
+  const float2 v = mul2(make_float2(x, y), make_float2(s, s));
+  pieces2(v.x, v.y, hi, lo);
+}
+__device__ __forceinline__ void pieces_a(const float (&c0)[4], const float (&c1)[4],
+                                         uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  pieces2(c0[0], c0[1], hi[0], lo[0]);
+  pieces2(c0[2], c0[3], hi[1], lo[1]);
+  pieces2(c1[0], c1[1], hi[2], lo[2]);
+  pieces2(c1[2], c1[3], hi[3], lo[3]);
 }
 // A fragments (16 rows x 16 of k) of accumulator tiles c0 (k 0..7) and c1 (k 8..15).
 __device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], float s0,

@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     __syncthreads();  // the previous head's tiles are free
 
     // ---- this head's tiles
-    const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes);
+    const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes +
+                                                        4 * kDeltaTri);
     if (tid < kC) {
       F[kfGhi * kC + tid] = sc[kScGhi * kC + tid];
       F[kfGlo * kC + tid] = sc[kScGlo * kC + tid];

@@ -38,7 +38,7 @@ cudaError_t launch_delta_step(const DeltaParams& p, bool bf16, cudaStream_t stre
 // Per (batch row, chunk, key head) the workspace holds k and q as fp16 tiles
 // [64][dstate], every row scaled by a power of two; per (batch row, chunk,
 // head) a block of per-token factors and the 64 x 64 tiles of the chunk.
-enum DeltaScal {       // arrays of 64 floats in a head block
+enum DeltaScal {       // arrays of 64 floats in a head block; the forward pass reads the first seven
   kScSk = 0,           // e^G kmul: S k16 -> the decayed prediction of v
   kScU = 1,            // beta 2^-t: (T16 R) -> u
   kScKend = 2,         // kmul e^(G_end - G): u -> its weight in the end state
@@ -52,12 +52,17 @@ enum DeltaScal {       // arrays of 64 floats in a head block
   kScGlo = 10,
   kScKn = 11,          // unit-length factor of k
   kScQn = 12,          // unit-length factor of q, times the readout scale
-  kScCount = 16,
+  kScCount = 13,
 };
-constexpr int kDeltaScalBytes = kScCount * kDeltaChunk * 4;
-constexpr int kDeltaTile = kDeltaChunk * kDeltaChunk * 2;  // one fp16 64 x 64 tile
-constexpr int kDeltaHeadFwd = kDeltaScalBytes + 3 * kDeltaTile;  // factors, T hi, T lo, P hi
-constexpr int kDeltaHeadBwd = kDeltaScalBytes + 4 * kDeltaTile;  // and P lo
+// A lower triangular 64 x 64 fp16 tile: its ten 16 x 16 blocks (i, j <= i) in
+// row order, 512 bytes each, the two 16-byte halves of a row swapped in rows 4
+// .. 7 and 12 .. 15 (eight rows at one column then lie in eight bank groups).
+constexpr int kDeltaTri = 10 * 512;
+__host__ __device__ constexpr int delta_tri_block(int i, int j) { return (i * (i + 1) / 2 + j) * 512; }
+constexpr int kDeltaScalFwd = 7 * kDeltaChunk * 4, kDeltaScalBwd = kScCount * kDeltaChunk * 4;
+// A head block: T hi, T lo, P hi, (backward: P lo,) then the factors.
+constexpr int kDeltaHeadFwd = 3 * kDeltaTri + kDeltaScalFwd;
+constexpr int kDeltaHeadBwd = 4 * kDeltaTri + kDeltaScalBwd;
 
 struct DeltaChunkParams {
   DeltaParams d;
@@ -67,8 +72,7 @@ struct DeltaChunkParams {
   unsigned char* ws_head;  // (batch, nchunks, nheads) x head block
   uint64_t wait_limit_ns;
   int test_stall;
-  int warps;             // consumer warps per CTA of the chunk kernel, 16 rows of headdim each
-  int stages;
+  int blocks, stages;    // 16-row blocks of the state and tile stages per CTA (set by the launch)
   // backward only
   const uint16_t* dy;    // (batch, seqlen, nheads, headdim)
   const float* dh_last;  // or null
@@ -84,7 +88,6 @@ struct DeltaChunkParams {
 };
 
 bool delta_chunk_supported(int dstate, int headdim);
-size_t delta_chunk_smem(const DeltaChunkParams& p, bool reverse);
 cudaError_t launch_delta_prep(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
 cudaError_t launch_delta_chunk_fwd(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
 cudaError_t launch_delta_chunk_rev(const DeltaChunkParams& p, cudaStream_t stream);

@@ -4,14 +4,18 @@
 // With G_i the running log decay inside the chunk, k and q of unit length and
 //   M_ij = (k_i . k_j) e^(G_i - G_j)  (j < i),   P_ij = (q_i . k_j) e^(G_i - G_j)  (j <= i)
 // the chunk's residuals r (u = beta r) solve (I + M diag(beta)) r = v - e^G S k,
-// so the kernel writes T = (I + M diag(beta))^-1 (forward substitution in fp32,
-// one column per thread), P, and the per-token factors (DeltaScal). k and q are
-// written as fp16 rows scaled by a power of two (exact for every element
-// within 2^14 of the row's largest), T as two fp16 pieces and P as one (two for
-// the backward pass), each row under its own power-of-two scale. G is summed
-// in fp64 and kept as two floats: differences of G stay exact to fp32 even
-// after a token with a decay of e^-100 (log decays are cut there: the factor is
-// below the smallest fp32 either way).
+// so the kernel writes T = (I + M diag(beta))^-1, P, and the per-token factors
+// (DeltaScal). T is inverted block by block: the four 16 x 16 diagonal blocks by
+// forward substitution (one column per lane, fp32), then
+//   T_10 = -T_11 (L_10 T_00) and T_32 likewise, then the 32 x 32 block below them,
+// the products as tf32 MMAs of two pieces (21 bits; the rest of fp32's range
+// needs no scale). k and q are written as fp16 rows scaled by a power of two
+// (exact for every element within 2^14 of the row's largest), T as two fp16
+// pieces and P as one (two for the backward pass), each row under its own
+// power-of-two scale; only blocks on and below the diagonal are kept. G is
+// summed in fp64 and kept as two floats: differences of G stay exact to fp32
+// even after a token with a decay of e^-100 (log decays are cut there: the
+// factor is below the smallest fp32 either way).
 //
 // One CTA takes a chunk of a key head and two of its value heads: k k^T and
 // q k^T (fp16 MMAs) are shared by the heads.
@@ -40,46 +44,99 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
 template <int N>
 struct PrepSmem {
   static constexpr int kTile = kC * N * 2;
-  static constexpr int kA = 2 * kTile > 4 * kDeltaTile ? 2 * kTile : 4 * kDeltaTile;
-  static constexpr int kL = kHeads * kC * kLs * 4;
-  static constexpr int kScal = kHeads * kDeltaScalBytes;
+  static constexpr int kL = kC * kLs * 4;                  // L, then T, of one head
+  static constexpr int kWork = kL + 4 * kDeltaTri;         // and the tiles on their way out
+  static constexpr int kA = 2 * kTile > kWork ? 2 * kTile : kWork;  // over the k/q tiles
+  static constexpr int kScal = kHeads * kDeltaScalBwd;
   static constexpr int kTok = 4 * kC * 4;
-  static constexpr int kBytes = kA + kL + kScal + kTok + 64;
+  static constexpr int kBytes = kA + kScal + kTok + 64;
 };
 
+// tf32 MMA of two-piece fp32 operands: d += a b, hi lo cross terms included.
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void tf32_pieces(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xFFFFE000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// d[16 x 16] = A[16 x 16 K] B[16 K x 16], both fp32 with row stride kLs.
+template <int K>
+__device__ __forceinline__ void block_product(float (&d)[2][4], const float* A, const float* B,
+                                              int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[n][q] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16 * K; k += 8) {
+    uint32_t ah[4], al[4];
+    tf32_pieces(A[g * kLs + k + t], ah[0], al[0]);
+    tf32_pieces(A[(g + 8) * kLs + k + t], ah[1], al[1]);
+    tf32_pieces(A[g * kLs + k + t + 4], ah[2], al[2]);
+    tf32_pieces(A[(g + 8) * kLs + k + t + 4], ah[3], al[3]);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      uint32_t bh0, bl0, bh1, bl1;
+      tf32_pieces(B[(k + t) * kLs + 8 * n + g], bh0, bl0);
+      tf32_pieces(B[(k + t + 4) * kLs + 8 * n + g], bh1, bl1);
+      mma_tf32(d[n], al, bh0, bh1);
+      mma_tf32(d[n], ah, bl0, bl1);
+      mma_tf32(d[n], ah, bh0, bh1);
+    }
+  }
+}
+__device__ __forceinline__ void block_store(const float (&d)[2][4], float* D, float sign, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    *reinterpret_cast<float2*>(D + g * kLs + 8 * n + 2 * t) =
+        make_float2(sign * d[n][0], sign * d[n][1]);
+    *reinterpret_cast<float2*>(D + (g + 8) * kLs + 8 * n + 2 * t) =
+        make_float2(sign * d[n][2], sign * d[n][3]);
+  }
+}
+
 template <int N, bool BWD>
-__global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaChunkParams p) {
+__global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChunkParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   using Sm = PrepSmem<N>;
   constexpr int RB = N * 2;        // bytes of a k/q row
   constexpr int LPR = N / 8;       // lanes (16-byte units) per row
   constexpr int RPW = 32 / LPR;    // rows per warp and step
   unsigned char* tiles = smem;
-  float* Lm = reinterpret_cast<float*>(smem + Sm::kA);
-  float* scal = reinterpret_cast<float*>(smem + Sm::kA + Sm::kL);
-  float* tok = reinterpret_cast<float*>(smem + Sm::kA + Sm::kL + Sm::kScal);  // kmul qmul kn qn
-  double* carry = reinterpret_cast<double*>(smem + Sm::kA + Sm::kL + Sm::kScal + Sm::kTok);
-  const DeltaParams& d = p.d;
+  float* L = reinterpret_cast<float*>(smem);
+  unsigned char* tri = smem + Sm::kL;  // T hi, T lo, P hi, P lo
+  float* scal = reinterpret_cast<float*>(smem + Sm::kA);
+  float* tok = reinterpret_cast<float*>(smem + Sm::kA + Sm::kScal);  // kmul qmul kn qn
+  double* carry = reinterpret_cast<double*>(smem + Sm::kA + Sm::kScal + Sm::kTok);
+  const DeltaParams& d_ = p.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, b = blockIdx.z;
-  const int rep = d.nheads / d.nkheads, subs = (rep + kHeads - 1) / kHeads;
+  const int rep = d_.nheads / d_.nkheads, subs = (rep + kHeads - 1) / kHeads;
   const int kh = blockIdx.y / subs, sub = blockIdx.y - kh * subs;
   const int64_t t0 = (int64_t)c * kC;
-  const int valid = (int)min((int64_t)kC, d.seqlen - t0);
+  const int valid = (int)min((int64_t)kC, d_.seqlen - t0);
   const size_t bc = (size_t)b * p.nchunks + c;
 
   // ---- k and q rows: largest magnitude, length, fp16 rows
-  unsigned char* kq_out = p.ws_kq + (bc * d.nkheads + kh) * (size_t)(2 * Sm::kTile);
+  unsigned char* kq_out = p.ws_kq + (bc * d_.nkheads + kh) * (size_t)(2 * Sm::kTile);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const uint16_t* src = static_cast<const uint16_t*>(w ? d.q : d.k);
+    const uint16_t* src = static_cast<const uint16_t*>(w ? d_.q : d_.k);
 #pragma unroll
     for (int it = 0; it < kC / (4 * RPW); ++it) {
       const int row = it * 4 * RPW + warp * RPW + lane / LPR, u = lane % LPR;
       uint4 raw = make_uint4(0u, 0u, 0u, 0u);
       if (row < valid)
         raw = *reinterpret_cast<const uint4*>(
-            src + (((size_t)b * d.seqlen + t0 + row) * d.nkheads + kh) * N + u * 8);
+            src + (((size_t)b * d_.seqlen + t0 + row) * d_.nkheads + kh) * N + u * 8);
       float f[8];
       unpack8(raw, f);
       float m = 0.f, ss = 0.f;
@@ -106,8 +163,8 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaChunkPa
       *reinterpret_cast<uint4*>(tiles + w * Sm::kTile + at) = out;
       if (sub == 0) *reinterpret_cast<uint4*>(kq_out + w * Sm::kTile + at) = out;
       if (u == 0) {
-        const float len = d.qk_norm ? 1.f / sqrtf(ss + kDeltaQkEps) : 1.f;
-        const float sc = w ? d.scale : 1.f;
+        const float len = d_.qk_norm ? 1.f / sqrtf(ss + kDeltaQkEps) : 1.f;
+        const float sc = w ? d_.scale : 1.f;
         tok[w * kC + row] = len * inv * sc;
         tok[(2 + w) * kC + row] = len * sc;
       }
@@ -123,13 +180,13 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaChunkPa
     double g = 0.0;
     float beta = 0.f;
     if (hl < nh && i < valid) {
-      const size_t at = ((size_t)b * d.seqlen + t0 + i) * d.nheads + h;
-      const float raw = bf16_to_f32(static_cast<const uint16_t*>(d.dt)[at]) +
-                        (d.dt_bias ? d.dt_bias[h] : 0.f);
-      float gf = delta_step_size(raw, d.softplus) * d.A[h];
+      const size_t at = ((size_t)b * d_.seqlen + t0 + i) * d_.nheads + h;
+      const float raw = bf16_to_f32(static_cast<const uint16_t*>(d_.dt)[at]) +
+                        (d_.dt_bias ? d_.dt_bias[h] : 0.f);
+      float gf = delta_step_size(raw, d_.softplus) * d_.A[h];
       gf = gf < kMinLogDecay ? kMinLogDecay : gf;
       g = (double)gf * 1.4426950408889634;  // log2 units
-      beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d.beta)[at]), d.beta_sigmoid);
+      beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d_.beta)[at]), d_.beta_sigmoid);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -139,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaChunkPa
     if ((warp & 1) == 0 && lane == 31) carry[hl] = g;
     __syncthreads();
     if (warp & 1) g += carry[hl];
-    float* sc = scal + hl * (kDeltaScalBytes / 4);
+    float* sc = scal + hl * (kDeltaScalBwd / 4);
     const float hi = (float)g;
     sc[kScGhi * kC + i] = hi;
     sc[kScGlo * kC + i] = (float)(g - (double)hi);
@@ -179,34 +236,40 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaChunkPa
       }
     }
   }
-  __syncthreads();  // the k/q tiles are free: P is staged over them
-
   const int r0 = warp * 16 + (lane >> 2), r1 = r0 + 8;
-#pragma unroll
-  for (int x = 0; x < kHeads; ++x) {
-    if (x >= nh) break;
-    float* sc = scal + x * (kDeltaScalBytes / 4);
-    float* L = Lm + x * kC * kLs;
-    unsigned char* pst = tiles + x * 2 * kDeltaTile;
+  constexpr int kTiles = BWD ? 4 : 3;
+  for (int x = 0; x < nh; ++x) {
+    __syncthreads();  // the k/q tiles, or the previous head's, are free
+    float* sc = scal + x * (kDeltaScalBwd / 4);
     const float gh0 = sc[kScGhi * kC + r0], gl0 = sc[kScGlo * kC + r0];
     const float gh1 = sc[kScGhi * kC + r1], gl1 = sc[kScGlo * kC + r1];
     const float km0 = tok[r0], km1 = tok[r1];
+
+    // ---- L = M diag(beta) and P on the warp's 16 rows
     float pv[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) pv[j][q] = 0.f;
       if (j > 2 * warp + 1) continue;
+      const int col = 8 * j + 2 * (lane & 3);
+      const float2 ch = *reinterpret_cast<const float2*>(sc + kScGhi * kC + col);
+      const float2 cl = *reinterpret_cast<const float2*>(sc + kScGlo * kC + col);
+      const float2 cb = *reinterpret_cast<const float2*>(sc + kScBeta * kC + col);
+      const float2 ck = *reinterpret_cast<const float2*>(tok + col);
+      float lv[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int col = 8 * j + 2 * (lane & 3) + (q & 1), row = q < 2 ? r0 : r1;
-        const float gm = ex2_approx(((q < 2 ? gh0 : gh1) - sc[kScGhi * kC + col]) +
-                                    ((q < 2 ? gl0 : gl1) - sc[kScGlo * kC + col]));
-        if (col <= row) pv[j][q] = qk[j][q] * gm;
-        L[row * kLs + col] = col < row ? kk[j][q] * gm * (q < 2 ? km0 : km1) * tok[col] *
-                                             sc[kScBeta * kC + col]
-                                       : 0.f;
+        const int cc = col + (q & 1), row = q < 2 ? r0 : r1;
+        const float gm = ex2_approx(((q < 2 ? gh0 : gh1) - ((q & 1) ? ch.y : ch.x)) +
+                                    ((q < 2 ? gl0 : gl1) - ((q & 1) ? cl.y : cl.x)));
+        if (cc <= row) pv[j][q] = qk[j][q] * gm;
+        lv[q] = cc < row ? kk[j][q] * gm * (q < 2 ? km0 : km1) *
+                               ((q & 1) ? ck.y * cb.y : ck.x * cb.x)
+                         : 0.f;
       }
+      *reinterpret_cast<float2*>(L + r0 * kLs + col) = make_float2(lv[0], lv[1]);
+      *reinterpret_cast<float2*>(L + r1 * kLs + col) = make_float2(lv[2], lv[3]);
     }
     float m0, m1;
     row_max(pv, m0, m1);
@@ -217,107 +280,117 @@ __global__ void __launch_bounds__(kThreads) delta_prep_kernel(const DeltaChunkPa
       uint32_t hi0, lo0, hi1, lo1;
       split2(pv[j][0], pv[j][1], s0.s, hi0, lo0);
       split2(pv[j][2], pv[j][3], s1.s, hi1, lo1);
-      const uint32_t a0 = swz<128>(r0, j) + (lane & 3) * 4, a1 = swz<128>(r1, j) + (lane & 3) * 4;
-      *reinterpret_cast<uint32_t*>(pst + a0) = hi0;
-      *reinterpret_cast<uint32_t*>(pst + a1) = hi1;
+      unsigned char* ph = tri + 2 * kDeltaTri + delta_tri_block(warp, j >> 1) + (lane & 3) * 4;
+      const uint32_t a0 = tri_at(lane >> 2, j & 1), a1 = tri_at((lane >> 2) + 8, j & 1);
+      *reinterpret_cast<uint32_t*>(ph + a0) = hi0;
+      *reinterpret_cast<uint32_t*>(ph + a1) = hi1;
       if (BWD) {
-        *reinterpret_cast<uint32_t*>(pst + kDeltaTile + a0) = lo0;
-        *reinterpret_cast<uint32_t*>(pst + kDeltaTile + a1) = lo1;
+        *reinterpret_cast<uint32_t*>(ph + kDeltaTri + a0) = lo0;
+        *reinterpret_cast<uint32_t*>(ph + kDeltaTri + a1) = lo1;
       }
+    }
+    // blocks (0, 1) and (2, 3) are read as part of T's 32 x 32 diagonal blocks
+    if (!(warp & 1)) {
+      const float d0[2][4] = {};
+      block_store(d0, L + warp * 16 * kLs + (warp + 1) * 16, 1.f, lane);
     }
     if ((lane & 3) == 0) {
       sc[kScP * kC + r0] = tok[kC + r0] * s0.inv;
       sc[kScP * kC + r1] = tok[kC + r1] * s1.inv;
     }
-  }
-  __syncthreads();
+    __syncwarp();
 
-  // ---- T = (I + L)^-1: column `col` of head hl per thread
-  const int col = tid & 63;
-  float xs[kC];
-  if (hl < nh) {
-    const float* L = Lm + hl * kC * kLs;
-    // columns 32.. are zero above row 32: the second warp starts there
-    if ((warp & 1) == 0) {
+    // ---- T, the diagonal block of the warp's rows: column `lane` by forward
+    // substitution (lanes 16 .. 31 repeat lanes 0 .. 15)
+    {
+      float* Ld = L + (warp * 16) * kLs + warp * 16;
+      const int col = lane & 15;
+      float xs[16];
 #pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        float acc = i == col ? 1.f : 0.f;
+      for (int i = 0; i < 16; ++i) {
+        float acc0 = i == col ? 1.f : 0.f, acc1 = 0.f;
 #pragma unroll
         for (int j = 0; j < i; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(L + i * kLs + j);
-          acc = fmaf(-l.x, xs[j], acc);
-          if (j + 1 < i) acc = fmaf(-l.y, xs[j + 1], acc);
-          if (j + 2 < i) acc = fmaf(-l.z, xs[j + 2], acc);
-          if (j + 3 < i) acc = fmaf(-l.w, xs[j + 3], acc);
+          const float4 l = *reinterpret_cast<const float4*>(Ld + i * kLs + j);
+          acc0 = fmaf(-l.x, xs[j], acc0);
+          if (j + 1 < i) acc1 = fmaf(-l.y, xs[j + 1], acc1);
+          if (j + 2 < i) acc0 = fmaf(-l.z, xs[j + 2], acc0);
+          if (j + 3 < i) acc1 = fmaf(-l.w, xs[j + 3], acc1);
         }
-        xs[i] = acc;
+        xs[i] = acc0 + acc1;
       }
-    } else {
+      __syncwarp();
+      if (lane < 16) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) xs[i] = 0.f;
-#pragma unroll
-      for (int i = 32; i < kC; ++i) {
-        float acc = i == col ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 32; j < i; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(L + i * kLs + j);
-          acc = fmaf(-l.x, xs[j], acc);
-          if (j + 1 < i) acc = fmaf(-l.y, xs[j + 1], acc);
-          if (j + 2 < i) acc = fmaf(-l.z, xs[j + 2], acc);
-          if (j + 3 < i) acc = fmaf(-l.w, xs[j + 3], acc);
-        }
-        xs[i] = acc;
+        for (int i = 0; i < 16; ++i) Ld[i * kLs + col] = xs[i];
       }
     }
-  }
-  __syncthreads();
-  if (hl < nh) {
-    float* L = Lm + hl * kC * kLs;
-#pragma unroll
-    for (int i = 0; i < kC; ++i) L[i * kLs + col] = xs[i];
-  }
-  __syncthreads();
-  if (hl < nh) {  // thread: one row, its scale and its two pieces
-    const int row = tid & 63;
-    const float* L = Lm + hl * kC * kLs + row * kLs;
-    float* sc = scal + hl * (kDeltaScalBytes / 4);
-    unsigned char* out = p.ws_head + (bc * d.nheads + h) * (size_t)p.head_bytes + kDeltaScalBytes;
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < kC; j += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(L + j);
-      m = fmaxf(fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-    }
-    const RowScale s = row_scale(exponent_of(m));
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      uint4 hi, lo;
-      const float4 v0 = *reinterpret_cast<const float4*>(L + u * 8);
-      const float4 v1 = *reinterpret_cast<const float4*>(L + u * 8 + 4);
-      split2(v0.x, v0.y, s.s, hi.x, lo.x);
-      split2(v0.z, v0.w, s.s, hi.y, lo.y);
-      split2(v1.x, v1.y, s.s, hi.z, lo.z);
-      split2(v1.z, v1.w, s.s, hi.w, lo.w);
-      const uint32_t at = swz<128>(row, u);
-      *reinterpret_cast<uint4*>(out + at) = hi;
-      *reinterpret_cast<uint4*>(out + kDeltaTile + at) = lo;
-    }
-    sc[kScU * kC + row] = sc[kScBeta * kC + row] * s.inv;
-    sc[kScT * kC + row] = s.inv;
-  }
-  __syncthreads();
+    __syncthreads();
 
-  // ---- P and the factors
-  constexpr int kPBytes = (BWD ? 2 : 1) * kDeltaTile;
-  for (int x = 0; x < nh; ++x) {
-    unsigned char* out = p.ws_head +
-                         (bc * d.nheads + kh * rep + sub * kHeads + x) * (size_t)p.head_bytes;
-    const uint4* ps = reinterpret_cast<const uint4*>(tiles + x * 2 * kDeltaTile);
-    uint4* po = reinterpret_cast<uint4*>(out + kDeltaScalBytes + 2 * kDeltaTile);
-    for (int i = tid; i < kPBytes / 16; i += kThreads) po[i] = ps[i];
-    const uint4* ss = reinterpret_cast<const uint4*>(scal + x * (kDeltaScalBytes / 4));
-    for (int i = tid; i < (kScQn + 1) * kC * 4 / 16; i += kThreads)
-      reinterpret_cast<uint4*>(out)[i] = ss[i];
+    // ---- T_10, T_32 (warps 1 and 3), then the 32 x 32 block below the diagonal
+    float d[2][4];
+    if (warp & 1) {
+      float* Lo = L + (warp * 16) * kLs + (warp - 1) * 16;
+      block_product<1>(d, Lo, L + (warp - 1) * 16 * kLs + (warp - 1) * 16, lane);
+      __syncwarp();
+      block_store(d, Lo, 1.f, lane);
+      __syncwarp();
+      block_product<1>(d, L + (warp * 16) * kLs + warp * 16, Lo, lane);
+      __syncwarp();
+      block_store(d, Lo, -1.f, lane);
+    }
+    __syncthreads();
+    const int bi = warp >> 1, bj = warp & 1;  // this warp's 16 x 16 of the 32 x 32 block
+    float* Lba = L + 32 * kLs;
+    block_product<2>(d, Lba + bi * 16 * kLs, L + bj * 16, lane);
+    __syncthreads();
+    block_store(d, Lba + bi * 16 * kLs + bj * 16, 1.f, lane);
+    __syncthreads();
+    block_product<2>(d, L + (32 + bi * 16) * kLs + 32, Lba + bj * 16, lane);
+    __syncthreads();
+    block_store(d, Lba + bi * 16 * kLs + bj * 16, -1.f, lane);
+    __syncthreads();
+
+    // ---- T's rows as two pieces: two threads per row
+    {
+      const int row = tid >> 1, half = tid & 1, nb = row / 16 + 1;  // blocks of this row
+      const float* Lr = L + row * kLs;
+      float m = 0.f;
+      for (int j = half; j < 2 * nb; j += 2) {
+        const float4 a = *reinterpret_cast<const float4*>(Lr + j * 8);
+        const float4 b = *reinterpret_cast<const float4*>(Lr + j * 8 + 4);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))));
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+      }
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      const RowScale s = row_scale(exponent_of(m));
+      for (int j = 0; j < nb; ++j) {
+        uint4 hi, lo;
+        const float4 v0 = *reinterpret_cast<const float4*>(Lr + j * 16 + half * 8);
+        const float4 v1 = *reinterpret_cast<const float4*>(Lr + j * 16 + half * 8 + 4);
+        split2(v0.x, v0.y, s.s, hi.x, lo.x);
+        split2(v0.z, v0.w, s.s, hi.y, lo.y);
+        split2(v1.x, v1.y, s.s, hi.z, lo.z);
+        split2(v1.z, v1.w, s.s, hi.w, lo.w);
+        unsigned char* at = tri + delta_tri_block(row / 16, j) + tri_at(row & 15, half);
+        *reinterpret_cast<uint4*>(at) = hi;
+        *reinterpret_cast<uint4*>(at + kDeltaTri) = lo;
+      }
+      if (half == 0) {
+        sc[kScU * kC + row] = sc[kScBeta * kC + row] * s.inv;
+        sc[kScT * kC + row] = s.inv;
+      }
+    }
+    __syncthreads();
+
+    // ---- out: the tiles, then the factors
+    uint4* out = reinterpret_cast<uint4*>(
+        p.ws_head + (bc * d_.nheads + kh * rep + sub * kHeads + x) * (size_t)p.head_bytes);
+    const uint4* ts = reinterpret_cast<const uint4*>(tri);
+    for (int i = tid; i < kTiles * kDeltaTri / 16; i += kThreads) out[i] = ts[i];
+    const uint4* ss = reinterpret_cast<const uint4*>(sc);
+    for (int i = tid; i < (BWD ? kDeltaScalBwd : kDeltaScalFwd) / 16; i += kThreads)
+      out[kTiles * kDeltaTri / 16 + i] = ss[i];
   }
 }
 

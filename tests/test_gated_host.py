@@ -143,7 +143,7 @@ def test_workspace_sizes(L):
     assert w(2, 100, 4, 2, 40, 64, 1) == 0 and w(2, 100, 4, 2, 64, 32, 1) == 0
     assert w(2, 100, 4, 2, 64, 64, 0) == 0                # fp32 io
     # two chunks: k and q tiles of the key heads, a block per head
-    assert w(2, 100, 4, 2, 64, 64, 1) == 2 * 2 * (2 * 2 * 64 * 64 * 2 + 4 * (4096 + 3 * 8192))
+    assert w(2, 100, 4, 2, 64, 64, 1) == 2 * 2 * (2 * 2 * 64 * 64 * 2 + 4 * (7 * 256 + 3 * 5120))
     assert w(2, 100, 3, 2, 64, 64, 1) == 0
     assert L.ssm_gated_delta_bwd_workspace_bytes(2, 100, 4, 2, 64, 64, 0) == 0
 
