@@ -75,15 +75,16 @@ __host__ __device__ inline Layout layout(int dstate, int blocks, int per_head, i
   return l;
 }
 
-// acc += A (two pieces) B^T, B tile rows = n (k contiguous): pairs jp of n-tiles
-template <bool LO>
-__device__ __forceinline__ void mma_pair(float (&a0)[4], float (&a1)[4], const uint32_t (&hi)[4],
-                                         const uint32_t (&lo)[4], const uint32_t (&b)[4]) {
-  mma_f16(a0, hi, b[0], b[1]);
-  mma_f16(a1, hi, b[2], b[3]);
-  if (LO) {
-    mma_f16(a0, lo, b[0], b[1]);
-    mma_f16(a1, lo, b[2], b[3]);
+// Pairs of neighbouring tiles += A times their B fragments. The accumulators of
+// one piece are all visited before the next piece's, so that no MMA waits for
+// the one before it.
+template <int T, int P>
+__device__ __forceinline__ void mma_tiles(float (&acc)[T][4], const uint32_t (&a)[4],
+                                          const uint32_t (&b)[P][4], int t0 = 0) {
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    mma_f16(acc[t0 + 2 * j], a, b[j][0], b[j][1]);
+    mma_f16(acc[t0 + 2 * j + 1], a, b[j][2], b[j][3]);
   }
 }
 
@@ -118,23 +119,31 @@ __device__ __forceinline__ void tri_product(float (&acc)[TT][4], const float (&x
       split_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi, lo);
     else
       half_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi);
+    uint32_t bh[TT / 2][4], bl[TT / 2][4];
 #pragma unroll
     for (int jj = 0; jj < TT / 2; ++jj) {
       const int jp = jp0 + jj;
       if (TR ? jp > kt : jp < kt) continue;  // warp-uniform
-      uint32_t b[4];
       const uint32_t at = TR ? delta_tri_block(kt, jp) + m.tr_tri : delta_tri_block(jp, kt) + m.nt_tri;
-      if (TR)
-        ldsm4t(b, bhi + at);
-      else
-        ldsm4(b, bhi + at);
-      mma_pair<XLO>(acc[2 * jj], acc[2 * jj + 1], hi, lo, b);
-      if (BLO) {
-        if (TR)
-          ldsm4t(b, blo + at);
-        else
-          ldsm4(b, blo + at);
-        mma_pair<false>(acc[2 * jj], acc[2 * jj + 1], hi, lo, b);
+      if (TR) {
+        ldsm4t(bh[jj], bhi + at);
+        if (BLO) ldsm4t(bl[jj], blo + at);
+      } else {
+        ldsm4(bh[jj], bhi + at);
+        if (BLO) ldsm4(bl[jj], blo + at);
+      }
+    }
+#pragma unroll
+    for (int piece = 0; piece < 3; ++piece) {
+      if ((piece == 1 && !XLO) || (piece == 2 && !BLO)) continue;
+#pragma unroll
+      for (int jj = 0; jj < TT / 2; ++jj) {
+        const int jp = jp0 + jj;
+        if (TR ? jp > kt : jp < kt) continue;
+        const uint32_t(&a)[4] = piece == 1 ? lo : hi;
+        const uint32_t(&b)[4] = piece == 2 ? bl[jj] : bh[jj];
+        mma_f16(acc[2 * jj], a, b[0], b[1]);
+        mma_f16(acc[2 * jj + 1], a, b[2], b[3]);
       }
     }
   }
@@ -151,10 +160,12 @@ __device__ __forceinline__ void state_product(float (&s)[NS / 8][4], const float
     uint32_t hi[4], lo[4];
     split_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi, lo);
 #pragma unroll
-    for (int jn = 0; jn < NS / 16; ++jn) {
-      uint32_t b[4];
-      ldsm4t(b, tile + swz<N * 2>(16 * kt + m.tr_row, u0 + 2 * jn + m.tr_unit));
-      mma_pair<true>(s[2 * jn], s[2 * jn + 1], hi, lo, b);
+    for (int jn = 0; jn < NS / 16; jn += 2) {
+      uint32_t b[2][4];
+      ldsm4t(b[0], tile + swz<N * 2>(16 * kt + m.tr_row, u0 + 2 * jn + m.tr_unit));
+      ldsm4t(b[1], tile + swz<N * 2>(16 * kt + m.tr_row, u0 + 2 * jn + 2 + m.tr_unit));
+      mma_tiles(s, hi, b, 2 * jn);
+      mma_tiles(s, lo, b, 2 * jn);
     }
   }
 }
@@ -519,15 +530,17 @@ __global__ void __launch_bounds__(256, 1) delta_fwd_kernel(const __grid_constant
     for (int kt = 0; kt < NS / 16; ++kt) {
       uint32_t hi[4], lo[4];
       pieces_a(S[2 * kt], S[2 * kt + 1], hi, lo);
+      uint32_t bk[4][4], bq[4][4];
 #pragma unroll
       for (int jp = 0; jp < 4; ++jp) {
-        uint32_t bb[4];
         const uint32_t at = swz<N * 2>(16 * jp + m.nt_row, u0 + 2 * kt + m.nt_unit);
-        ldsm4(bb, ks + at);
-        mma_pair<true>(x[2 * jp], x[2 * jp + 1], hi, lo, bb);
-        ldsm4(bb, qs + at);
-        mma_pair<BWD>(o[2 * jp], o[2 * jp + 1], hi, lo, bb);
+        ldsm4(bk[jp], ks + at);
+        ldsm4(bq[jp], qs + at);
       }
+      mma_tiles(x, hi, bk);
+      mma_tiles(o, hi, bq);
+      mma_tiles(x, lo, bk);
+      if (BWD) mma_tiles(o, lo, bq);
     }
     scale_rows(x, inv0, inv1);
     own<TT>(y, o, hf);
@@ -690,12 +703,12 @@ __global__ void __launch_bounds__(256, 1) delta_rev_kernel(const __grid_constant
     for (int kt = 0; kt < NS / 16; ++kt) {
       uint32_t hi[4], lo[4];
       pieces_a(S[2 * kt], S[2 * kt + 1], hi, lo);
+      uint32_t bk[4][4];
 #pragma unroll
-      for (int jp = 0; jp < 4; ++jp) {
-        uint32_t bb[4];
-        ldsm4(bb, ks + swz<N * 2>(16 * jp + m.nt_row, u0 + 2 * kt + m.nt_unit));
-        mma_pair<true>(x[2 * jp], x[2 * jp + 1], hi, lo, bb);
-      }
+      for (int jp = 0; jp < 4; ++jp)
+        ldsm4(bk[jp], ks + swz<N * 2>(16 * jp + m.nt_row, u0 + 2 * kt + m.nt_unit));
+      mma_tiles(x, hi, bk);
+      mma_tiles(x, lo, bk);
     }
     scale_rows(x, inv0, inv1);
     if (SP == 2) {

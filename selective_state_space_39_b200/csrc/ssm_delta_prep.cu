@@ -17,8 +17,11 @@
 // even after a token with a decay of e^-100 (log decays are cut there: the
 // factor is below the smallest fp32 either way).
 //
-// One CTA takes a chunk of a key head and two of its value heads: k k^T and
-// q k^T (fp16 MMAs) are shared by the heads.
+// One CTA takes a chunk of a key head and up to four of its value heads: the
+// fp16 rows, k k^T and q k^T (fp16 MMAs) are shared by the heads. Below the
+// diagonal blocks the decay is a product of a row's and a column's factor
+// around the start of the row's block, e^(G_i - G_s) e^(G_s - G_j), neither
+// above 1; inside them it is taken from the difference itself.
 #include "ssm_delta.cuh"
 
 namespace ssm {
@@ -27,19 +30,9 @@ namespace {
 
 constexpr int kC = kDeltaChunk;
 constexpr int kThreads = 128;
-constexpr int kHeads = 2;        // value heads per CTA
+constexpr int kHeads = 4;        // value heads per CTA, at most
 constexpr int kLs = kC + 4;      // row stride (floats) of the fp32 matrices
 constexpr float kMinLogDecay = -100.f;
-
-// 8 bf16 values of a unit -> fp32
-__device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(u[i]);
-    f[2 * i + 1] = bf16_hi(u[i]);
-  }
-}
 
 template <int N>
 struct PrepSmem {
@@ -49,14 +42,14 @@ struct PrepSmem {
   static constexpr int kA = 2 * kTile > kWork ? 2 * kTile : kWork;  // over the k/q tiles
   static constexpr int kScal = kHeads * kDeltaScalBwd;
   static constexpr int kTok = 4 * kC * 4;
-  static constexpr int kBytes = kA + kScal + kTok + 64;
+  static constexpr int kCols = 2 * 3 * kC * 4;             // column factors per row block
+  static constexpr int kBytes = kA + kScal + kTok + kCols + 64;
 };
 
 // tf32 MMA of two-piece fp32 operands: d += a b, hi lo cross terms included.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -65,17 +58,16 @@ __device__ __forceinline__ void tf32_pieces(float x, uint32_t& hi, uint32_t& lo)
   hi = __float_as_uint(x) & 0xFFFFE000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
-// d[16 x 16] = A[16 x 16 K] B[16 K x 16], both fp32 with row stride kLs.
-template <int K>
+// d[16 x 16] = A[16 x n] B[n x 16] over k0 <= n < k1, both fp32 with row stride kLs.
 __device__ __forceinline__ void block_product(float (&d)[2][4], const float* A, const float* B,
-                                              int lane) {
+                                              int k0, int k1, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int q = 0; q < 4; ++q) d[n][q] = 0.f;
-#pragma unroll
-  for (int k = 0; k < 16 * K; k += 8) {
+#pragma unroll 2
+  for (int k = k0; k < k1; k += 8) {
     uint32_t ah[4], al[4];
     tf32_pieces(A[g * kLs + k + t], ah[0], al[0]);
     tf32_pieces(A[(g + 8) * kLs + k + t], ah[1], al[1]);
@@ -115,7 +107,8 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
   unsigned char* tri = smem + Sm::kL;  // T hi, T lo, P hi, P lo
   float* scal = reinterpret_cast<float*>(smem + Sm::kA);
   float* tok = reinterpret_cast<float*>(smem + Sm::kA + Sm::kScal);  // kmul qmul kn qn
-  double* carry = reinterpret_cast<double*>(smem + Sm::kA + Sm::kScal + Sm::kTok);
+  float* cols = tok + 4 * kC;  // [row block 1..3][P, L] x 64
+  double* carry = reinterpret_cast<double*>(smem + Sm::kA + Sm::kScal + Sm::kTok + Sm::kCols);
   const DeltaParams& d_ = p.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, b = blockIdx.z;
@@ -127,38 +120,48 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
 
   // ---- k and q rows: largest magnitude, length, fp16 rows
   unsigned char* kq_out = p.ws_kq + (bc * d_.nkheads + kh) * (size_t)(2 * Sm::kTile);
+  constexpr int IT = kC / (4 * RPW);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const uint16_t* src = static_cast<const uint16_t*>(w ? d_.q : d_.k);
+    const uint16_t* src = static_cast<const uint16_t*>(w ? d_.q : d_.k) +
+                          (((size_t)b * d_.seqlen + t0) * d_.nkheads + kh) * N;
+    uint4 raw[IT];
+    const int u = lane % LPR, row0 = warp * RPW + lane / LPR;
 #pragma unroll
-    for (int it = 0; it < kC / (4 * RPW); ++it) {
-      const int row = it * 4 * RPW + warp * RPW + lane / LPR, u = lane % LPR;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (row < valid)
-        raw = *reinterpret_cast<const uint4*>(
-            src + (((size_t)b * d_.seqlen + t0 + row) * d_.nkheads + kh) * N + u * 8);
-      float f[8];
-      unpack8(raw, f);
-      float m = 0.f, ss = 0.f;
+    for (int it = 0; it < IT; ++it) {
+      const int row = it * 4 * RPW + row0;
+      raw[it] = row < valid ? *reinterpret_cast<const uint4*>(src + (size_t)row * d_.nkheads * N + u * 8)
+                            : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m = fmaxf(m, fabsf(f[i]));
-        ss = fmaf(f[i], f[i], ss);
+    for (int it = 0; it < IT; ++it) {
+      const int row = it * 4 * RPW + row0;
+      const uint32_t r4[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+      uint32_t m2 = 0;  // magnitudes of bf16 pairs order like integers
+      float2 s2 = make_float2(0.f, 0.f), f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m2 = __vmaxu2(m2, r4[i] & 0x7FFF7FFFu);
+        f[i] = make_float2(bf16_lo(r4[i]), bf16_hi(r4[i]));
+        s2 = fma2(f[i], f[i], s2);
       }
+      float ss = s2.x + s2.y;
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
       }
       // s = 2^-e brings the largest magnitude to [1, 2); its inverse goes into kmul
-      uint32_t e = exponent_of(m);
+      uint32_t e = max(m2 & 0xFFFFu, m2 >> 16) >> 7;
       e = e < 1u ? 1u : (e > 253u ? 253u : e);
       const float s = __uint_as_float((254u - e) << 23), inv = __uint_as_float(e << 23);
       uint4 out;
       uint32_t* o4 = &out.x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o4[i] = h2_bits(__floats2half2_rn(f[2 * i] * s, f[2 * i + 1] * s));
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = mul2(f[i], make_float2(s, s));
+        o4[i] = h2_bits(__floats2half2_rn(v.x, v.y));
+      }
       const uint32_t at = swz<RB>(row, u);
       *reinterpret_cast<uint4*>(tiles + w * Sm::kTile + at) = out;
       if (sub == 0) *reinterpret_cast<uint4*>(kq_out + w * Sm::kTile + at) = out;
@@ -172,14 +175,13 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
   }
 
   // ---- gates: two warps per head, one token per thread
-  const int hl = warp >> 1;                    // head of this half of the CTA
-  const int h = kh * rep + sub * kHeads + hl;  // may lie past the group's end
   const int nh = min(kHeads, rep - sub * kHeads);
-  {
-    const int i = tid & 63;
+  for (int x0 = 0; x0 < nh; x0 += 2) {
+    const int x = x0 + (warp >> 1), i = tid & 63;
     double g = 0.0;
     float beta = 0.f;
-    if (hl < nh && i < valid) {
+    if (x < nh && i < valid) {
+      const int h = kh * rep + sub * kHeads + x;
       const size_t at = ((size_t)b * d_.seqlen + t0 + i) * d_.nheads + h;
       const float raw = bf16_to_f32(static_cast<const uint16_t*>(d_.dt)[at]) +
                         (d_.dt_bias ? d_.dt_bias[h] : 0.f);
@@ -193,25 +195,29 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       const double up = __shfl_up_sync(0xffffffffu, g, o);
       if (lane >= o) g += up;
     }
-    if ((warp & 1) == 0 && lane == 31) carry[hl] = g;
+    if ((warp & 1) == 0 && lane == 31) carry[warp >> 1] = g;
     __syncthreads();
-    if (warp & 1) g += carry[hl];
-    float* sc = scal + hl * (kDeltaScalBwd / 4);
+    if (warp & 1) g += carry[warp >> 1];
+    float* sc = scal + (x < nh ? x : 0) * (kDeltaScalBwd / 4);
     const float hi = (float)g;
-    sc[kScGhi * kC + i] = hi;
-    sc[kScGlo * kC + i] = (float)(g - (double)hi);
-    sc[kScBeta * kC + i] = beta;
+    if (x < nh) {
+      sc[kScGhi * kC + i] = hi;
+      sc[kScGlo * kC + i] = (float)(g - (double)hi);
+      sc[kScBeta * kC + i] = beta;
+    }
     __syncthreads();
-    const float ehi = sc[kScGhi * kC + kC - 1], elo = sc[kScGlo * kC + kC - 1];
-    const float lo = sc[kScGlo * kC + i];
-    const float D = ex2_approx(hi + lo), E = ex2_approx((ehi - hi) + (elo - lo));
-    sc[kScSk * kC + i] = D * tok[i];
-    sc[kScKend * kC + i] = tok[i] * E;
-    sc[kScK * kC + i] = tok[i];
-    sc[kScSq * kC + i] = D * tok[kC + i];
-    sc[kScEnd * kC + i] = ex2_approx(ehi + elo);
-    sc[kScKn * kC + i] = tok[2 * kC + i];
-    sc[kScQn * kC + i] = tok[3 * kC + i];
+    if (x < nh) {
+      const float ehi = sc[kScGhi * kC + kC - 1], elo = sc[kScGlo * kC + kC - 1];
+      const float lo = sc[kScGlo * kC + i];
+      const float D = ex2_approx(hi + lo), E = ex2_approx((ehi - hi) + (elo - lo));
+      sc[kScSk * kC + i] = D * tok[i];
+      sc[kScKend * kC + i] = tok[i] * E;
+      sc[kScK * kC + i] = tok[i];
+      sc[kScSq * kC + i] = D * tok[kC + i];
+      sc[kScEnd * kC + i] = ex2_approx(ehi + elo);
+      sc[kScKn * kC + i] = tok[2 * kC + i];
+      sc[kScQn * kC + i] = tok[3 * kC + i];
+    }
   }
 
   // ---- k k^T and q k^T: warp w takes rows 16 w .. 16 w + 15, columns up to them
@@ -245,6 +251,18 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
     const float gh1 = sc[kScGhi * kC + r1], gl1 = sc[kScGlo * kC + r1];
     const float km0 = tok[r0], km1 = tok[r1];
 
+    // ---- column factors of the row blocks 1 .. 3, and each row's own
+    for (int i = tid; i < 3 * kC; i += kThreads) {
+      const int I = i / kC + 1, j = i & (kC - 1);
+      const float f = ex2_approx((sc[kScGhi * kC + 16 * I] - sc[kScGhi * kC + j]) +
+                                 (sc[kScGlo * kC + 16 * I] - sc[kScGlo * kC + j]));
+      cols[(I - 1) * 2 * kC + j] = f;
+      cols[((I - 1) * 2 + 1) * kC + j] = f * tok[j] * sc[kScBeta * kC + j];
+    }
+    const float a0 = ex2_approx((gh0 - sc[kScGhi * kC + 16 * warp]) + (gl0 - sc[kScGlo * kC + 16 * warp]));
+    const float a1 = ex2_approx((gh1 - sc[kScGhi * kC + 16 * warp]) + (gl1 - sc[kScGlo * kC + 16 * warp]));
+    __syncthreads();
+
     // ---- L = M diag(beta) and P on the warp's 16 rows
     float pv[8][4];
 #pragma unroll
@@ -253,20 +271,33 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       for (int q = 0; q < 4; ++q) pv[j][q] = 0.f;
       if (j > 2 * warp + 1) continue;
       const int col = 8 * j + 2 * (lane & 3);
-      const float2 ch = *reinterpret_cast<const float2*>(sc + kScGhi * kC + col);
-      const float2 cl = *reinterpret_cast<const float2*>(sc + kScGlo * kC + col);
-      const float2 cb = *reinterpret_cast<const float2*>(sc + kScBeta * kC + col);
-      const float2 ck = *reinterpret_cast<const float2*>(tok + col);
       float lv[4];
+      if (j < 2 * warp) {
+        const float2 cp = *reinterpret_cast<const float2*>(cols + (warp - 1) * 2 * kC + col);
+        const float2 cl = *reinterpret_cast<const float2*>(cols + ((warp - 1) * 2 + 1) * kC + col);
+        pv[j][0] = qk[j][0] * cp.x * a0;
+        pv[j][1] = qk[j][1] * cp.y * a0;
+        pv[j][2] = qk[j][2] * cp.x * a1;
+        pv[j][3] = qk[j][3] * cp.y * a1;
+        lv[0] = kk[j][0] * cl.x * (a0 * km0);
+        lv[1] = kk[j][1] * cl.y * (a0 * km0);
+        lv[2] = kk[j][2] * cl.x * (a1 * km1);
+        lv[3] = kk[j][3] * cl.y * (a1 * km1);
+      } else {
+        const float2 ch = *reinterpret_cast<const float2*>(sc + kScGhi * kC + col);
+        const float2 cl = *reinterpret_cast<const float2*>(sc + kScGlo * kC + col);
+        const float2 cb = *reinterpret_cast<const float2*>(sc + kScBeta * kC + col);
+        const float2 ck = *reinterpret_cast<const float2*>(tok + col);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int cc = col + (q & 1), row = q < 2 ? r0 : r1;
-        const float gm = ex2_approx(((q < 2 ? gh0 : gh1) - ((q & 1) ? ch.y : ch.x)) +
-                                    ((q < 2 ? gl0 : gl1) - ((q & 1) ? cl.y : cl.x)));
-        if (cc <= row) pv[j][q] = qk[j][q] * gm;
-        lv[q] = cc < row ? kk[j][q] * gm * (q < 2 ? km0 : km1) *
-                               ((q & 1) ? ck.y * cb.y : ck.x * cb.x)
-                         : 0.f;
+        for (int q = 0; q < 4; ++q) {
+          const int cc = col + (q & 1), row = q < 2 ? r0 : r1;
+          const float gm = ex2_approx(((q < 2 ? gh0 : gh1) - ((q & 1) ? ch.y : ch.x)) +
+                                      ((q < 2 ? gl0 : gl1) - ((q & 1) ? cl.y : cl.x)));
+          if (cc <= row) pv[j][q] = qk[j][q] * gm;
+          lv[q] = cc < row ? kk[j][q] * gm * (q < 2 ? km0 : km1) *
+                                 ((q & 1) ? ck.y * cb.y : ck.x * cb.x)
+                           : 0.f;
+        }
       }
       *reinterpret_cast<float2*>(L + r0 * kLs + col) = make_float2(lv[0], lv[1]);
       *reinterpret_cast<float2*>(L + r1 * kLs + col) = make_float2(lv[2], lv[3]);
@@ -288,11 +319,6 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
         *reinterpret_cast<uint32_t*>(ph + kDeltaTri + a0) = lo0;
         *reinterpret_cast<uint32_t*>(ph + kDeltaTri + a1) = lo1;
       }
-    }
-    // blocks (0, 1) and (2, 3) are read as part of T's 32 x 32 diagonal blocks
-    if (!(warp & 1)) {
-      const float d0[2][4] = {};
-      block_store(d0, L + warp * 16 * kLs + (warp + 1) * 16, 1.f, lane);
     }
     if ((lane & 3) == 0) {
       sc[kScP * kC + r0] = tok[kC + r0] * s0.inv;
@@ -331,22 +357,22 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
     float d[2][4];
     if (warp & 1) {
       float* Lo = L + (warp * 16) * kLs + (warp - 1) * 16;
-      block_product<1>(d, Lo, L + (warp - 1) * 16 * kLs + (warp - 1) * 16, lane);
+      block_product(d, Lo, L + (warp - 1) * 16 * kLs + (warp - 1) * 16, 0, 16, lane);
       __syncwarp();
       block_store(d, Lo, 1.f, lane);
       __syncwarp();
-      block_product<1>(d, L + (warp * 16) * kLs + warp * 16, Lo, lane);
+      block_product(d, L + (warp * 16) * kLs + warp * 16, Lo, 0, 16, lane);
       __syncwarp();
       block_store(d, Lo, -1.f, lane);
     }
     __syncthreads();
     const int bi = warp >> 1, bj = warp & 1;  // this warp's 16 x 16 of the 32 x 32 block
     float* Lba = L + 32 * kLs;
-    block_product<2>(d, Lba + bi * 16 * kLs, L + bj * 16, lane);
+    block_product(d, Lba + bi * 16 * kLs, L + bj * 16, bj * 16, 32, lane);  // T_01 = 0
     __syncthreads();
     block_store(d, Lba + bi * 16 * kLs + bj * 16, 1.f, lane);
     __syncthreads();
-    block_product<2>(d, L + (32 + bi * 16) * kLs + 32, Lba + bj * 16, lane);
+    block_product(d, L + (32 + bi * 16) * kLs + 32, Lba + bj * 16, 0, 16 * bi + 16, lane);
     __syncthreads();
     block_store(d, Lba + bi * 16 * kLs + bj * 16, -1.f, lane);
     __syncthreads();
