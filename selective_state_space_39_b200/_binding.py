@@ -587,25 +587,65 @@ def ssm_ssd_state_update(state, x, dt, A, B, C, D=None, dt_bias=None, softplus=T
 
 
 
+# The calls below are made once per layer and generated token, so their checks
+# are kept to one test per tensor; what is wrong with one is found afterwards.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _at(t, name, dtype, shape, dev):
+    """The pointer of a tensor that is as it must be, or _ptr's error."""
+    if t is None:
+        return None
+    try:
+        if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, name, dtype, shape, dev)
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return dev
+
+
+def _stream_of(stream, dev):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return _stream_ptr(stream, dev)
+
+
+def _on(dev, fn, *args):
+    """fn(*args) with dev current."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _delta_sizes(q, v, tokens):
     """(batch, L, heads, key heads, headdim, dstate) of v (batch[, L], heads,
     headdim) and q (batch[, L], key heads, dstate)."""
-    if q.dim() != 3 + tokens or v.dim() != 3 + tokens:
+    vs, qs = v.shape, q.shape
+    if len(qs) != 3 + tokens or len(vs) != 3 + tokens:
         raise ValueError("q and v must be (batch, seqlen, heads, width)" if tokens
                          else "q and v must be (batch, heads, width)")
-    L = v.shape[1] if tokens else 1
-    return v.shape[0], L, v.shape[-2], q.shape[-2], v.shape[-1], q.shape[-1]
+    return vs[0], vs[1] if tokens else 1, vs[-2], qs[-2], vs[-1], qs[-1]
 
 
-def _delta_inputs(q, k, v, dt, A, beta, dt_bias, tokens):
+def _delta_inputs(sizes, dev, q, k, v, dt, A, beta, dt_bias, tokens):
     """Checked pointers of a gated delta rule call's inputs, in the C order."""
-    B, L, H, Hk, P, N = _delta_sizes(q, v, tokens)
-    dev = v.device
-    bl = (B, L) if tokens else (B,)
-    return [_ptr(q, "q", v.dtype, bl + (Hk, N), dev), _ptr(k, "k", v.dtype, bl + (Hk, N), dev),
-            _ptr(v, "v", v.dtype, bl + (H, P)), _ptr(dt, "dt", v.dtype, bl + (H,), dev),
-            _ptr(A, "A", torch.float32, (H,), dev), _ptr(beta, "beta", v.dtype, bl + (H,), dev),
-            _ptr(dt_bias, "dt_bias", torch.float32, (H,), dev)]
+    B, L, H, Hk, P, N = sizes
+    ty = v.dtype
+    f32 = torch.float32
+    qk, gate = ((B, L, Hk, N), (B, L, H)) if tokens else ((B, Hk, N), (B, H))
+    return (_at(q, "q", ty, qk, dev), _at(k, "k", ty, qk, dev), _at(v, "v", ty, v.shape, dev),
+            _at(dt, "dt", ty, gate, dev), _at(A, "A", f32, (H,), dev),
+            _at(beta, "beta", ty, gate, dev), _at(dt_bias, "dt_bias", f32, (H,), dev))
 
 
 def gated_delta_workspace_bytes(batch, seqlen, nheads, nkheads, headdim, dstate,
@@ -629,28 +669,25 @@ def ssm_gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, softplus=True, beta_
     dt_bias (heads,), h0 (batch, heads, headdim, dstate) float32. ``scale``
     defaults to dstate ** -0.5. Returns (y, h_last); h_last is None when not
     requested, and may be given (it may be h0)."""
+    dev = _cuda_device(v, "v")
     sizes = _delta_sizes(q, v, True)
     B, L, H, Hk, P, N = sizes
-    dev = v.device
-    io = _io_code(v.dtype)
-    ins = _delta_inputs(q, k, v, dt, A, beta, dt_bias, True)
-    ph0 = _ptr(h0, "h0", torch.float32, (B, H, P, N), dev)
+    io, st, f32 = _io_code(v.dtype), (B, H, P, N), torch.float32
+    ins = _delta_inputs(sizes, dev, q, k, v, dt, A, beta, dt_bias, True)
+    ph0 = _at(h0, "h0", f32, st, dev)
     if y is None:
-        y = torch.empty((B, L, H, P), dtype=v.dtype, device=dev)
-    py = _ptr(y, "y", v.dtype, (B, L, H, P), dev)
+        y = torch.empty_like(v)
     if h_last is None and return_last_state:
-        h_last = torch.empty((B, H, P, N), dtype=torch.float32, device=dev)
-    ph = _ptr(h_last, "h_last", torch.float32, (B, H, P, N), dev)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = gated_delta_workspace_bytes(*sizes, v.dtype)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        pws = _ptr(workspace, "workspace", None, None, dev)
-        rc = lib().ssm_gated_delta_fwd(*sizes, io, *ins, 1 if softplus else 0,
-                                       1 if beta_sigmoid else 0, 1 if qk_norm else 0,
-                                       N ** -0.5 if scale is None else scale, ph0, py, ph, pws,
-                                       workspace.numel() * workspace.element_size(),
-                                       _stream_ptr(stream, dev))
+        h_last = torch.empty(st, dtype=f32, device=dev)
+    if workspace is None:
+        need = _on(dev, lib().ssm_gated_delta_workspace_bytes, *sizes, io)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    rc = _on(dev, lib().ssm_gated_delta_fwd, *sizes, io, *ins, 1 if softplus else 0,
+             1 if beta_sigmoid else 0, 1 if qk_norm else 0, N ** -0.5 if scale is None else scale,
+             ph0, _at(y, "y", v.dtype, v.shape, dev), _at(h_last, "h_last", f32, st, dev),
+             _ptr(workspace, "workspace", None, None, dev),
+             workspace.numel() * workspace.element_size() if workspace is not None else 0,
+             _stream_of(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_gated_delta_fwd", with_detail=True)
     return y, h_last
@@ -662,19 +699,16 @@ def ssm_gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, softplus=T
     of libssmscan.so: updates the float32 state (batch, heads, headdim, dstate)
     in place and returns y (batch, heads, headdim) in v's dtype; q, k (batch,
     key heads, dstate), v (batch, heads, headdim), dt, beta (batch, heads)."""
-    B, _, H, Hk, P, N = _delta_sizes(q, v, False)
-    dev = v.device
-    ins = _delta_inputs(q, k, v, dt, A, beta, dt_bias, False)
-    ps = _ptr(state, "state", torch.float32, (B, H, P, N), dev)
+    dev = _cuda_device(v, "v")
+    sizes = _delta_sizes(q, v, False)
+    B, _, H, Hk, P, N = sizes
+    ins = _delta_inputs(sizes, dev, q, k, v, dt, A, beta, dt_bias, False)
     if y is None:
-        y = torch.empty((B, H, P), dtype=v.dtype, device=dev)
-    py = _ptr(y, "y", v.dtype, (B, H, P), dev)
-    with torch.cuda.device(dev):
-        rc = lib().ssm_gated_delta_update(B, H, Hk, P, N, _io_code(v.dtype), ps, *ins,
-                                          1 if softplus else 0, 1 if beta_sigmoid else 0,
-                                          1 if qk_norm else 0,
-                                          N ** -0.5 if scale is None else scale, py,
-                                          _stream_ptr(stream, dev))
+        y = torch.empty_like(v)
+    rc = _on(dev, lib().ssm_gated_delta_update, B, H, Hk, P, N, _io_code(v.dtype),
+             _at(state, "state", torch.float32, (B, H, P, N), dev), *ins, 1 if softplus else 0,
+             1 if beta_sigmoid else 0, 1 if qk_norm else 0, N ** -0.5 if scale is None else scale,
+             _at(y, "y", v.dtype, v.shape, dev), _stream_of(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_gated_delta_update", with_detail=True)
     return y
@@ -688,31 +722,26 @@ def ssm_gated_delta_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, softplus=True, b
     ssm_gated_delta_fwd, dh_last may be None). Returns a dict: dq, dk, dv, ddt,
     dbeta in bfloat16, dA, ddt_bias (heads,) and dh0 in float32 (None when not
     asked for)."""
+    dev = _cuda_device(v, "v")
     sizes = _delta_sizes(q, v, True)
     B, L, H, Hk, P, N = sizes
-    dev = v.device
-    f32 = torch.float32
-    io = _io_code(v.dtype)
-    ins = _delta_inputs(q, k, v, dt, A, beta, dt_bias, True)
-    ph0 = _ptr(h0, "h0", f32, (B, H, P, N), dev)
-    pdy = _ptr(dy, "dy", v.dtype, (B, L, H, P), dev)
-    pdh = _ptr(dh_last, "dh_last", f32, (B, H, P, N), dev)
+    io, st, f32 = _io_code(v.dtype), (B, H, P, N), torch.float32
+    ins = _delta_inputs(sizes, dev, q, k, v, dt, A, beta, dt_bias, True)
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
          "ddt": torch.empty_like(dt), "dbeta": torch.empty_like(beta),
-         "dA": torch.empty((H,), dtype=f32, device=dev) if want_dA else None,
+         "dA": torch.empty_like(A) if want_dA else None,
          "ddt_bias": torch.empty((H,), dtype=f32, device=dev) if want_ddt_bias else None,
-         "dh0": torch.empty((B, H, P, N), dtype=f32, device=dev) if want_dh0 else None}
-    outs = [t.data_ptr() if t is not None else None for t in g.values()]
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = gated_delta_bwd_workspace_bytes(*sizes, v.dtype)
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        pws = _ptr(workspace, "workspace", None, None, dev)
-        rc = lib().ssm_gated_delta_bwd(*sizes, io, *ins, 1 if softplus else 0,
-                                       1 if beta_sigmoid else 0, 1 if qk_norm else 0,
-                                       N ** -0.5 if scale is None else scale, ph0, pdy, pdh,
-                                       *outs, pws, workspace.numel() * workspace.element_size(),
-                                       _stream_ptr(stream, dev))
+         "dh0": torch.empty(st, dtype=f32, device=dev) if want_dh0 else None}
+    if workspace is None:
+        need = _on(dev, lib().ssm_gated_delta_bwd_workspace_bytes, *sizes, io)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    rc = _on(dev, lib().ssm_gated_delta_bwd, *sizes, io, *ins, 1 if softplus else 0,
+             1 if beta_sigmoid else 0, 1 if qk_norm else 0, N ** -0.5 if scale is None else scale,
+             _at(h0, "h0", f32, st, dev), _at(dy, "dy", v.dtype, v.shape, dev),
+             _at(dh_last, "dh_last", f32, st, dev),
+             *[t.data_ptr() if t is not None else None for t in g.values()],
+             _ptr(workspace, "workspace", None, None, dev),
+             workspace.numel() * workspace.element_size(), _stream_of(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_gated_delta_bwd", with_detail=True)
     return g
@@ -731,11 +760,6 @@ def gated_norm_bwd_workspace_bytes(rows, dim, groups=1, dtype=torch.bfloat16) ->
     return int(lib().ssm_gated_norm_bwd_workspace_bytes(rows, dim, groups, _io_code(dtype)))
 
 
-def _norm_rows(x):
-    dim = x.shape[-1]
-    return (x.numel() // dim if dim else 0), dim
-
-
 def ssm_gated_norm_fwd(x, w, z=None, norm_before_gate=False, residual=None, residual_scale=1.0,
                        groups=1, eps=1e-5, y=None, h=None, stream=None):
     """The norm before and after a block through ssm_gated_norm_fwd of
@@ -744,27 +768,24 @@ def ssm_gated_norm_fwd(x, w, z=None, norm_before_gate=False, residual=None, resi
     after it (``norm_before_gate``), and residual + residual_scale * x in front
     of it (residual of x's shape, x's type or float32). Returns (y, h): h is
     the sum (``h`` may be given, and may be residual), or x without a residual."""
-    if x.dim() < 1:
+    dev = _cuda_device(x, "x")
+    shape, ty = x.shape, x.dtype
+    if not shape:
         raise ValueError("x must be (..., dim)")
-    rows, dim = _norm_rows(x)
-    dev, shape = x.device, tuple(x.shape)
-    px = _ptr(x, "x", x.dtype, shape)
-    pz = _ptr(z, "z", x.dtype, shape, dev)
-    pw = _ptr(w, "w", torch.float32, (dim,), dev)
-    pres = _ptr(residual, "residual", None, shape, dev)
-    rio = _io_code(residual.dtype if residual is not None else x.dtype)
+    dim = shape[-1]
+    rt = residual.dtype if residual is not None else ty
     if y is None:
         y = torch.empty_like(x)
-    py = _ptr(y, "y", x.dtype, shape, dev)
-    if residual is None and h is not None:
-        raise ValueError("h is an output only with a residual")
-    if residual is not None and h is None:
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is an output only with a residual")
+    elif h is None:
         h = torch.empty_like(residual)
-    ph = _ptr(h, "h", residual.dtype if residual is not None else None, shape, dev)
-    with torch.cuda.device(dev):
-        rc = lib().ssm_gated_norm_fwd(rows, dim, groups, _io_code(x.dtype), rio, px, pres,
-                                      residual_scale, pz, 1 if norm_before_gate else 0, pw, eps,
-                                      py, ph, _stream_ptr(stream, dev))
+    rc = _on(dev, lib().ssm_gated_norm_fwd, x.numel() // dim if dim else 0, dim, groups,
+             _io_code(ty), _io_code(rt), _at(x, "x", ty, shape, dev),
+             _at(residual, "residual", rt, shape, dev), residual_scale, _at(z, "z", ty, shape, dev),
+             1 if norm_before_gate else 0, _at(w, "w", torch.float32, (dim,), dev), eps,
+             _at(y, "y", ty, shape, dev), _at(h, "h", rt, shape, dev), _stream_of(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_gated_norm_fwd", with_detail=True)
     return y, (x if residual is None else h)
@@ -778,31 +799,28 @@ def ssm_gated_norm_bwd(h, w, dy, z=None, norm_before_gate=False, dh=None, residu
     a residual). ``residual``: whether there was one (dresidual is returned,
     and dx is residual_scale times it). Returns a dict: dx, dz (dy's type),
     dresidual (h's type), dw (dim,) float32; what does not apply is None."""
-    if h.dim() < 1:
+    dev = _cuda_device(h, "h")
+    shape, ht, ty = h.shape, h.dtype, dy.dtype
+    if not shape:
         raise ValueError("h must be (..., dim)")
-    if not residual and (h.dtype != dy.dtype or residual_scale != 1.0):
+    if not residual and (ht != ty or residual_scale != 1.0):
         raise ValueError("without a residual h has dy's type and residual_scale is 1")
-    rows, dim = _norm_rows(h)
-    dev, shape = h.device, tuple(h.shape)
-    ph = _ptr(h, "h", None, shape)
-    pw = _ptr(w, "w", torch.float32, (dim,), dev)
-    pdy = _ptr(dy, "dy", None, shape, dev)
-    pz = _ptr(z, "z", dy.dtype, shape, dev)
-    pdh = _ptr(dh, "dh", h.dtype, shape, dev)
+    dim = shape[-1]
+    rows, io = (h.numel() // dim if dim else 0), _io_code(ty)
     g = {"dx": torch.empty_like(dy), "dz": torch.empty_like(dy) if z is not None else None,
          "dresidual": torch.empty_like(h) if residual else None,
          "dw": torch.empty((dim,), dtype=torch.float32, device=dev) if want_dw else None}
-    P = {k: (v.data_ptr() if v is not None else None) for k, v in g.items()}
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = gated_norm_bwd_workspace_bytes(rows, dim, groups, dy.dtype) if want_dw else 0
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        pws = _ptr(workspace, "workspace", None, None, dev)
-        rc = lib().ssm_gated_norm_bwd(rows, dim, groups, _io_code(dy.dtype), _io_code(h.dtype), ph,
-                                      residual_scale, pz, 1 if norm_before_gate else 0, pw, eps,
-                                      pdy, pdh, P["dx"], P["dresidual"], P["dz"], P["dw"], pws,
-                                      workspace.numel() * workspace.element_size(),
-                                      _stream_ptr(stream, dev))
+    if workspace is None and want_dw:
+        need = lib().ssm_gated_norm_bwd_workspace_bytes(rows, dim, groups, io)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    P = [t.data_ptr() if t is not None else None for t in g.values()]
+    rc = _on(dev, lib().ssm_gated_norm_bwd, rows, dim, groups, io, _io_code(ht),
+             _at(h, "h", ht, shape, dev), residual_scale, _at(z, "z", ty, shape, dev),
+             1 if norm_before_gate else 0, _at(w, "w", torch.float32, (dim,), dev), eps,
+             _at(dy, "dy", ty, shape, dev), _at(dh, "dh", ht, shape, dev), P[0], P[2], P[1], P[3],
+             _ptr(workspace, "workspace", None, None, dev),
+             workspace.numel() * workspace.element_size() if workspace is not None else 0,
+             _stream_of(stream, dev))
     if rc != 0:
         raise SsmError(rc, "ssm_gated_norm_bwd", with_detail=True)
     return g

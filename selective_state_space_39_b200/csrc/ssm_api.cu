@@ -1300,7 +1300,7 @@ int ssm_gated_norm_fwd(int64_t rows, int64_t dim, int64_t groups, int io_dtype,
 size_t ssm_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups,
                                           int io_dtype) {
   if (norm_status(rows, dim, groups, io_dtype, SSM_DTYPE_F32) != SSM_OK || rows == 0) return 0;
-  return sizeof(float) * (size_t)norm_bwd_slices(rows, (int)dim, (int)groups) * dim;
+  return sizeof(float) * (size_t)norm_bwd_slices(rows, (int)groups) * dim;
 }
 
 int ssm_gated_norm_bwd(int64_t rows, int64_t dim, int64_t groups, int io_dtype, int h_dtype,

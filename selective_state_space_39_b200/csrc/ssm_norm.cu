@@ -9,16 +9,23 @@
 //   du = (t - n mean(t n)) / sqrt(mean(u^2) + eps),  dw = sum over rows of dn n
 //
 // One pass over the data: a group of T threads holds a row group in registers
-// (up to kMaxVecs units of 16 bytes of io per thread; longer rows are read
-// twice), sums the squares (backward: and t u) in fp32 by shuffles, and writes
-// the results. T is the power of two that leaves a thread about two units, so
-// rows of one head's width take 8 or 16 lanes and a warp holds several. dw is
-// summed in registers over the rows a block takes, in shared memory over its
-// row groups and over the blocks by a second kernel, always in the same order.
+// (up to four 16-byte units of io per thread; the backward pass of bf16 rows up
+// to two; longer rows are read twice), sums the squares (backward: and t u) in
+// fp32 by shuffles, and writes the results. T is the power of two that leaves a
+// thread one or two units, so rows of one head's width take 8 lanes and a warp
+// holds several. Rows that are no whole units, or lie off 16-byte boundaries,
+// are read two values per thread. The backward pass keeps 296 blocks, each
+// walking over its rows with the next row's loads in flight, sums dw in
+// registers over them, in shared memory over its row groups and over the
+// blocks by a second kernel, always in the same order.
 //
 // Bound: memory traffic (forward: x, z, residual in, y, h out; backward: h,
-// dy, z, dh in, dx, dz, dresidual out).
+// dy, z, dh in, dx, dz, dresidual out). Measured (CUDA graph): forward with an
+// fp32 residual, 16384 x 4096 bf16, 119 us = 6.8 TB/s; gated backward of
+// 131072 x 128 bf16, 39 us = 4.3 TB/s, the sigmoid and its derivative beside
+// the loads; 1000 x 1537 fp32 backward, 16 us, the latency of a few rows.
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm_device.cuh"
 #include "ssm_norm_internal.h"
@@ -29,48 +36,82 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// V values of type T as they lie in memory: 16-byte units, or (V = 2) two values
+// loaded one by one, the second only where `left`, the values up to the row's
+// end, has it.
 template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
-  if constexpr (V == 1) {
-    f[0] = Io<T>::load(p);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_lo(u[i]);
-      f[2 * i + 1] = bf16_hi(u[i]);
-    }
+struct Raw {
+  static constexpr int kWords = V == 2 ? 2 : V * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+};
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* p, int left) {
+  Raw<T, V> r;
+  if constexpr (V == 2) {
+    using W = std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t>;
+    r.w[0] = reinterpret_cast<const W*>(p)[0];
+    r.w[1] = left > 1 ? reinterpret_cast<const W*>(p)[1] : 0;
   } else {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + i);
-      f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
+    for (int i = 0; i < Raw<T, V>::kWords; i += 4) {
+      const uint4 v = *(reinterpret_cast<const uint4*>(p) + i / 4);
+      r.w[i] = v.x; r.w[i + 1] = v.y; r.w[i + 2] = v.z; r.w[i + 3] = v.w;
     }
   }
+  return r;
 }
-
+// Values are held as pairs for the packed fp32 instructions.
+template <int V>
+struct Pairs {
+  static constexpr int n = V / 2;
+  float2 f[n];
+};
 template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
-  if constexpr (V == 1) {
-    Io<T>::store(p, f[0]);
+__device__ __forceinline__ Pairs<V> unpack(const Raw<T, V>& r) {
+  Pairs<V> p;
+  if constexpr (V == 2) {
+    p.f[0] = sizeof(T) == 2 ? make_float2(bf16_lo(r.w[0]), bf16_lo(r.w[1]))
+                            : make_float2(__uint_as_float(r.w[0]), __uint_as_float(r.w[1]));
   } else if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) p.f[i] = make_float2(bf16_lo(r.w[i]), bf16_hi(r.w[i]));
   } else {
 #pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    for (int i = 0; i < V / 2; ++i)
+      p.f[i] = make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+  }
+  return p;
+}
+template <typename T, int V>
+__device__ __forceinline__ Pairs<V> load_pairs(const T* p, int left) {
+  return unpack<T, V>(load_raw<T, V>(p, left));
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T* p, const Pairs<V>& v, int left) {
+  if constexpr (V == 2) {
+    Io<T>::store(p, v.f[0].x);
+    if (left > 1) Io<T>::store(p + 1, v.f[0].y);
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16x2(v.f[0].x, v.f[0].y), pack_bf16x2(v.f[1].x, v.f[1].y),
+                   pack_bf16x2(v.f[2].x, v.f[2].y), pack_bf16x2(v.f[3].x, v.f[3].y));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; i += 2)
+      *reinterpret_cast<float4*>(p + 2 * i) =
+          make_float4(v.f[i].x, v.f[i].y, v.f[i + 1].x, v.f[i + 1].y);
   }
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // sigmoid: MUFU approximations for bf16 io (2^-22 relative), exact functions for fp32
 template <typename IOT>
-__device__ __forceinline__ float sigmoid(float z) {
+__device__ __forceinline__ float2 sigmoid(float2 z) {
   if constexpr (sizeof(IOT) == 2)
-    return rcp_approx(1.f + ex2_approx(-z * kLog2e));
+    return make_float2(rcp_approx(1.f + ex2_approx(-z.x * kLog2e)),
+                       rcp_approx(1.f + ex2_approx(-z.y * kLog2e)));
   else
-    return 1.f / (1.f + expf(-z));
+    return make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
 }
 
 // Sums over the T threads of a row group (T a power of two; above a warp
@@ -99,74 +140,87 @@ __device__ __forceinline__ void group_sum(float (&v)[K], int T, float* sh) {
   }
 }
 
-template <typename IOT, typename RT, int V, int M, bool FIT>
+template <typename IOT, typename RT, int V, int M, bool FIT, int GATE>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int T) {
   __shared__ float sh[32];
+  using P = Pairs<V>;
   const int per_block = blockDim.x / T, t = threadIdx.x % T;
   const int64_t total = p.rows * p.groups;
   const int64_t r_raw = (int64_t)blockIdx.x * per_block + threadIdx.x / T;
   const bool live = r_raw < total;
   const int64_t r = live ? r_raw : total - 1;
   const size_t base = (size_t)r * p.width;  // rows are contiguous, so their groups are too
-  const int wbase = (int)(r % p.groups) * p.width;
+  const int wbase = p.groups == 1 ? 0 : (int)(r % p.groups) * p.width;
   const IOT* x = static_cast<const IOT*>(p.x) + base;
   const RT* res = p.residual ? static_cast<const RT*>(p.residual) + base : nullptr;
-  const IOT* z = p.gate ? static_cast<const IOT*>(p.z) + base : nullptr;
+  const IOT* z = GATE ? static_cast<const IOT*>(p.z) + base : nullptr;
 
-  auto value = [&](int at, float(&u)[V], float(&g)[V], bool store) {
-    load_vec<IOT, V>(x + at, u);
+  // u (the normed value) and the gate's value where it comes last
+  auto value = [&](int at, const Raw<IOT, V>& xr, const Raw<RT, V>& rr, const Raw<IOT, V>& zr, P& u,
+                   P& g, bool store) {
+    u = unpack<IOT, V>(xr);
     if (res) {
-      float q[V];
-      load_vec<RT, V>(res + at, q);
+      const P q = unpack<RT, V>(rr);
 #pragma unroll
-      for (int i = 0; i < V; ++i) u[i] = fmaf(p.residual_scale, u[i], q[i]);
-      if (store && live) store_vec<RT, V>(static_cast<RT*>(p.h_out) + base + at, u);
+      for (int i = 0; i < P::n; ++i) u.f[i] = fma2(both(p.residual_scale), u.f[i], q.f[i]);
+      if (store && live) store_pairs<RT, V>(static_cast<RT*>(p.h_out) + base + at, u, p.width - at);
     }
-    if (p.gate) {
-      load_vec<IOT, V>(z + at, g);
+    if (GATE) {
+      g = unpack<IOT, V>(zr);
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] *= sigmoid<IOT>(g[i]);
-      if (p.gate == kGateFirst) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) u[i] *= g[i];
+      for (int i = 0; i < P::n; ++i) {
+        g.f[i] = mul2(g.f[i], sigmoid<IOT>(g.f[i]));
+        if (GATE == kGateFirst) u.f[i] = mul2(u.f[i], g.f[i]);
       }
     }
   };
+  auto square = [](const P& u, float2& s) {
+#pragma unroll
+    for (int i = 0; i < P::n; ++i) s = fma2(u.f[i], u.f[i], s);
+  };
 
-  float u[M][V], g[M][V];
-  float ss[1] = {0.f};
+  P u[M], g[M];
+  float2 s2 = make_float2(0.f, 0.f);
   if (FIT) {
+    Raw<IOT, V> xr[M], zr[M];
+    Raw<RT, V> rr[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       const int at = (m * T + t) * V;
       if (at >= p.width) break;
-      value(at, u[m], g[m], true);
+      xr[m] = load_raw<IOT, V>(x + at, p.width - at);
+      if (res) rr[m] = load_raw<RT, V>(res + at, p.width - at);
+      if (GATE) zr[m] = load_raw<IOT, V>(z + at, p.width - at);
     }
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      if ((m * T + t) * V >= p.width) break;
-#pragma unroll
-      for (int i = 0; i < V; ++i) ss[0] = fmaf(u[m][i], u[m][i], ss[0]);
+      const int at = (m * T + t) * V;
+      if (at >= p.width) break;
+      value(at, xr[m], rr[m], zr[m], u[m], g[m], true);
+      square(u[m], s2);
     }
   } else {
     for (int at = t * V; at < p.width; at += T * V) {
-      value(at, u[0], g[0], false);
-#pragma unroll
-      for (int i = 0; i < V; ++i) ss[0] = fmaf(u[0][i], u[0][i], ss[0]);
+      Raw<RT, V> rr;
+      Raw<IOT, V> zr;
+      if (res) rr = load_raw<RT, V>(res + at, p.width - at);
+      if (GATE) zr = load_raw<IOT, V>(z + at, p.width - at);
+      value(at, load_raw<IOT, V>(x + at, p.width - at), rr, zr, u[0], g[0], false);
+      square(u[0], s2);
     }
   }
+  float ss[1] = {s2.x + s2.y};
   group_sum<1>(ss, T, sh);
   const float inv = 1.f / sqrtf(ss[0] / (float)p.width + p.eps);
 
-  auto finish = [&](int at, float(&uu)[V], const float(&gg)[V]) {
-    float w[V];
-    load_vec<float, V>(p.w + wbase + at, w);
+  auto finish = [&](int at, P& uu, const P& gg) {
+    const P w = load_pairs<float, V>(p.w + wbase + at, p.width - at);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      uu[i] = uu[i] * inv * w[i];
-      if (p.gate == kGateLast) uu[i] *= gg[i];
+    for (int i = 0; i < P::n; ++i) {
+      uu.f[i] = mul2(mul2(uu.f[i], both(inv)), w.f[i]);
+      if (GATE == kGateLast) uu.f[i] = mul2(uu.f[i], gg.f[i]);
     }
-    if (live) store_vec<IOT, V>(static_cast<IOT*>(p.y) + base + at, uu);
+    if (live) store_pairs<IOT, V>(static_cast<IOT*>(p.y) + base + at, uu, p.width - at);
   };
   if (FIT) {
 #pragma unroll
@@ -177,128 +231,165 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int T
     }
   } else {
     for (int at = t * V; at < p.width; at += T * V) {
-      value(at, u[0], g[0], true);
+      Raw<RT, V> rr;
+      Raw<IOT, V> zr;
+      if (res) rr = load_raw<RT, V>(res + at, p.width - at);
+      if (GATE) zr = load_raw<IOT, V>(z + at, p.width - at);
+      value(at, load_raw<IOT, V>(x + at, p.width - at), rr, zr, u[0], g[0], true);
       finish(at, u[0], g[0]);
     }
   }
 }
 
-// Grid: (slices, groups). A block takes rows slice, slice + slices, ... of its
-// row slots in turn, so that a thread's columns stay the same.
-template <typename IOT, typename RT, int V, int M, bool FIT>
+// Grid: (slices, groups). A block takes row slots slice, slice + slices, ... in
+// turn, so that a thread's columns stay the same; the next rows' data are
+// loaded before the present ones are finished.
+template <typename IOT, typename RT, int V, int M, bool FIT, int GATE>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, int T) {
   extern __shared__ float dws[];  // dw sums of the block's row groups
   __shared__ float sh[64];
+  using P = Pairs<V>;
   const int per_block = blockDim.x / T, t = threadIdx.x % T, slot = threadIdx.x / T;
   const int group = blockIdx.y, wbase = group * p.width;
-  float acc[FIT ? M : 1][V];
+  P acc[FIT ? M : 1];
 #pragma unroll
   for (int m = 0; m < (FIT ? M : 1); ++m)
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[m][i] = 0.f;
+    for (int i = 0; i < P::n; ++i) acc[m].f[i] = make_float2(0.f, 0.f);
   if (!FIT && p.dw)
-    for (int i = threadIdx.x; i < p.width; i += blockDim.x) dws[i] = 0.f;
+    for (int i = threadIdx.x; i <= p.width; i += blockDim.x) dws[i] = 0.f;
+
+  struct Row {
+    Raw<RT, V> h;
+    Raw<IOT, V> dy, z;
+  };
+  auto load = [&](size_t base, int at, Row& r) {
+    r.h = load_raw<RT, V>(static_cast<const RT*>(p.h) + base + at, p.width - at);
+    r.dy = load_raw<IOT, V>(static_cast<const IOT*>(p.dy) + base + at, p.width - at);
+    if (GATE) r.z = load_raw<IOT, V>(static_cast<const IOT*>(p.z) + base + at, p.width - at);
+  };
+  // the gate's sigmoid; adds u^2 and t u
+  auto sums = [&](int at, const Row& r, P& sg, float2& uu, float2& tu) {
+    const P w = load_pairs<float, V>(p.w + wbase + at, p.width - at);
+    const P h = unpack<RT, V>(r.h), dn = unpack<IOT, V>(r.dy);
+    P z;
+    if (GATE) z = unpack<IOT, V>(r.z);
+#pragma unroll
+    for (int i = 0; i < P::n; ++i) {
+      float2 u = h.f[i], d = dn.f[i];
+      if (GATE) {
+        sg.f[i] = sigmoid<IOT>(z.f[i]);
+        const float2 g = mul2(z.f[i], sg.f[i]);
+        if (GATE == kGateFirst) u = mul2(u, g); else d = mul2(d, g);
+      }
+      uu = fma2(u, u, uu);
+      tu = fma2(mul2(d, w.f[i]), u, tu);
+    }
+  };
+  auto finish = [&](size_t base, int at, const Row& r, const P& sg, float inv, float c, bool live,
+                    P& sum) {
+    const P h = unpack<RT, V>(r.h), dy = unpack<IOT, V>(r.dy);
+    const P w = load_pairs<float, V>(p.w + wbase + at, p.width - at);
+    P extra, dh, dz, z;
+    if (GATE) z = unpack<IOT, V>(r.z);
+    if (p.dh) extra = load_pairs<RT, V>(static_cast<const RT*>(p.dh) + base + at, p.width - at);
+#pragma unroll
+    for (int i = 0; i < P::n; ++i) {
+      const float2 g = GATE ? mul2(z.f[i], sg.f[i]) : both(1.f);
+      const float2 u = GATE == kGateFirst ? mul2(h.f[i], g) : h.f[i];
+      const float2 dn = GATE == kGateLast ? mul2(dy.f[i], g) : dy.f[i];
+      const float2 n = mul2(u, both(inv));
+      const float2 du = mul2(both(inv), fma2(n, both(-c), mul2(dn, w.f[i])));
+      if (live) sum.f[i] = fma2(dn, n, sum.f[i]);
+      if (GATE) {
+        const float2 dg = GATE == kGateFirst ? mul2(du, h.f[i]) : mul2(mul2(dy.f[i], n), w.f[i]);
+        // SiLU'(z) = s (1 + z (1 - s))
+        const float2 one_s = fma2(sg.f[i], both(-1.f), both(1.f));
+        dz.f[i] = mul2(dg, mul2(sg.f[i], fma2(z.f[i], one_s, both(1.f))));
+      }
+      dh.f[i] = GATE == kGateFirst ? mul2(du, g) : du;
+      if (p.dh) dh.f[i] = add2(dh.f[i], extra.f[i]);
+    }
+    if (!live) return;
+    if (GATE) store_pairs<IOT, V>(static_cast<IOT*>(p.dz) + base + at, dz, p.width - at);
+    if (p.dresidual) store_pairs<RT, V>(static_cast<RT*>(p.dresidual) + base + at, dh, p.width - at);
+#pragma unroll
+    for (int i = 0; i < P::n; ++i) dh.f[i] = mul2(dh.f[i], both(p.residual_scale));
+    store_pairs<IOT, V>(static_cast<IOT*>(p.dx) + base + at, dh, p.width - at);
+  };
+  auto base_of = [&](int64_t r0) {
+    const int64_t r = r0 + slot < p.rows ? r0 + slot : p.rows - 1;
+    return ((size_t)r * p.groups + group) * p.width;
+  };
 
   const int64_t step = (int64_t)gridDim.x * per_block;
+  Row row[M];
+  if (FIT) {
+    const size_t base = base_of((int64_t)blockIdx.x * per_block);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int at = (m * T + t) * V;
+      if (at >= p.width) break;
+      load(base, at, row[m]);
+    }
+  }
   for (int64_t r0 = (int64_t)blockIdx.x * per_block; r0 < p.rows; r0 += step) {
     const bool live = r0 + slot < p.rows;
-    const int64_t r = live ? r0 + slot : p.rows - 1;
-    const size_t base = ((size_t)r * p.groups + group) * p.width;
-    const RT* h = static_cast<const RT*>(p.h) + base;
-    const IOT* dy = static_cast<const IOT*>(p.dy) + base;
-    const IOT* z = p.gate ? static_cast<const IOT*>(p.z) + base : nullptr;
-
-    // u, t = dn w; sums of u^2 and t u
-    float ss[2] = {0.f, 0.f};
-    float hv[M][V], dv[M][V], zv[M][V];
-    auto sums = [&](int at, const float(&hh)[V], const float(&dd)[V], const float(&zz)[V]) {
-      float w[V];
-      load_vec<float, V>(p.w + wbase + at, w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float u = hh[i], dn = dd[i];
-        if (p.gate) {
-          const float g = zz[i] * sigmoid<IOT>(zz[i]);
-          if (p.gate == kGateFirst) u *= g; else dn *= g;
-        }
-        ss[0] = fmaf(u, u, ss[0]);
-        ss[1] = fmaf(dn * w[i], u, ss[1]);
-      }
-    };
-    auto fetch = [&](int at, float(&hh)[V], float(&dd)[V], float(&zz)[V]) {
-      load_vec<RT, V>(h + at, hh);
-      load_vec<IOT, V>(dy + at, dd);
-      if (p.gate) load_vec<IOT, V>(z + at, zz);
-    };
+    const size_t base = base_of(r0);
+    float2 uu = make_float2(0.f, 0.f), tu = uu;
+    P sg[M];
     if (FIT) {
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         const int at = (m * T + t) * V;
         if (at >= p.width) break;
-        fetch(at, hv[m], dv[m], zv[m]);
-      }
-#pragma unroll
-      for (int m = 0; m < M; ++m) {
-        const int at = (m * T + t) * V;
-        if (at >= p.width) break;
-        sums(at, hv[m], dv[m], zv[m]);
+        sums(at, row[m], sg[m], uu, tu);
       }
     } else {
       for (int at = t * V; at < p.width; at += T * V) {
-        fetch(at, hv[0], dv[0], zv[0]);
-        sums(at, hv[0], dv[0], zv[0]);
+        load(base, at, row[0]);
+        sums(at, row[0], sg[0], uu, tu);
       }
     }
+    Row next[M];
+    if (FIT && r0 + step < p.rows) {
+      const size_t nb = base_of(r0 + step);
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int at = (m * T + t) * V;
+        if (at >= p.width) break;
+        load(nb, at, next[m]);
+      }
+    }
+    float ss[2] = {uu.x + uu.y, tu.x + tu.y};
     group_sum<2>(ss, T, sh);
     const float inv = 1.f / sqrtf(ss[0] / (float)p.width + p.eps);
     const float c = ss[1] * inv / (float)p.width;  // mean(t n)
-
-    auto finish = [&](int at, const float(&hh)[V], const float(&dd)[V], const float(&zz)[V],
-                      float(&sum)[V]) {
-      float w[V], dh[V], dzv[V], extra[V];
-      load_vec<float, V>(p.w + wbase + at, w);
-      if (p.dh) load_vec<RT, V>(static_cast<const RT*>(p.dh) + base + at, extra);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float sg = 0.f, g = 1.f;
-        if (p.gate) {
-          sg = sigmoid<IOT>(zz[i]);
-          g = zz[i] * sg;
-        }
-        const float u = p.gate == kGateFirst ? hh[i] * g : hh[i];
-        const float dn = p.gate == kGateLast ? dd[i] * g : dd[i];
-        const float n = u * inv;
-        const float du = inv * (dn * w[i] - n * c);
-        if (live) sum[i] = fmaf(dn, n, sum[i]);
-        const float dg = p.gate == kGateFirst ? du * hh[i] : dd[i] * n * w[i];
-        dzv[i] = dg * sg * (1.f + zz[i] * (1.f - sg));
-        dh[i] = p.gate == kGateFirst ? du * g : du;
-        if (p.dh) dh[i] += extra[i];
-      }
-      if (!live) return;
-      if (p.gate) store_vec<IOT, V>(static_cast<IOT*>(p.dz) + base + at, dzv);
-      if (p.dresidual) store_vec<RT, V>(static_cast<RT*>(p.dresidual) + base + at, dh);
-#pragma unroll
-      for (int i = 0; i < V; ++i) dh[i] *= p.residual_scale;
-      store_vec<IOT, V>(static_cast<IOT*>(p.dx) + base + at, dh);
-    };
     if (FIT) {
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         const int at = (m * T + t) * V;
         if (at >= p.width) break;
-        finish(at, hv[m], dv[m], zv[m], acc[m]);
+        finish(base, at, row[m], sg[m], inv, c, live, acc[m]);
+        row[m] = next[m];
       }
     } else {  // one row at a time (T = the block): the columns' sums live in shared memory
       for (int at = t * V; at < p.width; at += T * V) {
-        fetch(at, hv[0], dv[0], zv[0]);
-        float sum[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] = p.dw ? dws[at + i] : 0.f;
-        finish(at, hv[0], dv[0], zv[0], sum);
+        load(base, at, row[0]);
+        float2 a = make_float2(0.f, 0.f), b = a;
+        sums(at, row[0], sg[0], a, b);
         if (p.dw) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) dws[at + i] = sum[i];
+          for (int i = 0; i < P::n; ++i)
+            acc[0].f[i] = make_float2(dws[at + 2 * i], dws[at + 2 * i + 1]);
+        }
+        finish(base, at, row[0], sg[0], inv, c, live, acc[0]);
+        if (p.dw) {
+#pragma unroll
+          for (int i = 0; i < P::n; ++i) {
+            dws[at + 2 * i] = acc[0].f[i].x;
+            dws[at + 2 * i + 1] = acc[0].f[i].y;
+          }
         }
       }
     }
@@ -311,7 +402,10 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, int T
       const int at = (m * T + t) * V;
       if (at >= p.width) break;
 #pragma unroll
-      for (int i = 0; i < V; ++i) dws[slot * p.width + at + i] = acc[m][i];
+      for (int i = 0; i < P::n; ++i) {
+        dws[slot * p.width + at + 2 * i] = acc[m].f[i].x;
+        if (at + 2 * i + 1 < p.width) dws[slot * p.width + at + 2 * i + 1] = acc[m].f[i].y;
+      }
     }
   }
   __syncthreads();
@@ -322,23 +416,22 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, int T
   }
 }
 
-// dw: 32 columns per block, the slices' sums by 8 warps in a fixed order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* part, int slices, int dim,
-                                                      float* dw) {
-  __shared__ float sh[8][33];
+// dw: 32 columns per block, the slices' sums by 32 warps in a fixed order.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int slices, int dim,
+                                                       float* dw) {
+  __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (col < dim) {
-#pragma unroll 4
-    for (int i = warp; i < slices; i += 8) s += part[(size_t)i * dim + col];
+#pragma unroll 8
+    for (int i = warp; i < slices; i += 32) s += part[(size_t)i * dim + col];
   }
   sh[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < dim) {
+  s = sh[lane][warp];  // column `warp` of the block, summed across the lanes
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sh[i][lane];
-    dw[col] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < dim) dw[blockIdx.x * 32 + warp] = s;
 }
 
 struct Shape {
@@ -346,7 +439,7 @@ struct Shape {
 };
 Shape shape(const NormParams& p, int types, bool vec, int max_m) {
   Shape s;
-  s.V = vec ? (types == 2 ? 4 : 8) : 1;
+  s.V = vec ? (types == 2 ? 4 : 8) : 2;
   const int units = (p.width + s.V - 1) / s.V;
   s.T = 8;
   while (s.T < 512 && s.T * 2 < units) s.T *= 2;
@@ -356,23 +449,23 @@ Shape shape(const NormParams& p, int types, bool vec, int max_m) {
   return s;
 }
 
-template <typename IOT, typename RT, int V>
+template <typename IOT, typename RT, int V, int GATE>
 cudaError_t fwd_m(const NormParams& p, const Shape& s, cudaStream_t stream) {
   const int64_t per = s.threads / s.T, blocks = (p.rows * p.groups + per - 1) / per;
   const unsigned g = (unsigned)blocks;
   switch (s.M) {
-    case 1: norm_fwd_kernel<IOT, RT, V, 1, true><<<g, s.threads, 0, stream>>>(p, s.T); break;
-    case 2: norm_fwd_kernel<IOT, RT, V, 2, true><<<g, s.threads, 0, stream>>>(p, s.T); break;
-    case 4: norm_fwd_kernel<IOT, RT, V, 4, true><<<g, s.threads, 0, stream>>>(p, s.T); break;
-    default: norm_fwd_kernel<IOT, RT, V, 1, false><<<g, s.threads, 0, stream>>>(p, s.T); break;
+    case 1: norm_fwd_kernel<IOT, RT, V, 1, true, GATE><<<g, s.threads, 0, stream>>>(p, s.T); break;
+    case 2: norm_fwd_kernel<IOT, RT, V, 2, true, GATE><<<g, s.threads, 0, stream>>>(p, s.T); break;
+    case 4: norm_fwd_kernel<IOT, RT, V, 4, true, GATE><<<g, s.threads, 0, stream>>>(p, s.T); break;
+    default: norm_fwd_kernel<IOT, RT, V, 1, false, GATE><<<g, s.threads, 0, stream>>>(p, s.T); break;
   }
   return cudaGetLastError();
 }
 
 template <typename K>
 cudaError_t run_bwd(K* kern, const NormParams& p, const Shape& s, cudaStream_t stream) {
-  const int slices = norm_bwd_slices(p.rows, p.dim, p.groups);
-  const size_t bytes = p.dw ? (size_t)(s.M ? s.threads / s.T : 1) * p.width * 4 : 0;
+  const int slices = norm_bwd_slices(p.rows, p.groups);
+  const size_t bytes = p.dw ? ((size_t)(s.M ? s.threads / s.T : 1) * p.width + 1) * 4 : 0;
   if (bytes > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -381,46 +474,65 @@ cudaError_t run_bwd(K* kern, const NormParams& p, const Shape& s, cudaStream_t s
   kern<<<dim3(slices, p.groups), s.threads, bytes, stream>>>(p, s.T);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.dw) return e;
-  norm_dw_kernel<<<(p.dim + 31) / 32, 256, 0, stream>>>(p.ws, slices, p.dim, p.dw);
+  norm_dw_kernel<<<(p.dim + 31) / 32, 1024, 0, stream>>>(p.ws, slices, p.dim, p.dw);
   return cudaGetLastError();
 }
 
-template <typename IOT, typename RT, int V>
+template <typename IOT, typename RT, int V, int GATE>
 cudaError_t bwd_m(const NormParams& p, const Shape& s, cudaStream_t stream) {
   switch (s.M) {
-    case 1: return run_bwd(norm_bwd_kernel<IOT, RT, V, 1, true>, p, s, stream);
-    case 2: return run_bwd(norm_bwd_kernel<IOT, RT, V, 2, true>, p, s, stream);
-    case 4: return run_bwd(norm_bwd_kernel<IOT, RT, V, 4, true>, p, s, stream);
+    case 1: return run_bwd(norm_bwd_kernel<IOT, RT, V, 1, true, GATE>, p, s, stream);
+    case 2: return run_bwd(norm_bwd_kernel<IOT, RT, V, 2, true, GATE>, p, s, stream);
+    case 4:
+      // four units of eight values and their gradients do not fit the registers
+      if constexpr (V < 8) return run_bwd(norm_bwd_kernel<IOT, RT, V, 4, true, GATE>, p, s, stream);
+      [[fallthrough]];
     default: {
       Shape one = s;
-      one.T = one.threads = 512;  // one row per block
-      return run_bwd(norm_bwd_kernel<IOT, RT, V, 1, false>, p, one, stream);
+      one.M = 0;
+      one.T = one.threads = 512;  // one row per block, read twice
+      return run_bwd(norm_bwd_kernel<IOT, RT, V, 1, false, GATE>, p, one, stream);
     }
   }
 }
 
+template <bool BWD, typename IOT, typename RT, int V>
+cudaError_t gated(const NormParams& p, const Shape& s, cudaStream_t st) {
+  switch (p.gate) {
+    case kGateFirst:
+      return BWD ? bwd_m<IOT, RT, V, kGateFirst>(p, s, st) : fwd_m<IOT, RT, V, kGateFirst>(p, s, st);
+    case kGateLast:
+      return BWD ? bwd_m<IOT, RT, V, kGateLast>(p, s, st) : fwd_m<IOT, RT, V, kGateLast>(p, s, st);
+    default:
+      return BWD ? bwd_m<IOT, RT, V, kGateNone>(p, s, st) : fwd_m<IOT, RT, V, kGateNone>(p, s, st);
+  }
+}
+template <bool BWD>
+cudaError_t typed(const NormParams& p, int types, bool vec, cudaStream_t st) {
+  const Shape s = shape(p, types, vec, 4);
+  if (types == 2) return vec ? gated<BWD, float, float, 4>(p, s, st) : gated<BWD, float, float, 2>(p, s, st);
+  if (types == 1)
+    return vec ? gated<BWD, uint16_t, float, 8>(p, s, st) : gated<BWD, uint16_t, float, 2>(p, s, st);
+  return vec ? gated<BWD, uint16_t, uint16_t, 8>(p, s, st)
+             : gated<BWD, uint16_t, uint16_t, 2>(p, s, st);
+}
+
 }  // namespace
 
-int norm_bwd_slices(int64_t rows, int dim, int groups) {
-  // about eight blocks per SM over the groups, at least four rows a slice
-  const int64_t want = std::max<int64_t>(1, (148 * 8) / groups);
-  const int64_t most = std::max<int64_t>(1, rows / 4);
-  (void)dim;
+int norm_bwd_slices(int64_t rows, int groups) {
+  // two blocks per SM over the groups (131072 rows of 128, gated: 38.9 us; four
+  // 41.2, eight 46.8 us), at least two rows a slice
+  const int64_t want = std::max<int64_t>(1, (148 * 2) / groups);
+  const int64_t most = std::max<int64_t>(1, rows / 2);
   return (int)std::min<int64_t>(want, most);
 }
 
 cudaError_t launch_norm_fwd(const NormParams& p, int types, bool vec, cudaStream_t stream) {
-  const Shape s = shape(p, types, vec, 4);
-  if (types == 2) return vec ? fwd_m<float, float, 4>(p, s, stream) : fwd_m<float, float, 1>(p, s, stream);
-  if (types == 1) return vec ? fwd_m<uint16_t, float, 8>(p, s, stream) : fwd_m<uint16_t, float, 1>(p, s, stream);
-  return vec ? fwd_m<uint16_t, uint16_t, 8>(p, s, stream) : fwd_m<uint16_t, uint16_t, 1>(p, s, stream);
+  return typed<false>(p, types, vec, stream);
 }
 
 cudaError_t launch_norm_bwd(const NormParams& p, int types, bool vec, cudaStream_t stream) {
-  const Shape s = shape(p, types, vec, 4);
-  if (types == 2) return vec ? bwd_m<float, float, 4>(p, s, stream) : bwd_m<float, float, 1>(p, s, stream);
-  if (types == 1) return vec ? bwd_m<uint16_t, float, 8>(p, s, stream) : bwd_m<uint16_t, float, 1>(p, s, stream);
-  return vec ? bwd_m<uint16_t, uint16_t, 8>(p, s, stream) : bwd_m<uint16_t, uint16_t, 1>(p, s, stream);
+  return typed<true>(p, types, vec, stream);
 }
 
 }  // namespace ssm

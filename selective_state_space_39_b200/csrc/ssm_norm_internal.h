@@ -28,13 +28,13 @@ struct NormParams {
   void* dresidual;       // (rows, dim) like h, or null
   void* dz;              // (rows, dim) io, with a gate
   float* dw;             // (dim) or null
-  float* ws;             // (norm_bwd_blocks, dim) partial dw
+  float* ws;             // (norm_bwd_slices, dim) partial dw
 };
 
 // types: 0 io bf16, h bf16; 1 io bf16, h fp32; 2 both fp32
 cudaError_t launch_norm_fwd(const NormParams& p, int types, bool vec, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormParams& p, int types, bool vec, cudaStream_t stream);
 // Row slices of the backward pass (partial sums of dw per slice).
-int norm_bwd_slices(int64_t rows, int dim, int groups);
+int norm_bwd_slices(int64_t rows, int groups);
 
 }  // namespace ssm

@@ -345,6 +345,12 @@ def test_refusals_on_the_gpu():
         ssm_gated_delta_fwd(d["q"].transpose(1, 2), *args[1:])
     with pytest.raises(TypeError):
         ssm_gated_delta_fwd(args[0].float(), *args[1:])
+    with pytest.raises(TypeError):
+        ssm_gated_delta_fwd(*[a.half() for a in args])
+    with pytest.raises(ValueError):
+        ssm_gated_delta_fwd(*args, h0=d["h0"][:, :2])
+    with pytest.raises(ValueError):
+        ssm_gated_delta_fwd(args[0], args[1].cpu(), *args[2:])
     with pytest.raises(SsmError):
         ssm_gated_delta_fwd(*args, y=d["v"])
     with pytest.raises(SsmError):  # fp32 gradients are not built
