@@ -12,8 +12,11 @@
 // are summed per row beside the two products.
 //
 // Bound, one token: the state's read and write (268 MB for 64 x 64 heads x 64
-// x 128). Bound, many tokens: the chain of one token (two shuffle reductions
-// and the update); the next token's operands are loaded one token ahead.
+// x 128, bf16 io: 44.8 us = 6.0 TB/s; a variant with the next token's operands
+// in registers, half the warps per SM, took 71 us). Bound, many tokens: the
+// chain of one token (three shuffles, u and the update); operands are loaded
+// up to 16 tokens ahead, the gates (exp, log1p, sigmoid) taken eight tokens at
+// a time, one per lane.
 #include "ssm_delta.cuh"
 
 namespace ssm {
@@ -22,122 +25,185 @@ namespace {
 
 constexpr int kLanes = 8;  // lanes per state row
 
-template <typename IOT, int N>
+// Four values of a lane as they lie in memory.
+template <typename IOT>
+struct Quad;
+template <>
+struct Quad<float> {
+  float4 w;
+  __device__ void load(const float* p) { w = *reinterpret_cast<const float4*>(p); }
+  __device__ void get(float2 (&f)[2]) const {
+    f[0] = make_float2(w.x, w.y);
+    f[1] = make_float2(w.z, w.w);
+  }
+};
+template <>
+struct Quad<uint16_t> {
+  uint2 w;
+  __device__ void load(const uint16_t* p) { w = *reinterpret_cast<const uint2*>(p); }
+  __device__ void get(float2 (&f)[2]) const {
+    f[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+    f[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+  }
+};
+
+// One token on the lane's part of a row; returns y[p] (all eight lanes).
+template <typename IOT, int U>
+__device__ __forceinline__ float one_token(float2 (&s)[2 * U], const Quad<IOT> (&k)[U],
+                                           const Quad<IOT> (&q)[U], float v, float a, float beta,
+                                           int qk_norm, float scale) {
+  float2 sk = make_float2(0.f, 0.f), sq = sk, kq = sk, kk = sk, qq = sk;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float2 kf[2], qf[2];
+    k[i].get(kf);
+    q[i].get(qf);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      sk = fma2(s[2 * i + j], kf[j], sk);
+      sq = fma2(s[2 * i + j], qf[j], sq);
+      kq = fma2(kf[j], qf[j], kq);
+      kk = fma2(kf[j], kf[j], kk);
+      qq = fma2(qf[j], qf[j], qq);
+    }
+  }
+  float r[5] = {sk.x + sk.y, sq.x + sq.y, kq.x + kq.y, kk.x + kk.y, qq.x + qq.y};
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) r[j] += __shfl_xor_sync(0xffffffffu, r[j], o);
+  }
+  float kr = 1.f, qr = scale;
+  if (qk_norm) {
+    kr = rsqrtf(r[3] + kDeltaQkEps);
+    qr = scale * rsqrtf(r[4] + kDeltaQkEps);
+  }
+  const float u = beta * (v - a * kr * r[0]);
+  const float w = u * kr;  // weight of the raw k
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float2 kf[2];
+    k[i].get(kf);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      s[2 * i + j] = fma2(make_float2(w, w), kf[j], mul2(make_float2(a, a), s[2 * i + j]));
+  }
+  return qr * fmaf(a, r[1], w * r[2]);
+}
+
+// ONE: a single token (fewer registers, more state bytes in flight). Otherwise
+// D tokens' operands are held ahead.
+template <typename IOT, int N, bool ONE>
 __global__ void __launch_bounds__(256) delta_step_kernel(const DeltaParams p) {
   using IO = Io<IOT>;
   constexpr int U = N / 32;  // units of four values per lane
+  constexpr int D = ONE ? 1 : (int)(sizeof(IOT) == 2 ? 16 : 8) / U;
   const int l8 = threadIdx.x & (kLanes - 1);
   const int64_t rows = (int64_t)p.batch * p.nheads * p.headdim;
   const int64_t row_raw = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
   if (row_raw - ((threadIdx.x & 31) / kLanes) >= rows) return;  // warp-uniform
   const bool live = row_raw < rows;
-  const int64_t row = live ? row_raw : rows - 1;
-  const uint32_t bh = (uint32_t)(row / p.headdim);
-  const int pp = (int)(row - (int64_t)bh * p.headdim);
+  const uint32_t row = (uint32_t)(live ? row_raw : rows - 1);  // at most 2^31 rows
+  const uint32_t bh = row / (uint32_t)p.headdim;
+  const int pp = (int)(row - bh * (uint32_t)p.headdim);
   const uint32_t b = bh / (uint32_t)p.nheads;
   const int h = (int)(bh - b * (uint32_t)p.nheads);
   const int kh = h / (p.nheads / p.nkheads);
-  const size_t L = (size_t)p.seqlen;
+  const size_t L = ONE ? 1 : (size_t)p.seqlen;
 
   const IOT* q = static_cast<const IOT*>(p.q) + (b * L * p.nkheads + kh) * N + l8 * 4;
   const IOT* k = static_cast<const IOT*>(p.k) + (b * L * p.nkheads + kh) * N + l8 * 4;
   const IOT* v = static_cast<const IOT*>(p.v) + (b * L * p.nheads + h) * p.headdim + pp;
-  const IOT* dt = static_cast<const IOT*>(p.dt) + b * L * p.nheads + h;
+  const IOT* dt = static_cast<const IOT*>(p.dt) + b * L * p.nheads + h;  // token 0's
   const IOT* be = static_cast<const IOT*>(p.beta) + b * L * p.nheads + h;
   IOT* y = static_cast<IOT*>(p.y) + (b * L * p.nheads + h) * p.headdim + pp;
   const size_t qs = (size_t)p.nkheads * N, vs = (size_t)p.nheads * p.headdim;
 
-  float4 s[U];
+  float2 s[2 * U];
   if (p.h0) {
-    const float4* src = reinterpret_cast<const float4*>(p.h0 + row * N) + l8;
+    const float4* src = reinterpret_cast<const float4*>(p.h0 + (size_t)row * N) + l8;
 #pragma unroll
-    for (int i = 0; i < U; ++i) s[i] = src[i * kLanes];
+    for (int i = 0; i < U; ++i) {
+      const float4 f = src[i * kLanes];
+      s[2 * i] = make_float2(f.x, f.y);
+      s[2 * i + 1] = make_float2(f.z, f.w);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < U; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 2 * U; ++i) s[i] = make_float2(0.f, 0.f);
   }
   const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
 
-  float4 kn[U], qn[U];
-  float vn = 0.f, dn = 0.f, bn = 0.f;
-  auto fetch = [&]() {
+  Quad<IOT> kn[D][U], qn[D][U];
+  float vn[D];
+  auto fetch = [&](int j) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      kn[i] = IO::load4(k + i * kLanes * 4);
-      qn[i] = IO::load4(q + i * kLanes * 4);
+      kn[j][i].load(k + i * kLanes * 4);
+      qn[j][i].load(q + i * kLanes * 4);
     }
-    vn = IO::load(v);
-    dn = IO::load(dt);
-    bn = IO::load(be);
-    k += qs; q += qs; v += vs; dt += p.nheads; be += p.nheads;
+    vn[j] = IO::load(v);
+    k += qs; q += qs; v += vs;
   };
-  if (L > 0) fetch();
-  for (size_t t = 0; t < L; ++t) {
-    float4 kc[U], qc[U];
+  // the gates of eight tokens at a time, one token per lane of the row
+  float raw_dt = 0.f, raw_be = 0.f, a8 = 0.f, b8 = 0.f;
+  auto fetch_gates = [&](size_t t) {
+    const size_t at = (t + l8 < L ? t + l8 : L - 1) * p.nheads;
+    raw_dt = IO::load(dt + at);
+    raw_be = IO::load(be + at);
+  };
+  if (L > 0) fetch_gates(0);
 #pragma unroll
-    for (int i = 0; i < U; ++i) { kc[i] = kn[i]; qc[i] = qn[i]; }
-    const float vc = vn;
-    const float a = expf(delta_step_size(dn + bias, p.softplus) * A);
-    const float beta = delta_beta(bn, p.beta_sigmoid);
-    if (t + 1 < L) fetch();
-    float r[5] = {0.f, 0.f, 0.f, 0.f, 0.f};  // S.k, S.q, k.q, k.k, q.q
+  for (int j = 0; j < D; ++j)
+    if (j < (int64_t)L) fetch(j);
+  for (size_t t0 = 0; t0 < L; t0 += D) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const float ss[4] = {s[i].x, s[i].y, s[i].z, s[i].w};
-      const float kk[4] = {kc[i].x, kc[i].y, kc[i].z, kc[i].w};
-      const float qq[4] = {qc[i].x, qc[i].y, qc[i].z, qc[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r[0] = fmaf(ss[j], kk[j], r[0]);
-        r[1] = fmaf(ss[j], qq[j], r[1]);
-        r[2] = fmaf(kk[j], qq[j], r[2]);
-        r[3] = fmaf(kk[j], kk[j], r[3]);
-        r[4] = fmaf(qq[j], qq[j], r[4]);
+    for (int j = 0; j < D; ++j) {
+      if (t0 + j >= L) break;
+      const int j8 = (int)((t0 + j) & (kLanes - 1));
+      if (j8 == 0) {
+        a8 = expf(delta_step_size(raw_dt + bias, p.softplus) * A);
+        b8 = delta_beta(raw_be, p.beta_sigmoid);
+        if (!ONE && t0 + j + kLanes < L) fetch_gates(t0 + j + kLanes);
       }
+      const float a = __shfl_sync(0xffffffffu, a8, j8, kLanes);
+      const float beta = __shfl_sync(0xffffffffu, b8, j8, kLanes);
+      const float out = one_token<IOT, U>(s, kn[j], qn[j], vn[j], a, beta, p.qk_norm, p.scale);
+      if (!ONE && t0 + j + D < L) fetch(j);
+      if (p.y && live && l8 == 0) IO::store(y, out);
+      y += vs;
     }
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) {
-#pragma unroll
-      for (int j = 0; j < 5; ++j) r[j] += __shfl_xor_sync(0xffffffffu, r[j], o);
-    }
-    float kr = 1.f, qr = p.scale;
-    if (p.qk_norm) {
-      kr = 1.f / sqrtf(r[3] + kDeltaQkEps);
-      qr = p.scale / sqrtf(r[4] + kDeltaQkEps);
-    }
-    const float u = beta * (vc - a * kr * r[0]);
-    const float w = u * kr;  // weight of the raw k
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      s[i].x = fmaf(w, kc[i].x, a * s[i].x);
-      s[i].y = fmaf(w, kc[i].y, a * s[i].y);
-      s[i].z = fmaf(w, kc[i].z, a * s[i].z);
-      s[i].w = fmaf(w, kc[i].w, a * s[i].w);
-    }
-    if (p.y && live && l8 == 0) IO::store(y, qr * fmaf(a, r[1], w * r[2]));
-    y += vs;
   }
   if (p.h_last && live) {
-    float4* dst = reinterpret_cast<float4*>(p.h_last + row * N) + l8;
+    float4* dst = reinterpret_cast<float4*>(p.h_last + (size_t)row * N) + l8;
 #pragma unroll
-    for (int i = 0; i < U; ++i) dst[i * kLanes] = s[i];
+    for (int i = 0; i < U; ++i)
+      dst[i * kLanes] = make_float4(s[2 * i].x, s[2 * i].y, s[2 * i + 1].x, s[2 * i + 1].y);
   }
 }
 
-template <typename IOT>
-cudaError_t launch_io(const DeltaParams& p, cudaStream_t stream) {
+template <typename IOT, int N>
+cudaError_t launch_n(const DeltaParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.batch * p.nheads * p.headdim;
   // small problems spread over the SMs in smaller blocks
   const int threads = rows * kLanes < 148 * 256 ? 64 : 256;
   const unsigned blocks = (unsigned)((rows * kLanes + threads - 1) / threads);
+  if (p.seqlen == 1)
+    delta_step_kernel<IOT, N, true><<<blocks, threads, 0, stream>>>(p);
+  else
+    delta_step_kernel<IOT, N, false><<<blocks, threads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename IOT>
+cudaError_t launch_io(const DeltaParams& p, cudaStream_t stream) {
   switch (p.dstate) {
-    case 32: delta_step_kernel<IOT, 32><<<blocks, threads, 0, stream>>>(p); break;
-    case 64: delta_step_kernel<IOT, 64><<<blocks, threads, 0, stream>>>(p); break;
-    case 128: delta_step_kernel<IOT, 128><<<blocks, threads, 0, stream>>>(p); break;
-    case 256: delta_step_kernel<IOT, 256><<<blocks, threads, 0, stream>>>(p); break;
+    case 32: return launch_n<IOT, 32>(p, stream);
+    case 64: return launch_n<IOT, 64>(p, stream);
+    case 128: return launch_n<IOT, 128>(p, stream);
+    case 256: return launch_n<IOT, 256>(p, stream);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
