@@ -954,7 +954,7 @@ static bool delta_chunked(const DeltaDims& d) {
 }
 
 struct DeltaWs {
-  size_t kq, head, state, dstate, r, doto, dotv, dotu, part, bytes;
+  size_t kq, head, state, state16, dstate16, end, r, doto, dotv, dotu, part, bytes;
 };
 static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
   DeltaWs w{};
@@ -970,8 +970,10 @@ static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
   w.head = take(bc * d.nheads * (bwd ? kDeltaHeadBwd : kDeltaHeadFwd));
   if (bwd) {
     const size_t dots = bc * d.nheads * (d.headdim / 16) * kDeltaChunk * 4;
-    w.state = take((size_t)d.batch * (nc + 1) * state);
-    w.dstate = take(bc * state);
+    w.state = take(bc * state);
+    w.state16 = take(bc * state / 2);
+    w.dstate16 = take(bc * state / 2);
+    w.end = take(bc * d.nheads * (d.headdim / 16) * 2 * 4);
     w.r = take((size_t)d.batch * d.seqlen * d.nheads * d.headdim * 2);
     w.doto = take(dots);
     w.dotv = take(dots);
@@ -1017,7 +1019,9 @@ static DeltaChunkParams delta_chunk_params(const DeltaParams& dp, const DeltaDim
   p.test_stall = env_long("SSM_DELTA_TEST_STALL", 0) != 0 ? 1 : 0;
   if (bwd) {
     p.ws_state = reinterpret_cast<float*>(ws + w.state);
-    p.ws_dstate = reinterpret_cast<float*>(ws + w.dstate);
+    p.ws_state16 = reinterpret_cast<uint16_t*>(ws + w.state16);
+    p.ws_dstate16 = reinterpret_cast<uint16_t*>(ws + w.dstate16);
+    p.ws_end = reinterpret_cast<float*>(ws + w.end);
     p.ws_r = reinterpret_cast<uint16_t*>(ws + w.r);
     p.ws_doto = reinterpret_cast<float*>(ws + w.doto);
     p.ws_dotv = reinterpret_cast<float*>(ws + w.dotv);

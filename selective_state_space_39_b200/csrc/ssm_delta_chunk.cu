@@ -329,6 +329,33 @@ __device__ __forceinline__ void store_state(const float (&s)[NS / 8][4], float* 
         mul2(make_float2(s[j][2], s[j][3]), make_float2(inv1, inv1));
   }
 }
+// The rows as bf16 (for products whose results are bf16).
+template <int N, int NS>
+__device__ __forceinline__ void store_state16(const float (&s)[NS / 8][4], uint16_t* dst, float inv0,
+                                              float inv1, int lane) {
+  uint16_t* r0 = dst + (lane >> 2) * N + 2 * (lane & 3);
+#pragma unroll
+  for (int j = 0; j < NS / 8; ++j) {
+    *reinterpret_cast<uint32_t*>(r0 + 8 * j) = pack_bf16x2(s[j][0] * inv0, s[j][1] * inv0);
+    *reinterpret_cast<uint32_t*>(r0 + 8 * N + 8 * j) = pack_bf16x2(s[j][2] * inv1, s[j][3] * inv1);
+  }
+}
+// <s, src> over the warp's part of the state, src fp32 (all lanes).
+template <int N, int NS>
+__device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const float* src, float inv0,
+                                           float inv1, int lane) {
+  const float* r0 = src + (lane >> 2) * N + 2 * (lane & 3);
+  float2 d0 = make_float2(0.f, 0.f), d1 = d0;
+#pragma unroll
+  for (int j = 0; j < NS / 8; ++j) {
+    d0 = fma2(make_float2(s[j][0], s[j][1]), *reinterpret_cast<const float2*>(r0 + 8 * j), d0);
+    d1 = fma2(make_float2(s[j][2], s[j][3]), *reinterpret_cast<const float2*>(r0 + 8 * N + 8 * j), d1);
+  }
+  float d = (d0.x + d0.y) * inv0 + (d1.x + d1.y) * inv1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  return d;
+}
 // Decays the state and brings it under the scale of max(state, terms of
 // largest exponents e0, e1): the sum of 64 terms of k rows below 2 then stays
 // below 2^15.
@@ -504,10 +531,9 @@ __global__ void __launch_bounds__(256, 1) delta_fwd_kernel(const __grid_constant
 
   for (int c = 0; c < p.nchunks; ++c) {
     const int st = c % p.stages;
-    if (BWD)
-      store_state<N, NS>(S, p.ws_state + (((size_t)t.b * (p.nchunks + 1) + c) * d.nheads + h) *
-                                             ((size_t)d.headdim * N) + (size_t)pw * N + hf * NS,
-                         inv0, inv1, lane);
+    const size_t st_at = (((size_t)t.b * p.nchunks + c) * d.nheads + h) * ((size_t)d.headdim * N) +
+                         (size_t)pw * N + hf * NS;
+    if (BWD) store_state16<N, NS>(S, p.ws_state16 + st_at, inv0, inv1, lane);
     if (!wait_stage<SP>(&full[st], (uint32_t)((c / p.stages) & 1), p.wait_limit_ns, 1 + blk)) {
       give_up(p, full, c);
       return;
@@ -613,14 +639,11 @@ __global__ void __launch_bounds__(256, 1) delta_fwd_kernel(const __grid_constant
     row_max(u, m0, m1);
     const NewScale n = rescale(S, inv0, inv1, exponent_of(m0), exponent_of(m1), sc[kScEnd * kC]);
     state_product<N, NS>(S, u, n.s0, n.s1, ks, u0, m);
+    if (BWD) store_state<N, NS>(S, p.ws_state + st_at, inv0, inv1, lane);
     if (last_of(&count[st], warps) && c + p.stages < p.nchunks)
       issue(p, t, l, smem, full, c + p.stages, st);
   }
-  if (BWD)
-    store_state<N, NS>(S, p.ws_state + (((size_t)t.b * (p.nchunks + 1) + p.nchunks) * d.nheads + h) *
-                                           ((size_t)d.headdim * N) + (size_t)pw * N + hf * NS,
-                       inv0, inv1, lane);
-  else if (d.h_last)
+  if (!BWD && d.h_last)
     store_state<N, NS>(S, d.h_last + state_at, inv0, inv1, lane);
 }
 
@@ -679,8 +702,22 @@ __global__ void __launch_bounds__(256, 1) delta_rev_kernel(const __grid_constant
   for (int s = 0; s < p.nchunks; ++s) {
     const int st = s % p.stages, c = p.nchunks - 1 - s;
     const size_t bch = ((size_t)t.b * p.nchunks + c) * d.nheads + h;
-    store_state<N, NS>(S, p.ws_dstate + bch * ((size_t)d.headdim * N) + (size_t)pw * N + hf * NS,
-                       inv0, inv1, lane);
+    const size_t part = (size_t)pw * N + hf * NS, st_at = bch * ((size_t)d.headdim * N) + part;
+    {
+      const float dot = state_dot<N, NS>(S, p.ws_state + st_at, inv0, inv1, lane);
+      if (lane == 0) {
+        p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
+        if (SP == 1) p.ws_end[(bch * pb + pw / 16) * 2 + 1] = 0.f;
+      }
+    }
+    store_state16<N, NS>(S, p.ws_dstate16 + st_at, inv0, inv1, lane);
+    if (c > 0) {  // the next state on its way from DRAM: 16 rows, 128 bytes per prefetch
+      const float* nx = p.ws_state + (bch - d.nheads) * ((size_t)d.headdim * N) + part;
+#pragma unroll
+      for (int i = 0; i < 16 * NS / 32; i += 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + (size_t)((i + lane) / (NS / 32)) * N +
+                                                      (i + lane) % (NS / 32) * 32));
+    }
     if (!wait_stage<SP>(&full[st], (uint32_t)((s / p.stages) & 1), p.wait_limit_ns, 1 + blk)) {
       give_up(p, full, s);
       return;

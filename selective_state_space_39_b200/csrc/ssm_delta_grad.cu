@@ -15,10 +15,11 @@
 // head adds its value heads in order, so dq and dk are written once, through
 // x / |x| when q and k were scaled to unit length. Operands are bf16 (q, k, dy
 // exactly; S, dS, r, dv and the weights rounded once), sums fp32: the outputs
-// are bf16 themselves.
+// are bf16 themselves. <S_end, dS_end> comes from the reverse pass, in fp32.
 //
-// Bound: the states' traffic (S, dS and the next S in fp32, 192 KB per chunk
-// and head of 128 x 128) beside about 5 M bf16 MACs per chunk and head.
+// One CTA of sixteen warps fills an SM's shared memory: a warp takes 16 tokens
+// by a quarter of the columns; the head's tiles come by asynchronous copies,
+// the states' while the weights are computed.
 #include "ssm_delta.cuh"
 
 namespace ssm {
@@ -26,14 +27,14 @@ namespace ssm {
 namespace {
 
 constexpr int kC = kDeltaChunk;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWs = kC * 2 + 16;  // row stride (bytes) of the 64 x 64 tiles
 
 struct GradLayout {
   int xs, ps;  // row strides (bytes) of the dstate-wide and headdim-wide tiles
   int k, q, s, ds, dy, r, dr, w1, w2, ns, f, bytes;
 };
-enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfDelta, kfSig, kfCol, kfRow = kfCol + 4, kfRed = kfRow + 4, kfCount = kfRed + 1 };
+enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfDelta, kfSig, kfCol, kfRow = kfCol + 4, kfCount = kfRow + 2 };
 
 __host__ __device__ inline GradLayout grad_layout(int N, int P) {
   GradLayout g;
@@ -55,6 +56,11 @@ __host__ __device__ inline GradLayout grad_layout(int N, int P) {
   return g;
 }
 
+// 16-byte asynchronous copy, zeros where `in` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
 __device__ __forceinline__ void st16(unsigned char* p, float v) {
   *reinterpret_cast<uint16_t*>(p) = f32_to_bf16(v);
 }
@@ -62,12 +68,12 @@ __device__ __forceinline__ void st16(unsigned char* p, float v) {
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaChunkParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int T = N / 16;  // n-tiles of a warp's half of dstate
+  constexpr int T = N / 32;  // n-tiles of a warp's quarter of dstate
   const DeltaParams& d = p.d;
   const int P = d.headdim;
   const GradLayout g = grad_layout(N, P);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int mi = warp & 3, half = warp >> 2;
+  const int mi = warp & 3, part = warp >> 2;
   const int c = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
   const int rep = d.nheads / d.nkheads;
   const int64_t t0 = (int64_t)c * kC;
@@ -82,51 +88,23 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   const int tr_row = (lane & 7) + (lane & 8), tr_u = lane >> 4;
   const int r0 = mi * 16 + (lane >> 2), r1 = r0 + 8;
 
-  // ---- raw k and q, and 1 / (|x|^2 + eps)
+  // ---- raw k and q
   constexpr int LPR = N / 8;
-  for (int w = 0; w < 2; ++w) {
-    const uint16_t* src = static_cast<const uint16_t*>(w ? d.q : d.k);
-    for (int i = tid; i < kC * LPR; i += kThreads) {
-      const int row = i / LPR, u = i % LPR;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (row < valid)
-        raw = *reinterpret_cast<const uint4*>(src + ((row0 + row) * d.nkheads + kh) * N + u * 8);
-      *reinterpret_cast<uint4*>(smem + (w ? g.q : g.k) + row * g.xs + u * 16) = raw;
-      const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ss = fmaf(bf16_lo(v[j]), bf16_lo(v[j]), fmaf(bf16_hi(v[j]), bf16_hi(v[j]), ss));
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (u == 0) F[(w ? kfLq : kfLk) * kC + row] = d.qk_norm ? 1.f / (ss + kDeltaQkEps) : 0.f;
-    }
-  }
-  __syncthreads();
-
-  // ---- k k^T (for dbeta): rows of block mi, columns of this warp's half
-  float kk[2][2][4] = {};
-#pragma unroll
-  for (int kt = 0; kt < N / 16; ++kt) {
-    uint32_t a[4];
-    ldsm4(a, sm + g.k + (mi * 16 + a_row) * g.xs + (2 * kt + a_u) * 16);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int jp = 2 * half + x;
-      if (jp > mi) continue;
-      uint32_t bb[4];
-      ldsm4(bb, sm + g.k + (16 * jp + nt_row) * g.xs + (2 * kt + nt_u) * 16);
-      mma_bf16(kk[x][0], a, bb[0], bb[1]);
-      mma_bf16(kk[x][1], a, bb[2], bb[3]);
-    }
+  for (int i = tid; i < 2 * kC * LPR; i += kThreads) {
+    const int w = i / (kC * LPR), j = i - w * kC * LPR, row = j / LPR, u = j % LPR;
+    const uint16_t* src = static_cast<const uint16_t*>(w ? d.q : d.k) +
+                          ((row0 + (row < valid ? row : 0)) * d.nkheads + kh) * N + u * 8;
+    copy16(sm + (w ? g.q : g.k) + row * g.xs + u * 16, src, row < valid);
   }
 
+  float kk[2][4] = {};
   float tq[T][4] = {}, tk[T][4] = {};
   for (int hx = 0; hx < rep; ++hx) {
     const int h = kh * rep + hx;
     const size_t bch = bc * d.nheads + h;
     __syncthreads();  // the previous head's tiles are free
 
-    // ---- this head's tiles
+    // ---- this head's tiles: dy, r and dv rows first, then the states
     const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes +
                                                         4 * kDeltaTri);
     if (tid < kC) {
@@ -139,85 +117,96 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     const int ppr = P / 8;
     for (int i = tid; i < 3 * kC * ppr; i += kThreads) {
       const int w = i / (kC * ppr), j = i - w * kC * ppr, row = j / ppr, u = j - row * ppr;
-      const uint16_t* src = w == 0 ? p.dy : (w == 1 ? p.ws_r : p.dv);
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (row < valid)
-        raw = *reinterpret_cast<const uint4*>(src + ((row0 + row) * d.nheads + h) * P + u * 8);
-      *reinterpret_cast<uint4*>(smem + (w == 0 ? g.dy : (w == 1 ? g.r : g.dr)) + row * g.ps +
-                                u * 16) = raw;
+      const uint16_t* src = (w == 0 ? p.dy : (w == 1 ? p.ws_r : p.dv)) +
+                            ((row0 + (row < valid ? row : 0)) * d.nheads + h) * P + u * 8;
+      copy16(sm + (w == 0 ? g.dy : (w == 1 ? g.r : g.dr)) + row * g.ps + u * 16, src, row < valid);
     }
+    cp_async_commit_group();
     const size_t sz = (size_t)P * N;
-    const size_t at = ((size_t)b * (p.nchunks + 1) + c) * d.nheads + h;
-    const float4* S0 = reinterpret_cast<const float4*>(p.ws_state + at * sz);
-    const float4* S1 = reinterpret_cast<const float4*>(p.ws_state + (at + d.nheads) * sz);
-    const float4* dS = reinterpret_cast<const float4*>(p.ws_dstate + bch * sz);
-    float dot = 0.f;
-    for (int i = tid; i < P * (N / 4); i += kThreads) {
-      const int row = i / (N / 4), u = i - row * (N / 4);
-      const float4 s0 = S0[i], s1 = S1[i], ds = dS[i];
-      dot = fmaf(s1.x, ds.x, fmaf(s1.y, ds.y, fmaf(s1.z, ds.z, fmaf(s1.w, ds.w, dot))));
-      *reinterpret_cast<uint2*>(smem + g.s + row * g.xs + u * 8) =
-          make_uint2(pack_bf16x2(s0.x, s0.y), pack_bf16x2(s0.z, s0.w));
-      *reinterpret_cast<uint2*>(smem + g.ds + row * g.xs + u * 8) =
-          make_uint2(pack_bf16x2(ds.x, ds.y), pack_bf16x2(ds.z, ds.w));
+    for (int i = tid; i < 2 * P * LPR; i += kThreads) {
+      const int w = i / (P * LPR), j = i - w * P * LPR, row = j / LPR, u = j % LPR;
+      copy16(sm + (w ? g.ds : g.s) + row * g.xs + u * 16,
+             (w ? p.ws_dstate16 : p.ws_state16) + bch * sz + (size_t)j * 8, true);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (lane == 0) F[kfRed * kC + warp] = dot;
+    cp_async_commit_group();
+    cp_async_wait_group<1>();
     __syncthreads();
 
-    // ---- dy r^T and dv r^T -> W, N + N^T, and the column sums of dbeta
-    float wv[2][2][4] = {}, xv[2][2][4] = {};
-    for (int kt = 0; kt < P / 16; ++kt) {
-      uint32_t a[4], e[4];
-      ldsm4(a, sm + g.dy + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
-      ldsm4(e, sm + g.dr + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+    if (hx == 0) {  // 1 / (|x|^2 + eps) of every k and q row, and k k^T (for dbeta)
+      const int row = tid >> 3, l8 = tid & 7;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int jp = 2 * half + x;
-        if (jp > mi) continue;
-        uint32_t bb[4];
-        ldsm4(bb, sm + g.r + (16 * jp + nt_row) * g.ps + (2 * kt + nt_u) * 16);
-        mma_bf16(wv[x][0], a, bb[0], bb[1]);
-        mma_bf16(wv[x][1], a, bb[2], bb[3]);
-        mma_bf16(xv[x][0], e, bb[0], bb[1]);
-        mma_bf16(xv[x][1], e, bb[2], bb[3]);
+      for (int w = 0; w < 2; ++w) {
+        float ss = 0.f;
+#pragma unroll
+        for (int u = l8; u < LPR; u += 8) {
+          const uint4 raw = *reinterpret_cast<const uint4*>(smem + (w ? g.q : g.k) + row * g.xs + u * 16);
+          const uint32_t v[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            ss = fmaf(bf16_lo(v[j]), bf16_lo(v[j]), fmaf(bf16_hi(v[j]), bf16_hi(v[j]), ss));
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (l8 == 0) F[(w ? kfLq : kfLk) * kC + row] = d.qk_norm ? 1.f / (ss + kDeltaQkEps) : 0.f;
+      }
+      if (part <= mi) {
+#pragma unroll
+        for (int kt = 0; kt < N / 16; ++kt) {
+          uint32_t a[4], bb[4];
+          ldsm4(a, sm + g.k + (mi * 16 + a_row) * g.xs + (2 * kt + a_u) * 16);
+          ldsm4(bb, sm + g.k + (16 * part + nt_row) * g.xs + (2 * kt + nt_u) * 16);
+          mma_bf16(kk[0], a, bb[0], bb[1]);
+          mma_bf16(kk[1], a, bb[2], bb[3]);
+        }
       }
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int jp = 2 * half + x;
+
+    // ---- dy r^T and dv r^T -> W, N + N^T, and the column sums of dbeta: rows of
+    // block mi, columns of block `part`
+    float cs[2][2] = {};
+    if (part <= mi) {
+      float wv[2][4] = {}, xv[2][4] = {};
+      for (int kt = 0; kt < P / 16; ++kt) {
+        uint32_t a[4], e[4], bb[4];
+        ldsm4(a, sm + g.dy + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+        ldsm4(e, sm + g.dr + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+        ldsm4(bb, sm + g.r + (16 * part + nt_row) * g.ps + (2 * kt + nt_u) * 16);
+        mma_bf16(wv[0], a, bb[0], bb[1]);
+        mma_bf16(wv[1], a, bb[2], bb[3]);
+        mma_bf16(xv[0], e, bb[0], bb[1]);
+        mma_bf16(xv[1], e, bb[2], bb[3]);
+      }
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        float cs[2] = {0.f, 0.f};
-        if (jp <= mi) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int i = q < 2 ? r0 : r1, j = 16 * jp + 8 * y + 2 * (lane & 3) + (q & 1);
-            const float gm = j <= i ? ex2_approx((F[kfGhi * kC + i] - F[kfGhi * kC + j]) +
-                                                 (F[kfGlo * kC + i] - F[kfGlo * kC + j]))
-                                    : 0.f;
-            const float kni = F[kfKn * kC + i], knj = F[kfKn * kC + j];
-            const float gb = gm * F[kfBeta * kC + j];
-            const float w = j <= i ? gb * wv[x][y][q] : 0.f;
-            const float n = j < i ? -gb * xv[x][y][q] : 0.f;
-            if (j < i) cs[q & 1] = fmaf(gm * kni * knj * kk[x][y][q], xv[x][y][q], cs[q & 1]);
-            st16(smem + g.w1 + i * kWs + j * 2, w * knj);
-            st16(smem + g.w2 + i * kWs + j * 2, w * F[kfQn * kC + i]);
-            if (j <= i) {
-              st16(smem + g.ns + i * kWs + j * 2, n * knj);
-              st16(smem + g.ns + j * kWs + i * 2, n * kni);
-            }
+        for (int q = 0; q < 4; ++q) {
+          const int i = q < 2 ? r0 : r1, j = 16 * part + 8 * y + 2 * (lane & 3) + (q & 1);
+          const float gm = j <= i ? ex2_approx((F[kfGhi * kC + i] - F[kfGhi * kC + j]) +
+                                               (F[kfGlo * kC + i] - F[kfGlo * kC + j]))
+                                  : 0.f;
+          const float kni = F[kfKn * kC + i], knj = F[kfKn * kC + j];
+          const float gb = gm * F[kfBeta * kC + j];
+          const float w = j <= i ? gb * wv[y][q] : 0.f;
+          const float n = j < i ? -gb * xv[y][q] : 0.f;
+          if (j < i) cs[y][q & 1] = fmaf(gm * kni * knj * kk[y][q], xv[y][q], cs[y][q & 1]);
+          st16(smem + g.w1 + i * kWs + j * 2, w * knj);
+          st16(smem + g.w2 + i * kWs + j * 2, w * F[kfQn * kC + i]);
+          if (j <= i) {
+            st16(smem + g.ns + i * kWs + j * 2, n * knj);
+            st16(smem + g.ns + j * kWs + i * 2, n * kni);
           }
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) cs[q] += __shfl_xor_sync(0xffffffffu, cs[q], o);
-          if (lane < 4) F[(kfCol + mi) * kC + 16 * jp + 8 * y + 2 * lane + q] = cs[q];
         }
       }
     }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) cs[y][q] += __shfl_xor_sync(0xffffffffu, cs[y][q], o);
+        if (lane < 4) F[(kfCol + mi) * kC + 16 * part + 8 * y + 2 * lane + q] = cs[y][q];
+      }
+    cp_async_wait_group<0>();
     __syncthreads();
 
     // ---- dq += e^G dy S + W k;  dk += beta e^(G_end - G) r dS - e^G dv S + W^T q + (N + N^T) k
@@ -237,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < T / 2; ++j) {
           uint32_t bb[4];
-          ldsm4t(bb, sm + at_b + (16 * kt + tr_row) * g.xs + (half * T + 2 * j + tr_u) * 16);
+          ldsm4t(bb, sm + at_b + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
           mma_bf16(t[2 * j], a, bb[0], bb[1]);
           mma_bf16(t[2 * j + 1], a, bb[2], bb[3]);
         }
@@ -260,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 #pragma unroll
       for (int j = 0; j < T / 2; ++j) {
         uint32_t bk[4], bq[4];
-        ldsm4t(bk, sm + g.k + (16 * kt + tr_row) * g.xs + (half * T + 2 * j + tr_u) * 16);
-        ldsm4t(bq, sm + g.q + (16 * kt + tr_row) * g.xs + (half * T + 2 * j + tr_u) * 16);
+        ldsm4t(bk, sm + g.k + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
+        ldsm4t(bq, sm + g.q + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
         if (kt <= mi) {
           mma_bf16(tq[2 * j], a, bk[0], bk[1]);
           mma_bf16(tq[2 * j + 1], a, bk[2], bk[3]);
@@ -311,9 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       F[(kfRow)*kC + tid] = dg;
       asm volatile("bar.sync 1, 64;" ::: "memory");
       if (warp == 0) dg += F[(kfRow)*kC + 32];
-      float end = 0.f;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) end += F[kfRed * kC + i];
+      float end = 0.f;  // <S_end, dS_end>, over the reverse pass's warps in order
+      for (int i = 0; i < 2 * sl; ++i) end += p.ws_end[bch * 2 * sl + i];
       dg += end;
       float dA = 0.f, dbias = 0.f;
       if (tid < valid) {
@@ -351,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     float d0 = 0.f, d1 = 0.f;
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      const int at = (half * T + j) * 16 + (lane & 3) * 4;
+      const int at = (part * T + j) * 16 + (lane & 3) * 4;
       const uint32_t x0 = *reinterpret_cast<const uint32_t*>(x + r0 * g.xs + at);
       const uint32_t x1 = *reinterpret_cast<const uint32_t*>(x + r1 * g.xs + at);
       const float(&t)[4] = w ? tq[j] : tk[j];
@@ -363,9 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       d0 += __shfl_xor_sync(0xffffffffu, d0, o);
       d1 += __shfl_xor_sync(0xffffffffu, d1, o);
     }
-    if ((lane & 3) == 0) {
-      F[(kfCol + 2 * w + half) * kC + r0] = d0;
-      F[(kfCol + 2 * w + half) * kC + r1] = d1;
+    if ((lane & 3) == 0) {  // over the weights' tiles, which are free
+      float* D = reinterpret_cast<float*>(smem + g.w1) + (4 * w + part) * kC;
+      D[r0] = d0;
+      D[r1] = d1;
     }
   }
   __syncthreads();
@@ -373,14 +362,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   for (int w = 0; w < 2; ++w) {
     const unsigned char* x = smem + (w ? g.q : g.k);
     const float n0 = F[(w ? kfQn : kfKn) * kC + r0], n1 = F[(w ? kfQn : kfKn) * kC + r1];
+    const float* D = reinterpret_cast<const float*>(smem + g.w1) + 4 * w * kC;
     const float e0 = F[(w ? kfLq : kfLk) * kC + r0] *
-                     (F[(kfCol + 2 * w) * kC + r0] + F[(kfCol + 2 * w + 1) * kC + r0]);
+                     (D[r0] + D[kC + r0] + D[2 * kC + r0] + D[3 * kC + r0]);
     const float e1 = F[(w ? kfLq : kfLk) * kC + r1] *
-                     (F[(kfCol + 2 * w) * kC + r1] + F[(kfCol + 2 * w + 1) * kC + r1]);
+                     (D[r1] + D[kC + r1] + D[2 * kC + r1] + D[3 * kC + r1]);
     uint16_t* dst = w ? p.dq : p.dk;
 #pragma unroll
     for (int j = 0; j < T; ++j) {
-      const int at = (half * T + j) * 16 + (lane & 3) * 4;
+      const int at = (part * T + j) * 16 + (lane & 3) * 4;
       const uint32_t x0 = *reinterpret_cast<const uint32_t*>(x + r0 * g.xs + at);
       const uint32_t x1 = *reinterpret_cast<const uint32_t*>(x + r1 * g.xs + at);
       const float(&t)[4] = w ? tq[j] : tk[j];

@@ -76,8 +76,10 @@ struct DeltaChunkParams {
   // backward only
   const uint16_t* dy;    // (batch, seqlen, nheads, headdim)
   const float* dh_last;  // or null
-  float* ws_state;       // (batch, nchunks + 1, nheads, headdim, dstate): state before each chunk
-  float* ws_dstate;      // (batch, nchunks, nheads, headdim, dstate): adjoint after each chunk
+  float* ws_state;       // (batch, nchunks, nheads, headdim, dstate): state after each chunk
+  uint16_t* ws_state16;  // ... before each chunk, bf16
+  uint16_t* ws_dstate16; // ... its adjoint after each chunk, bf16
+  float* ws_end;         // (batch, nchunks, nheads, headdim/16, 2): <state, adjoint> after each chunk
   uint16_t* ws_r;        // (batch, seqlen, nheads, headdim): v minus the state's prediction
   float* ws_doto;        // (batch, nchunks, nheads, headdim/16, 64): dy.y over 16 rows
   float* ws_dotv;        //   ... dv.v
