@@ -60,8 +60,18 @@ __device__ __forceinline__ uint32_t swz(int row, int c) {
   return (uint32_t)(row * RB + ((c ^ (row & 7)) << 4));
 }
 
+// Byte offset of 16-byte unit `u` of token `row` in a k or q tile: blocks of 64
+// columns, 128-byte rows.
+__device__ __forceinline__ uint32_t kq_at(int row, int u) {
+  return (uint32_t)((u >> 3) * (kDeltaChunk * 128)) + swz<128>(row, u & 7);
+}
 // Byte offset inside a 16 x 16 block of a triangular tile (kDeltaTri).
 __device__ __forceinline__ uint32_t tri_at(int row, int half) {
+  return (uint32_t)(((row >> 3) * 2 + half) * 128 + (row & 7) * 16);
+}
+// Byte offset in a column tile (16 columns of v, 32-byte rows): the two halves
+// of a row are swapped in rows 4 .. 7 of every eight.
+__device__ __forceinline__ uint32_t col_at(int row, int half) {
   return (uint32_t)(row * 32 + ((half ^ ((row >> 2) & 1)) << 4));
 }
 

@@ -55,8 +55,7 @@ constexpr int kMaxStages = 4;
 constexpr int kMaxBlocks = 8;  // 16-row blocks per CTA
 
 // Shared memory: `stages` x [k/q tiles | head blocks], then per 16-row block two
-// buffers of `tiles` column tiles (64 tokens x 16 columns, 32-byte rows with
-// the two halves swapped as in a triangular tile's blocks).
+// buffers of `tiles` column tiles (64 tokens x 16 columns).
 constexpr int kCol = kC * 32;  // bytes of a column tile
 struct Layout {
   int kq, head, heads, tiles, stage;  // bytes; heads of a CTA; column tiles
@@ -93,6 +92,7 @@ __device__ __forceinline__ void mma_tiles(float (&acc)[T][4], const uint32_t (&a
 struct LaneMap {
   int nt_row, nt_unit, tr_row, tr_unit;
   uint32_t nt_tri, tr_tri;  // the same inside a block of a triangular tile
+  uint32_t nt_col;          // and of a column tile
 };
 __device__ __forceinline__ LaneMap lane_map(int lane) {
   LaneMap m;
@@ -102,6 +102,7 @@ __device__ __forceinline__ LaneMap lane_map(int lane) {
   m.tr_unit = lane >> 4;
   m.nt_tri = tri_at(m.nt_row, m.nt_unit);
   m.tr_tri = tri_at(m.tr_row, m.tr_unit);
+  m.nt_col = col_at(m.nt_row, m.nt_unit);
   return m;
 }
 
@@ -162,8 +163,8 @@ __device__ __forceinline__ void state_product(float (&s)[NS / 8][4], const float
 #pragma unroll
     for (int jn = 0; jn < NS / 16; jn += 2) {
       uint32_t b[2][4];
-      ldsm4t(b[0], tile + swz<N * 2>(16 * kt + m.tr_row, u0 + 2 * jn + m.tr_unit));
-      ldsm4t(b[1], tile + swz<N * 2>(16 * kt + m.tr_row, u0 + 2 * jn + 2 + m.tr_unit));
+      ldsm4t(b[0], tile + kq_at(16 * kt + m.tr_row, u0 + 2 * jn + m.tr_unit));
+      ldsm4t(b[1], tile + kq_at(16 * kt + m.tr_row, u0 + 2 * jn + 2 + m.tr_unit));
       mma_tiles(s, hi, b, 2 * jn);
       mma_tiles(s, lo, b, 2 * jn);
     }
@@ -224,7 +225,7 @@ __device__ __forceinline__ void load_rows(float (&x)[T][4], uint32_t tile, int t
 #pragma unroll
   for (int jp = 0; jp < T / 2; ++jp) {
     uint32_t r[4];
-    ldsm4t(r, tile + (t0 + 16 * jp) * 32 + m.nt_tri);
+    ldsm4t(r, tile + (t0 + 16 * jp) * 32 + m.nt_col);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = 2 * jp + (q >> 1), e = (q & 1) * 2;
@@ -248,7 +249,7 @@ __device__ __forceinline__ void store_rows(const float (&x)[T][4], uint32_t tile
       const int j = 2 * jp + (q >> 1), e = (q & 1) * 2;
       r[q] = pack_bf16x2(x[j][e], x[j][e + 1]);
     }
-    stsm4t(tile + (t0 + 16 * jp) * 32 + m.nt_tri, r);
+    stsm4t(tile + (t0 + 16 * jp) * 32 + m.nt_col, r);
   }
   __syncwarp();
 #pragma unroll
@@ -257,7 +258,7 @@ __device__ __forceinline__ void store_rows(const float (&x)[T][4], uint32_t tile
     uint4 w;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                 : "r"(tile + tri_at(tk, u))
+                 : "r"(tile + col_at(tk, u))
                  : "memory");
     if (tk < valid) *reinterpret_cast<uint4*>(out + (size_t)tk * out_stride + u * 8) = w;
   }
@@ -272,7 +273,7 @@ __device__ __forceinline__ void fetch_rows(uint32_t tile, const uint16_t* src, s
   for (int it = 0; it < T / 2; ++it) {
     const int tk = t0 + it * 16 + (lane >> 1), u = lane & 1;
     const bool in = tk < valid;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + tri_at(tk, u)),
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + col_at(tk, u)),
                  "l"(src + (in ? (size_t)tk * stride : 0) + u * 8), "r"(in ? 16 : 0)
                  : "memory");
   }
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(256, 1) delta_fwd_kernel(const __grid_constant
       uint32_t bk[4][4], bq[4][4];
 #pragma unroll
       for (int jp = 0; jp < 4; ++jp) {
-        const uint32_t at = swz<N * 2>(16 * jp + m.nt_row, u0 + 2 * kt + m.nt_unit);
+        const uint32_t at = kq_at(16 * jp + m.nt_row, u0 + 2 * kt + m.nt_unit);
         ldsm4(bk[jp], ks + at);
         ldsm4(bq[jp], qs + at);
       }
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(256, 1) delta_rev_kernel(const __grid_constant
       uint32_t bk[4][4];
 #pragma unroll
       for (int jp = 0; jp < 4; ++jp)
-        ldsm4(bk[jp], ks + swz<N * 2>(16 * jp + m.nt_row, u0 + 2 * kt + m.nt_unit));
+        ldsm4(bk[jp], ks + kq_at(16 * jp + m.nt_row, u0 + 2 * kt + m.nt_unit));
       mma_tiles(x, hi, bk);
       mma_tiles(x, lo, bk);
     }

@@ -35,8 +35,9 @@ bool delta_step_dstate_supported(int dstate);
 cudaError_t launch_delta_step(const DeltaParams& p, bool bf16, cudaStream_t stream);
 
 // ---- chunk by chunk (bf16 io) ---------------------------------------------
-// Per (batch row, chunk, key head) the workspace holds k and q as fp16 tiles
-// [64][dstate], every row scaled by a power of two; per (batch row, chunk,
+// Per (batch row, chunk, key head) the workspace holds k and q as fp16 tiles,
+// every row scaled by a power of two, in blocks of 64 tokens x 64 columns with
+// the 128-byte swizzle; per (batch row, chunk,
 // head) a block of per-token factors and the 64 x 64 tiles of the chunk.
 enum DeltaScal {       // arrays of 64 floats in a head block; the forward pass reads the first seven
   kScSk = 0,           // e^G kmul: S k16 -> the decayed prediction of v
@@ -54,11 +55,14 @@ enum DeltaScal {       // arrays of 64 floats in a head block; the forward pass 
   kScQn = 12,          // unit-length factor of q, times the readout scale
   kScCount = 13,
 };
-// A lower triangular 64 x 64 fp16 tile: its ten 16 x 16 blocks (i, j <= i) in
-// row order, 512 bytes each, the two 16-byte halves of a row swapped in rows 4
-// .. 7 and 12 .. 15 (eight rows at one column then lie in eight bank groups).
+// A lower triangular 64 x 64 fp16 tile: its ten 16 x 16 blocks (i, j <= i),
+// column of blocks by column, 512 bytes each, as 2 x 2 core matrices of eight
+// rows of 16 bytes (the tensor cores' layout without a swizzle; any eight rows
+// at one column lie in eight bank groups).
 constexpr int kDeltaTri = 10 * 512;
-__host__ __device__ constexpr int delta_tri_block(int i, int j) { return (i * (i + 1) / 2 + j) * 512; }
+__host__ __device__ constexpr int delta_tri_block(int i, int j) {
+  return j * 2048 - 256 * j * (j - 1) + (i - j) * 512;
+}
 constexpr int kDeltaScalFwd = 7 * kDeltaChunk * 4, kDeltaScalBwd = kScCount * kDeltaChunk * 4;
 // A head block: T hi, T lo, P hi, (backward: P lo,) then the factors.
 constexpr int kDeltaHeadFwd = 3 * kDeltaTri + kDeltaScalFwd;

@@ -99,7 +99,6 @@ template <int N, bool BWD>
 __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChunkParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   using Sm = PrepSmem<N>;
-  constexpr int RB = N * 2;        // bytes of a k/q row
   constexpr int LPR = N / 8;       // lanes (16-byte units) per row
   constexpr int RPW = 32 / LPR;    // rows per warp and step
   unsigned char* tiles = smem;
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
         const float2 v = mul2(f[i], make_float2(s, s));
         o4[i] = h2_bits(__floats2half2_rn(v.x, v.y));
       }
-      const uint32_t at = swz<RB>(row, u);
+      const uint32_t at = kq_at(row, u);
       *reinterpret_cast<uint4*>(tiles + w * Sm::kTile + at) = out;
       if (sub == 0) *reinterpret_cast<uint4*>(kq_out + w * Sm::kTile + at) = out;
       if (u == 0) {
@@ -228,13 +227,13 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
     for (int kt = 0; kt < N / 16; ++kt) {
       uint32_t ak[4], aq[4];
       const int ar = warp * 16 + (lane & 15), au = 2 * kt + (lane >> 4);
-      ldsm4(ak, ks + swz<RB>(ar, au));
-      ldsm4(aq, qs + swz<RB>(ar, au));
+      ldsm4(ak, ks + kq_at(ar, au));
+      ldsm4(aq, qs + kq_at(ar, au));
 #pragma unroll
       for (int jp = 0; jp < 4; ++jp) {
         if (jp > warp) continue;
         uint32_t bb[4];
-        ldsm4(bb, ks + swz<RB>(16 * jp + (lane & 7) + ((lane & 16) >> 1), 2 * kt + ((lane >> 3) & 1)));
+        ldsm4(bb, ks + kq_at(16 * jp + (lane & 7) + ((lane & 16) >> 1), 2 * kt + ((lane >> 3) & 1)));
         mma_f16(kk[2 * jp], ak, bb[0], bb[1]);
         mma_f16(kk[2 * jp + 1], ak, bb[2], bb[3]);
         mma_f16(qk[2 * jp], aq, bb[0], bb[1]);
