@@ -28,454 +28,11 @@
 // to bf16, takes one fp16 piece of S, u and P (2^-12 each).
 #include <stdlib.h>
 
-#include <algorithm>
-
-#include "ssm_delta.cuh"
+#include "ssm_delta_rows.cuh"
 
 namespace ssm {
 
 namespace {
-
-constexpr int kC = kDeltaChunk;
-
-__device__ int g_delta_timeout;  // set by a CTA that gave up a bounded wait
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-constexpr int kMaxStages = 4;
-constexpr int kMaxBlocks = 8;  // 16-row blocks per CTA
-
-// Shared memory: `stages` x [k/q tiles | head blocks], then per 16-row block two
-// buffers of `tiles` column tiles (64 tokens x 16 columns).
-constexpr int kCol = kC * 32;  // bytes of a column tile
-struct Layout {
-  int kq, head, heads, tiles, stage;  // bytes; heads of a CTA; column tiles
-};
-// `blocks` 16-row blocks per CTA out of heads of `per_head` blocks each.
-__host__ __device__ inline Layout layout(int dstate, int blocks, int per_head, int tiles,
-                                         int head_bytes) {
-  Layout l;
-  l.kq = 2 * kC * dstate * 2;
-  l.head = head_bytes;
-  l.heads = per_head % blocks == 0 ? 1
-            : blocks % per_head == 0 ? blocks / per_head
-                                     : (blocks + per_head - 2) / per_head + 1;
-  l.tiles = tiles;
-  l.stage = l.kq + l.heads * l.head;
-  return l;
-}
-
-// Pairs of neighbouring tiles += A times their B fragments. The accumulators of
-// one piece are all visited before the next piece's, so that no MMA waits for
-// the one before it.
-template <int T, int P>
-__device__ __forceinline__ void mma_tiles(float (&acc)[T][4], const uint32_t (&a)[4],
-                                          const uint32_t (&b)[P][4], int t0 = 0) {
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    mma_f16(acc[t0 + 2 * j], a, b[j][0], b[j][1]);
-    mma_f16(acc[t0 + 2 * j + 1], a, b[j][2], b[j][3]);
-  }
-}
-
-// Lane's row/unit offsets of the two fragment loads (see swz):
-//   nt: B rows are n          tr: B rows are k (transposing load)
-struct LaneMap {
-  int nt_row, nt_unit, tr_row, tr_unit;
-  uint32_t nt_tri, tr_tri;  // the same inside a block of a triangular tile
-  uint32_t nt_col;          // and of a column tile
-};
-__device__ __forceinline__ LaneMap lane_map(int lane) {
-  LaneMap m;
-  m.nt_row = (lane & 7) + ((lane & 16) >> 1);
-  m.nt_unit = (lane >> 3) & 1;
-  m.tr_row = (lane & 7) + (lane & 8);
-  m.tr_unit = lane >> 4;
-  m.nt_tri = tri_at(m.nt_row, m.nt_unit);
-  m.tr_tri = tri_at(m.tr_row, m.tr_unit);
-  m.nt_col = col_at(m.nt_row, m.nt_unit);
-  return m;
-}
-
-// acc[16 x 8 TT tokens] += x[16 x 64 tokens] B over a triangular tile, x as two
-// pieces, B as one or two. TR false: B[n][k], blocks n >= k, the accumulators
-// holding the tokens from 16 jp0 on; true: B[k][n] (TT = 8, jp0 = 0).
-template <bool TR, bool XLO, bool BLO, int TT>
-__device__ __forceinline__ void tri_product(float (&acc)[TT][4], const float (&x)[8][4], float s0,
-                                            float s1, uint32_t bhi, uint32_t blo, int jp0,
-                                            const LaneMap& m) {
-#pragma unroll
-  for (int kt = 0; kt < 4; ++kt) {
-    uint32_t hi[4], lo[4];
-    if (XLO)
-      split_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi, lo);
-    else
-      half_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi);
-    uint32_t bh[TT / 2][4], bl[TT / 2][4];
-#pragma unroll
-    for (int jj = 0; jj < TT / 2; ++jj) {
-      const int jp = jp0 + jj;
-      if (TR ? jp > kt : jp < kt) continue;  // warp-uniform
-      const uint32_t at = TR ? delta_tri_block(kt, jp) + m.tr_tri : delta_tri_block(jp, kt) + m.nt_tri;
-      if (TR) {
-        ldsm4t(bh[jj], bhi + at);
-        if (BLO) ldsm4t(bl[jj], blo + at);
-      } else {
-        ldsm4(bh[jj], bhi + at);
-        if (BLO) ldsm4(bl[jj], blo + at);
-      }
-    }
-#pragma unroll
-    for (int piece = 0; piece < 3; ++piece) {
-      if ((piece == 1 && !XLO) || (piece == 2 && !BLO)) continue;
-#pragma unroll
-      for (int jj = 0; jj < TT / 2; ++jj) {
-        const int jp = jp0 + jj;
-        if (TR ? jp > kt : jp < kt) continue;
-        const uint32_t(&a)[4] = piece == 1 ? lo : hi;
-        const uint32_t(&b)[4] = piece == 2 ? bl[jj] : bh[jj];
-        mma_f16(acc[2 * jj], a, b[0], b[1]);
-        mma_f16(acc[2 * jj + 1], a, b[2], b[3]);
-      }
-    }
-  }
-}
-
-// s[16 x NS] += x[16 x 64 tokens] tile[64 tokens x N], columns from 8 u0 on, x
-// as two pieces.
-template <int N, int NS>
-__device__ __forceinline__ void state_product(float (&s)[NS / 8][4], const float (&x)[8][4],
-                                              float s0, float s1, uint32_t tile, int u0,
-                                              const LaneMap& m) {
-#pragma unroll
-  for (int kt = 0; kt < 4; ++kt) {
-    uint32_t hi[4], lo[4];
-    split_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi, lo);
-#pragma unroll
-    for (int jn = 0; jn < NS / 16; jn += 2) {
-      uint32_t b[2][4];
-      ldsm4t(b[0], tile + kq_at(16 * kt + m.tr_row, u0 + 2 * jn + m.tr_unit));
-      ldsm4t(b[1], tile + kq_at(16 * kt + m.tr_row, u0 + 2 * jn + 2 + m.tr_unit));
-      mma_tiles(s, hi, b, 2 * jn);
-      mma_tiles(s, lo, b, 2 * jn);
-    }
-  }
-}
-
-// x *= per-row factors (rows g and g + 8)
-template <int T>
-__device__ __forceinline__ void scale_rows(float (&x)[T][4], float f0, float f1) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const float2 a = mul2(make_float2(x[j][0], x[j][1]), make_float2(f0, f0));
-    const float2 b = mul2(make_float2(x[j][2], x[j][3]), make_float2(f1, f1));
-    x[j][0] = a.x; x[j][1] = a.y;
-    x[j][2] = b.x; x[j][3] = b.y;
-  }
-}
-// x *= per-token factors (columns)
-template <int T>
-__device__ __forceinline__ void scale_cols(float (&x)[T][4], const float* f, int lane) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const float2 c = *reinterpret_cast<const float2*>(f + 8 * j + 2 * (lane & 3));
-    const float2 a = mul2(make_float2(x[j][0], x[j][1]), c);
-    const float2 b = mul2(make_float2(x[j][2], x[j][3]), c);
-    x[j][0] = a.x; x[j][1] = a.y;
-    x[j][2] = b.x; x[j][3] = b.y;
-  }
-}
-template <int T>
-__device__ __forceinline__ void add_tiles(float (&x)[T][4], const float (&y)[T][4]) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const float2 a = add2(make_float2(x[j][0], x[j][1]), make_float2(y[j][0], y[j][1]));
-    const float2 b = add2(make_float2(x[j][2], x[j][3]), make_float2(y[j][2], y[j][3]));
-    x[j][0] = a.x; x[j][1] = a.y;
-    x[j][2] = b.x; x[j][3] = b.y;
-  }
-}
-template <int T>
-__device__ __forceinline__ void zero(float (&x)[T][4]) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-}
-// The warp's tiles out of all eight: the half `hf` of them when TT is 4.
-template <int TT>
-__device__ __forceinline__ void own(float (&d)[TT][4], const float (&x)[8][4], int hf) {
-#pragma unroll
-  for (int j = 0; j < TT; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) d[j][q] = TT == 8 ? x[j][q] : (hf ? x[4 + (j & 3)][q] : x[j & 3][q]);
-}
-
-// The 16 columns of a column tile [token][p] as fp32 accumulator-shaped values
-// [p][token], tokens t0 .. t0 + 8 T - 1.
-template <int T>
-__device__ __forceinline__ void load_rows(float (&x)[T][4], uint32_t tile, int t0, const LaneMap& m) {
-#pragma unroll
-  for (int jp = 0; jp < T / 2; ++jp) {
-    uint32_t r[4];
-    ldsm4t(r, tile + (t0 + 16 * jp) * 32 + m.nt_col);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int j = 2 * jp + (q >> 1), e = (q & 1) * 2;
-      x[j][e] = bf16_lo(r[q]);
-      x[j][e + 1] = bf16_hi(r[q]);
-    }
-  }
-}
-
-// Accumulator-shaped values [p][token] of tokens t0 .. -> bf16 rows of a column
-// tile, then to global memory (32 bytes a token).
-template <int T>
-__device__ __forceinline__ void store_rows(const float (&x)[T][4], uint32_t tile, int t0,
-                                           uint16_t* out, size_t out_stride, int valid, int lane,
-                                           const LaneMap& m) {
-#pragma unroll
-  for (int jp = 0; jp < T / 2; ++jp) {
-    uint32_t r[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int j = 2 * jp + (q >> 1), e = (q & 1) * 2;
-      r[q] = pack_bf16x2(x[j][e], x[j][e + 1]);
-    }
-    stsm4t(tile + (t0 + 16 * jp) * 32 + m.nt_col, r);
-  }
-  __syncwarp();
-#pragma unroll
-  for (int it = 0; it < T / 2; ++it) {
-    const int tk = t0 + it * 16 + (lane >> 1), u = lane & 1;
-    uint4 w;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                 : "r"(tile + col_at(tk, u))
-                 : "memory");
-    if (tk < valid) *reinterpret_cast<uint4*>(out + (size_t)tk * out_stride + u * 8) = w;
-  }
-}
-
-// Asynchronous copy of tokens t0 .. t0 + 8 T - 1 of 16 columns into a column
-// tile; tokens from `valid` on become zero. src: the chunk's first token.
-template <int T>
-__device__ __forceinline__ void fetch_rows(uint32_t tile, const uint16_t* src, size_t stride, int t0,
-                                           int valid, int lane) {
-#pragma unroll
-  for (int it = 0; it < T / 2; ++it) {
-    const int tk = t0 + it * 16 + (lane >> 1), u = lane & 1;
-    const bool in = tk < valid;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + col_at(tk, u)),
-                 "l"(src + (in ? (size_t)tk * stride : 0) + u * 8), "r"(in ? 16 : 0)
-                 : "memory");
-  }
-}
-
-// Per-token dot products of x and y over the warp's 16 rows -> out[8 T].
-template <int T>
-__device__ __forceinline__ void row_dots(const float (&x)[T][4], const float (&y)[T][4],
-                                         float* out, int lane) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    float a = fmaf(x[j][0], y[j][0], x[j][2] * y[j][2]);
-    float b = fmaf(x[j][1], y[j][1], x[j][3] * y[j][3]);
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (lane < 4) *reinterpret_cast<float2*>(out + 8 * j + 2 * lane) = make_float2(a, b);
-  }
-}
-
-// The carried rows: s = true value / inv, inv a power of two per row.
-template <int N, int NS>
-__device__ __forceinline__ void load_state(float (&s)[NS / 8][4], const float* src, float& inv0,
-                                           float& inv1, int lane) {
-  if (!src) {
-    zero(s);
-    inv0 = inv1 = 1.f;
-    return;
-  }
-  const float* r0 = src + (lane >> 2) * N + 2 * (lane & 3);
-#pragma unroll
-  for (int j = 0; j < NS / 8; ++j) {
-    const float2 a = *reinterpret_cast<const float2*>(r0 + 8 * j);
-    const float2 b = *reinterpret_cast<const float2*>(r0 + 8 * N + 8 * j);
-    s[j][0] = a.x; s[j][1] = a.y; s[j][2] = b.x; s[j][3] = b.y;
-  }
-  float m0, m1;
-  row_max(s, m0, m1);
-  const RowScale a = row_scale<6>(exponent_of(m0)), b = row_scale<6>(exponent_of(m1));
-  scale_rows(s, a.s, b.s);
-  inv0 = a.inv;
-  inv1 = b.inv;
-}
-template <int N, int NS>
-__device__ __forceinline__ void store_state(const float (&s)[NS / 8][4], float* dst, float inv0,
-                                            float inv1, int lane) {
-  float* r0 = dst + (lane >> 2) * N + 2 * (lane & 3);
-#pragma unroll
-  for (int j = 0; j < NS / 8; ++j) {
-    *reinterpret_cast<float2*>(r0 + 8 * j) = mul2(make_float2(s[j][0], s[j][1]), make_float2(inv0, inv0));
-    *reinterpret_cast<float2*>(r0 + 8 * N + 8 * j) =
-        mul2(make_float2(s[j][2], s[j][3]), make_float2(inv1, inv1));
-  }
-}
-// The rows as bf16 (for products whose results are bf16).
-template <int N, int NS>
-__device__ __forceinline__ void store_state16(const float (&s)[NS / 8][4], uint16_t* dst, float inv0,
-                                              float inv1, int lane) {
-  uint16_t* r0 = dst + (lane >> 2) * N + 2 * (lane & 3);
-#pragma unroll
-  for (int j = 0; j < NS / 8; ++j) {
-    *reinterpret_cast<uint32_t*>(r0 + 8 * j) = pack_bf16x2(s[j][0] * inv0, s[j][1] * inv0);
-    *reinterpret_cast<uint32_t*>(r0 + 8 * N + 8 * j) = pack_bf16x2(s[j][2] * inv1, s[j][3] * inv1);
-  }
-}
-// <s, src> over the warp's part of the state, src fp32 (all lanes).
-template <int N, int NS>
-__device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const float* src, float inv0,
-                                           float inv1, int lane) {
-  const float* r0 = src + (lane >> 2) * N + 2 * (lane & 3);
-  float2 d0 = make_float2(0.f, 0.f), d1 = d0;
-#pragma unroll
-  for (int j = 0; j < NS / 8; ++j) {
-    d0 = fma2(make_float2(s[j][0], s[j][1]), *reinterpret_cast<const float2*>(r0 + 8 * j), d0);
-    d1 = fma2(make_float2(s[j][2], s[j][3]), *reinterpret_cast<const float2*>(r0 + 8 * N + 8 * j), d1);
-  }
-  float d = (d0.x + d0.y) * inv0 + (d1.x + d1.y) * inv1;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  return d;
-}
-// Decays the state and brings it under the scale of max(state, terms of
-// largest exponents e0, e1): the sum of 64 terms of k rows below 2 then stays
-// below 2^15.
-struct NewScale {
-  float s0, s1;
-};
-template <int T>
-__device__ __forceinline__ NewScale rescale(float (&s)[T][4], float& inv0, float& inv1,
-                                            uint32_t e0, uint32_t e1, float end) {
-  float m0, m1;
-  row_max(s, m0, m1);
-  const RowScale a = row_scale<6>(max(e0, exponent_of(m0 * inv0)));
-  const RowScale b = row_scale<6>(max(e1, exponent_of(m1 * inv1)));
-  // 2^100: a row that is all zero has no exponent of its own
-  scale_rows(s, end * fminf(inv0 * a.s, 1.2676506e30f), end * fminf(inv1 * b.s, 1.2676506e30f));
-  inv0 = a.inv;
-  inv1 = b.inv;
-  NewScale n;
-  n.s0 = a.s;
-  n.s1 = b.s;
-  return n;
-}
-
-// ---------------------------------------------------------------- the CTA ----
-// SP warps share a block of 16 rows (SP = 2: half of dstate each).
-struct Cta {
-  int b, kh, rb0, active, h0, nheads;  // row blocks of this CTA in its key head's group
-};
-__device__ __forceinline__ Cta cta_of(const DeltaChunkParams& p) {
-  const DeltaParams& d = p.d;
-  Cta c;
-  const int pb = d.headdim / 16, group = d.nheads / d.nkheads * pb;
-  const int slices = (group + p.blocks - 1) / p.blocks;
-  const int bk = blockIdx.x / slices, sl = blockIdx.x - bk * slices;
-  c.b = bk / d.nkheads;
-  c.kh = bk - c.b * d.nkheads;
-  c.rb0 = sl * p.blocks;
-  c.active = min(p.blocks, group - c.rb0);
-  const int first = c.rb0 / pb;
-  c.nheads = (c.rb0 + c.active - 1) / pb - first + 1;
-  c.h0 = c.kh * (d.nheads / d.nkheads) + first;
-  return c;
-}
-
-// One thread: issues the copies of chunk c into stage st.
-__device__ __forceinline__ void issue(const DeltaChunkParams& p, const Cta& t, const Layout& l,
-                                      unsigned char* smem, uint64_t* full, int c, int st) {
-  const DeltaParams& d = p.d;
-  const size_t bc = (size_t)t.b * p.nchunks + c;
-  unsigned char* base = smem + (size_t)st * l.stage;
-  const uint32_t heads = (uint32_t)(t.nheads * l.head);
-  mbar_arrive_expect_tx(&full[st], (uint32_t)l.kq + heads);
-  bulk_load(smem_u32(base), p.ws_kq + (bc * d.nkheads + t.kh) * (size_t)l.kq, l.kq, &full[st]);
-  bulk_load(smem_u32(base + l.kq), p.ws_head + (bc * d.nheads + t.h0) * (size_t)p.head_bytes, heads,
-            &full[st]);
-}
-
-// The warp is done with a stage: true in the lane that is to refill it, lane 0
-// of the last of the CTA's warps.
-__device__ __forceinline__ bool last_of(unsigned* count, unsigned warps) {
-  __syncwarp();
-  if ((threadIdx.x & 31) != 0) return false;
-  __threadfence_block();
-  const bool last = atomicAdd(count, 1u) == warps - 1;
-  if (last) {
-    *count = 0;
-    __threadfence_block();
-    fence_async_smem();  // reads of the old tiles before the copies over them
-  }
-  return last;
-}
-
-// Both warps of a pair reach this; false for both if either's wait ran out.
-__device__ __forceinline__ bool pair_and(int id, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)ok), "r"(id)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void pair_sync(int id) {
-  asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
-}
-template <int SP>
-__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, uint64_t limit,
-                                           int pair_id) {
-  cp_async_wait_group<0>();  // the warp's own column tiles (visible after the barriers below)
-  bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit));
-  __syncwarp();
-  if (SP == 2) ok = pair_and(pair_id, ok);
-  return ok;
-}
-// A wait ran out at step s: note it, and leave only when the copies already
-// issued have landed (or that wait, too, has run out).
-__device__ __forceinline__ void give_up(const DeltaChunkParams& p, uint64_t* full, int s) {
-  if ((threadIdx.x & 31) == 0) atomicExch(&g_delta_timeout, 1);
-  for (int i = s; i < s + p.stages && i < p.nchunks; ++i)
-    mbar_wait_bounded(&full[i % p.stages], (uint32_t)((i / p.stages) & 1), p.wait_limit_ns);
-}
-
-// x += the partner warp's x, through shared memory (after scaling to true values)
-template <int T>
-__device__ __forceinline__ void put_tiles(const float (&x)[T][4], float* buf, int lane) {
-#pragma unroll
-  for (int j = 0; j < T; ++j)
-    *reinterpret_cast<float4*>(buf + (j * 32 + lane) * 4) =
-        make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
-}
-template <int T>
-__device__ __forceinline__ void add_from(float (&x)[T][4], const float* buf, int lane) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const float4 v = *reinterpret_cast<const float4*>(buf + (j * 32 + lane) * 4);
-    x[j][0] += v.x; x[j][1] += v.y; x[j][2] += v.z; x[j][3] += v.w;
-  }
-}
 
 template <int N, int SP, bool BWD>
 __global__ void __launch_bounds__(256, 1) delta_fwd_kernel(const __grid_constant__ DeltaChunkParams p) {
@@ -866,6 +423,7 @@ bool delta_chunk_supported(int dstate, int headdim) {
 }
 
 cudaError_t launch_delta_chunk_fwd(const DeltaChunkParams& pin, bool bwd, cudaStream_t stream) {
+  if (!getenv("SSM_DELTA_OLD")) return launch_delta_tc(pin, bwd, stream);
   DeltaChunkParams p = pin;
   if (bwd) return p.d.dstate == 64 ? fwd<64, true>(p, stream) : fwd<128, true>(p, stream);
   return p.d.dstate == 64 ? fwd<64, false>(p, stream) : fwd<128, false>(p, stream);
@@ -877,12 +435,11 @@ cudaError_t launch_delta_chunk_rev(const DeltaChunkParams& pin, cudaStream_t str
 }
 
 cudaError_t delta_chunk_status(cudaStream_t stream, int* timed_out) {
-  cudaError_t e = cudaStreamSynchronize(stream);
-  if (e != cudaSuccess) return e;
-  const int zero = 0;
-  e = cudaMemcpyFromSymbol(timed_out, g_delta_timeout, sizeof(int));
-  if (e != cudaSuccess || !*timed_out) return e;
-  return cudaMemcpyToSymbol(g_delta_timeout, &zero, sizeof(int));
+  int tc = 0;
+  cudaError_t e = delta_tc_status(stream, &tc);
+  if (e == cudaSuccess) e = timeout_status(stream, timed_out);
+  *timed_out |= tc;
+  return e;
 }
 
 }  // namespace ssm

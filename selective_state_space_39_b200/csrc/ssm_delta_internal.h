@@ -98,6 +98,9 @@ cudaError_t launch_delta_prep(const DeltaChunkParams& p, bool bwd, cudaStream_t 
 cudaError_t launch_delta_chunk_fwd(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
 cudaError_t launch_delta_chunk_rev(const DeltaChunkParams& p, cudaStream_t stream);
 cudaError_t launch_delta_grad(const DeltaChunkParams& p, cudaStream_t stream);
+// ssm_delta_tc.cu: the forward pass over the chunks on tcgen05
+cudaError_t launch_delta_tc(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
+cudaError_t delta_tc_status(cudaStream_t stream, int* timed_out);
 // Whether a bounded wait gave up since the last call (synchronises the stream).
 cudaError_t delta_chunk_status(cudaStream_t stream, int* timed_out);
 
