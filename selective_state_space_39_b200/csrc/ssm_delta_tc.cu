@@ -268,23 +268,19 @@ __device__ __forceinline__ void issue_loop(const DeltaChunkParams& p, const Cta&
   }
 }
 
-// Largest magnitudes of the rows over both warps of a pair; false when the
-// partner does not come within the limit.
-template <int SP>
-__device__ __forceinline__ bool pair_max(float& m0, float& m1, float* mine, const float* other,
-                                         uint64_t* bar, uint32_t& parity, uint64_t limit, int lane) {
-  if (SP == 1) return true;
+// Largest magnitudes of the rows over both warps of a pair. The pair's barriers
+// have no limit of their own: both warps come to every one of them, also after
+// a wait that ran out (they go on to the end of the chunk), and leave together
+// by the vote.
+__device__ __forceinline__ void put_max(float m0, float m1, float* mine, int lane) {
   if ((lane & 3) == 0) {
     mine[lane >> 2] = m0;
     mine[8 + (lane >> 2)] = m1;
   }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-  const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit));
-  parity ^= 1u;
+}
+__device__ __forceinline__ void get_max(float& m0, float& m1, const float* other, int lane) {
   m0 = fmaxf(m0, other[lane >> 2]);
   m1 = fmaxf(m1, other[8 + (lane >> 2)]);
-  return ok;
 }
 
 constexpr int kRowWarps = 8, kTcThreads = kRowWarps * 32 + 128;
@@ -294,7 +290,7 @@ template <int N, int SP, bool BWD>
 __global__ void __launch_bounds__(kTcThreads, 1)
     delta_tc_kernel(const __grid_constant__ DeltaChunkParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], freed[kMaxStages], bars[kBars], pair[4];
+  __shared__ __align__(8) uint64_t full[kMaxStages], freed[kMaxStages], bars[kBars];
   __shared__ float maxima[3][kRowWarps][16];  // a buffer per use in a chunk
   __shared__ uint32_t slot;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -311,7 +307,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&freed[i], warps);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
     for (int i = 0; i < kBars; ++i)
       mbar_init(&bars[i], (i >= kPutS && i <= kPutP) ? warps : 1u);
     fence_mbar_init();
@@ -357,15 +352,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float S[NS / 8][4], inv0, inv1;  // the state's rows, the inverse of its pieces' scale
       load_state<N, NS>(S, d.h0 ? d.h0 + state_at : nullptr, inv0, inv1, lane);
       scale_rows(S, inv0, inv1);
-      uint32_t pairs = 0;  // parity of the pair's next meeting
       auto meet = [&](float& m0, float& m1, int use) {
-        return pair_max<SP>(m0, m1, mx + use * kRowWarps * 16, ox + use * kRowWarps * 16, &pair[warp & 3],
-                            pairs, p.wait_limit_ns, lane);
+        if (SP == 1) return;
+        put_max(m0, m1, mx + use * kRowWarps * 16, lane);
+        pair_sync(1 + (warp & 3));
+        get_max(m0, m1, ox + use * kRowWarps * 16, lane);
       };
-      auto put_state = [&]() {
+      // the state's pieces, unless a wait has run out in either warp
+      auto put_state = [&](bool ok) {
         float m0, m1;
         row_max(S, m0, m1);
-        if (!meet(m0, m1, 0)) return false;
+        if (SP == 2) {
+          put_max(m0, m1, mx, lane);
+          ok = pair_and(1 + (warp & 3), ok);
+          get_max(m0, m1, ox, lane);
+        }
+        if (!ok) return false;
         const RowScale a = row_scale(exponent_of(m0)), b = row_scale(exponent_of(m1));
         inv0 = a.inv;
         inv1 = b.inv;
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wrote(&bars[kPutS]);
         return true;
       };
-      bool ok = put_state();
+      bool ok = put_state(true);
       int st = 0;
       uint32_t fpar = 0;
       for (int c = 0; ok && c < p.nchunks; ++c) {
@@ -392,9 +394,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
         // ---- R = V - (e^G K) S^T; T R
         float x[TT][4], u[TT][4], y[TT][4];
-        ok = wait_stage<1>(&full[st], fpar, p.wait_limit_ns, 0) &&
-             wait_warp(&bars[kBarK], par, p.wait_limit_ns);
-        if (!ok) break;
+        ok = wait_stage<1>(&full[st], fpar, p.wait_limit_ns, 0);
+        ok = wait_warp(&bars[kBarK], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmX + tcol, x);
         load_rows(u, vrow, tk, m);
         scale_rows(x, -inv0, -inv1);
@@ -402,24 +403,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         add_tiles(x, u);
         float m0, m1;
         row_max(x, m0, m1);
-        ok = meet(m0, m1, 1);
-        if (!ok) break;
+        meet(m0, m1, 1);
         RowScale r0 = row_scale(exponent_of(m0)), r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(x, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
         wrote(&bars[kPutR]);
 
         // ---- meanwhile the next chunk's v, and the readout of the entering state
         if (c + 1 < p.nchunks) fetch(c + 1);
-        ok = wait_warp(&bars[kBarQ], par, p.wait_limit_ns);
-        if (!ok) break;
+        ok = wait_warp(&bars[kBarQ], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmO + tcol, y);
         scale_rows(y, inv0, inv1);
         scale_cols(y, sc + kScSq * kC + tk, lane);
         if (BWD) store_state16<N, NS>(S, p.ws_state16 + st_at, 1.f, 1.f, lane);
 
         // ---- u = beta T R; K^T (e^(G_end - G) u)
-        ok = wait_warp(&bars[kBarT], par, p.wait_limit_ns);
-        if (!ok) break;
+        ok = wait_warp(&bars[kBarT], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmU + hcol, x);
         scale_rows(x, r0.inv, r1.inv);
         if (BWD) {  // r leaves by the rows of v
@@ -435,8 +433,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // e^(G_end - G) <= 1: one scale serves u's pieces for K^T and for P
         scale_cols(x, sc + kScK * kC + tk, lane);
         row_max(x, m0, m1);
-        ok = meet(m0, m1, 2);
-        if (!ok) break;
+        meet(m0, m1, 2);
         r0 = row_scale(exponent_of(m0));
         r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(u, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
@@ -448,26 +445,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
         // ---- S <- e^G_end S + K^T u, and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
-        ok = wait_warp(&bars[kBarU], par, p.wait_limit_ns);
-        if (!ok) break;
+        ok = wait_warp(&bars[kBarU], par, ok ? p.wait_limit_ns : 0) && ok;
+        constexpr int G = NS / 8 < 8 ? NS / 8 : 8;  // tiles per load
 #pragma unroll
-        for (int i = 0; i < NS / 8; i += TT) {
-          tm_load(row + kTmU + hf * NS + 8 * i, u);
+        for (int i = 0; i < NS / 8; i += G) {
+          float ds[G][4];
+          tm_load(row + kTmU + hf * NS + 8 * i, ds);
 #pragma unroll
-          for (int j = 0; j < TT; ++j) {
+          for (int j = 0; j < G; ++j) {
             float(&s)[4] = S[i + j];
             const float2 a = fma2(make_float2(s[0], s[1]), make_float2(end, end),
-                                  mul2(make_float2(u[j][0], u[j][1]), make_float2(r0.inv, r0.inv)));
+                                  mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
             const float2 b = fma2(make_float2(s[2], s[3]), make_float2(end, end),
-                                  mul2(make_float2(u[j][2], u[j][3]), make_float2(r1.inv, r1.inv)));
+                                  mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
             s[0] = a.x; s[1] = a.y; s[2] = b.x; s[3] = b.y;
           }
         }
-        ok = wait_warp(&bars[kBarP], par, p.wait_limit_ns);  // the columns of the pieces are free
-        if (!ok) break;
+        ok = wait_warp(&bars[kBarP], par, ok ? p.wait_limit_ns : 0) && ok;  // the columns of the pieces are free
         const RowScale w0 = r0, w1 = r1;
         const uint32_t ycol = row + kTmY + hcol;
-        if (c + 1 < p.nchunks) ok = put_state();
+        if (c + 1 < p.nchunks) ok = put_state(ok);
         if (!ok) break;
         if (BWD) store_state<N, NS>(S, p.ws_state + st_at, 1.f, 1.f, lane);
 
