@@ -38,8 +38,7 @@ template <int N>
 struct PrepSmem {
   static constexpr int kTile = kC * N * 2;
   static constexpr int kL = kC * kLs * 4;                  // L, then T, of one head
-  static constexpr int kWork = kL + 4 * kDeltaTri;         // and the tiles on their way out
-  static constexpr int kA = 2 * kTile > kWork ? 2 * kTile : kWork;  // over the k/q tiles
+  static constexpr int kA = 2 * kTile > kL ? 2 * kTile : kL;  // over the k/q tiles
   static constexpr int kScal = kHeads * kDeltaScalBwd;
   static constexpr int kTok = 4 * kC * 4;
   static constexpr int kCols = 2 * 3 * kC * 4;             // column factors per row block
@@ -103,7 +102,6 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
   constexpr int RPW = 32 / LPR;    // rows per warp and step
   unsigned char* tiles = smem;
   float* L = reinterpret_cast<float*>(smem);
-  unsigned char* tri = smem + Sm::kL;  // T hi, T lo, P hi, P lo
   float* scal = reinterpret_cast<float*>(smem + Sm::kA);
   float* tok = reinterpret_cast<float*>(smem + Sm::kA + Sm::kScal);  // kmul qmul kn qn
   float* cols = tok + 4 * kC;  // [row block 1..3][P, L] x 64
@@ -244,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
   const int r0 = warp * 16 + (lane >> 2), r1 = r0 + 8;
   constexpr int kTiles = BWD ? 4 : 3;
   for (int x = 0; x < nh; ++x) {
-    __syncthreads();  // the k/q tiles, or the previous head's, are free
+    __syncthreads();  // the k/q tiles, or the previous head's matrix, are free
+    unsigned char* tri = p.ws_head + (bc * d_.nheads + kh * rep + sub * kHeads + x) * (size_t)p.head_bytes;
     float* sc = scal + x * (kDeltaScalBwd / 4);
     const float gh0 = sc[kScGhi * kC + r0], gl0 = sc[kScGlo * kC + r0];
     const float gh1 = sc[kScGhi * kC + r1], gl1 = sc[kScGlo * kC + r1];
@@ -310,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       uint32_t hi0, lo0, hi1, lo1;
       split2(pv[j][0], pv[j][1], s0.s, hi0, lo0);
       split2(pv[j][2], pv[j][3], s1.s, hi1, lo1);
+      // a store of the warp is a whole core matrix: 128 bytes
       unsigned char* ph = tri + 2 * kDeltaTri + delta_tri_block(warp, j >> 1) + (lane & 3) * 4;
       const uint32_t a0 = tri_at(lane >> 2, j & 1), a1 = tri_at((lane >> 2) + 8, j & 1);
       *reinterpret_cast<uint32_t*>(ph + a0) = hi0;
@@ -408,14 +408,10 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
     }
     __syncthreads();
 
-    // ---- out: the tiles, then the factors
-    uint4* out = reinterpret_cast<uint4*>(
-        p.ws_head + (bc * d_.nheads + kh * rep + sub * kHeads + x) * (size_t)p.head_bytes);
-    const uint4* ts = reinterpret_cast<const uint4*>(tri);
-    for (int i = tid; i < kTiles * kDeltaTri / 16; i += kThreads) out[i] = ts[i];
+    // ---- the factors
     const uint4* ss = reinterpret_cast<const uint4*>(sc);
     for (int i = tid; i < (BWD ? kDeltaScalBwd : kDeltaScalFwd) / 16; i += kThreads)
-      out[kTiles * kDeltaTri / 16 + i] = ss[i];
+      reinterpret_cast<uint4*>(tri + kTiles * kDeltaTri)[i] = ss[i];
   }
 }
 
