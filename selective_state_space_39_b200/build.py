@@ -12,13 +12,13 @@ SOURCES = [os.path.join(CSRC, f) for f in ("ssm_scan_kernels.cu", "ssm_scan_bwd.
                                            "ssm_conv1d.cu", "ssm_seqpar.cu", "ssm_ssd.cu",
                                            "ssm_ssd_tc.cu", "ssm_ssd_decode.cu",
                                            "ssm_delta_step.cu", "ssm_delta_prep.cu",
-                                           "ssm_delta_chunk.cu", "ssm_delta_grad.cu", "ssm_norm.cu",
+                                           "ssm_delta_tc.cu", "ssm_delta_grad.cu", "ssm_norm.cu",
                                            "ssm_api.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("ssm_device.cuh", "ssm_internal.h",
                                             "ssm_bwd_internal.h", "ssm_conv_internal.h",
                                             "ssm_seqpar_internal.h", "ssm_ssd_internal.h", "ssm_tc.cuh",
                                             "ssm_ssd_decode_internal.h",
-                                            "ssm_delta_internal.h", "ssm_delta.cuh", "ssm_norm_internal.h")] + [
+                                            "ssm_delta_internal.h", "ssm_delta.cuh", "ssm_delta_rows.cuh", "ssm_norm_internal.h")] + [
     os.path.join(os.path.dirname(HERE), "include", "ssm_scan.h")]
 LIB_PATH = os.path.join(HERE, "libssmscan.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -1104,7 +1104,7 @@ int ssm_gated_delta_fwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t n
     if (aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && (!y || aligned(y, 16))) {
       const DeltaChunkParams cp = delta_chunk_params(p, d, false, workspace);
       cudaError_t e = launch_delta_prep(cp, false, s);
-      if (e == cudaSuccess) e = launch_delta_chunk_fwd(cp, false, s);
+      if (e == cudaSuccess) e = launch_delta_fwd(cp, false, s);
       return cuda_status(e, "gated delta rule launch (chunks)");
     }
   }
@@ -1222,8 +1222,8 @@ int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t n
   cp.ddt_bias = ddt_bias;
   cp.dh0 = dh0;
   cudaError_t e = launch_delta_prep(cp, true, s);
-  if (e == cudaSuccess) e = launch_delta_chunk_fwd(cp, true, s);
-  if (e == cudaSuccess) e = launch_delta_chunk_rev(cp, s);
+  if (e == cudaSuccess) e = launch_delta_fwd(cp, true, s);
+  if (e == cudaSuccess) e = launch_delta_rev(cp, s);
   if (e == cudaSuccess) e = launch_delta_grad(cp, s);
   return cuda_status(e, "gated delta rule backward launch");
 }

@@ -1,7 +1,7 @@
 // ssm_delta_internal.h -- parameters of the gated delta rule shared by the C
-// entry points (ssm_api.cu) and its kernels (ssm_delta_step.cu: token by
-// token; ssm_delta_prep.cu, ssm_delta_chunk.cu, ssm_delta_grad.cu: chunk by
-// chunk). Not part of the public ABI.
+// entry points (ssm_api.cu) and its kernels (ssm_delta_step.cu: token by token;
+// ssm_delta_prep.cu, ssm_delta_tc.cu, ssm_delta_grad.cu: chunk by chunk). Not
+// part of the public ABI.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -63,10 +63,15 @@ constexpr int kDeltaTri = 10 * 512;
 __host__ __device__ constexpr int delta_tri_block(int i, int j) {
   return j * 2048 - 256 * j * (j - 1) + (i - j) * 512;
 }
+// The same of a transposed tile (upper triangular), row of blocks j of block
+// column i: a step over 16 rows of the original reaches its columns 0 .. i.
+__host__ __device__ constexpr int delta_tri_block_t(int i, int j) { return 256 * i * (i + 1) + j * 512; }
 constexpr int kDeltaScalFwd = 7 * kDeltaChunk * 4, kDeltaScalBwd = kScCount * kDeltaChunk * 4;
-// A head block: T hi, T lo, P hi, (backward: P lo,) then the factors.
+// A head block: T hi, T lo, P hi, then the factors; for the backward pass T and P
+// hi and lo, the factors, and the same four tiles transposed.
 constexpr int kDeltaHeadFwd = 3 * kDeltaTri + kDeltaScalFwd;
-constexpr int kDeltaHeadBwd = 4 * kDeltaTri + kDeltaScalBwd;
+constexpr int kDeltaLoadBwd = 4 * kDeltaTri + kDeltaScalBwd;  // what either walk reads
+constexpr int kDeltaHeadBwd = kDeltaLoadBwd + 4 * kDeltaTri;
 
 struct DeltaChunkParams {
   DeltaParams d;
@@ -93,14 +98,12 @@ struct DeltaChunkParams {
   float *dA, *ddt_bias, *dh0;
 };
 
-bool delta_chunk_supported(int dstate, int headdim);
 cudaError_t launch_delta_prep(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
-cudaError_t launch_delta_chunk_fwd(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
-cudaError_t launch_delta_chunk_rev(const DeltaChunkParams& p, cudaStream_t stream);
+// The walk over the chunks (bwd: it keeps what the gradients need), and in reverse.
+bool delta_chunk_supported(int dstate, int headdim);
+cudaError_t launch_delta_fwd(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
+cudaError_t launch_delta_rev(const DeltaChunkParams& p, cudaStream_t stream);
 cudaError_t launch_delta_grad(const DeltaChunkParams& p, cudaStream_t stream);
-// ssm_delta_tc.cu: the forward pass over the chunks on tcgen05
-cudaError_t launch_delta_tc(const DeltaChunkParams& p, bool bwd, cudaStream_t stream);
-cudaError_t delta_tc_status(cudaStream_t stream, int* timed_out);
 // Whether a bounded wait gave up since the last call (synchronises the stream).
 cudaError_t delta_chunk_status(cudaStream_t stream, int* timed_out);
 

@@ -45,6 +45,13 @@ struct PrepSmem {
   static constexpr int kBytes = kA + kScal + kTok + kCols + 64;
 };
 
+// The transpose of the warp's 8 x 8 matrix of 16-bit values.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // tf32 MMA of two-piece fp32 operands: d += a b, hi lo cross terms included.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -105,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
   float* scal = reinterpret_cast<float*>(smem + Sm::kA);
   float* tok = reinterpret_cast<float*>(smem + Sm::kA + Sm::kScal);  // kmul qmul kn qn
   float* cols = tok + 4 * kC;  // [row block 1..3][P, L] x 64
+  float* rows_s = cols;      // T's row scales, once the column factors are spent
   double* carry = reinterpret_cast<double*>(smem + Sm::kA + Sm::kScal + Sm::kTok + Sm::kCols);
   const DeltaParams& d_ = p.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -317,6 +325,13 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       if (BWD) {
         *reinterpret_cast<uint32_t*>(ph + kDeltaTri + a0) = lo0;
         *reinterpret_cast<uint32_t*>(ph + kDeltaTri + a1) = lo1;
+        // P^T: an 8 x 8 matrix and its place are both transposed
+        unsigned char* pt = tri + kDeltaLoadBwd + 2 * kDeltaTri + delta_tri_block_t(warp, j >> 1) +
+                            tri_at((j & 1) * 8 + (lane >> 2), 0) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(pt) = transpose8(hi0);
+        *reinterpret_cast<uint32_t*>(pt + 128) = transpose8(hi1);
+        *reinterpret_cast<uint32_t*>(pt + kDeltaTri) = transpose8(lo0);
+        *reinterpret_cast<uint32_t*>(pt + kDeltaTri + 128) = transpose8(lo1);
       }
     }
     if ((lane & 3) == 0) {
@@ -404,9 +419,24 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       if (half == 0) {
         sc[kScU * kC + row] = sc[kScBeta * kC + row] * s.inv;
         sc[kScT * kC + row] = s.inv;
+        rows_s[row] = s.s;
       }
     }
     __syncthreads();
+    if (BWD) {  // T^T: column `row` of T, eight rows of a block at a time
+      const int row = tid >> 1, half = tid & 1;
+      for (int i = row / 16; i < 4; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = i * 16 + half * 8 + 2 * q;
+          pieces2(L[r * kLs + row] * rows_s[r], L[(r + 1) * kLs + row] * rows_s[r + 1], hi[q], lo[q]);
+        }
+        unsigned char* at = tri + kDeltaLoadBwd + delta_tri_block_t(i, row / 16) + tri_at(row & 15, half);
+        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(at + kDeltaTri) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
 
     // ---- the factors
     const uint4* ss = reinterpret_cast<const uint4*>(sc);

@@ -1,6 +1,7 @@
-// ssm_delta_rows.cuh -- what the chunk kernels of the gated delta rule share:
-// the shared-memory plan and its copies, a warp's 16 rows of the state and of
-// the chunk's matrices as accumulator fragments, bounded waits.
+// ssm_delta_rows.cuh -- what the two walks over the chunks of the gated delta
+// rule share (ssm_delta_tc.cu): the shared-memory plan and its copies, a warp's
+// 16 rows of the state and of the chunk's matrices as accumulator-shaped
+// fragments, bounded waits.
 #pragma once
 
 #include <algorithm>
@@ -33,12 +34,14 @@ constexpr int kMaxBlocks = 8;  // 16-row blocks per CTA
 // buffers of `tiles` column tiles (64 tokens x 16 columns).
 constexpr int kCol = kC * 32;  // bytes of a column tile
 struct Layout {
-  int kq, head, heads, tiles, stage;  // bytes; heads of a CTA; column tiles
+  int kq, head, head_off, heads, tiles, stage;  // bytes; heads of a CTA; column tiles
 };
-// `blocks` 16-row blocks per CTA out of heads of `per_head` blocks each.
+// `blocks` 16-row blocks per CTA out of heads of `per_head` blocks each; the
+// bytes from head_off of every head block.
 __host__ __device__ inline Layout layout(int dstate, int blocks, int per_head, int tiles,
-                                         int head_bytes) {
+                                         int head_bytes, int head_off) {
   Layout l;
+  l.head_off = head_off;
   l.kq = 2 * kC * dstate * 2;
   l.head = head_bytes;
   l.heads = per_head % blocks == 0 ? 1
@@ -49,101 +52,10 @@ __host__ __device__ inline Layout layout(int dstate, int blocks, int per_head, i
   return l;
 }
 
-// Pairs of neighbouring tiles += A times their B fragments. The accumulators of
-// one piece are all visited before the next piece's, so that no MMA waits for
-// the one before it.
-template <int T, int P>
-__device__ __forceinline__ void mma_tiles(float (&acc)[T][4], const uint32_t (&a)[4],
-                                          const uint32_t (&b)[P][4], int t0 = 0) {
-#pragma unroll
-  for (int j = 0; j < P; ++j) {
-    mma_f16(acc[t0 + 2 * j], a, b[j][0], b[j][1]);
-    mma_f16(acc[t0 + 2 * j + 1], a, b[j][2], b[j][3]);
-  }
-}
-
-// Lane's row/unit offsets of the two fragment loads (see swz):
-//   nt: B rows are n          tr: B rows are k (transposing load)
-struct LaneMap {
-  int nt_row, nt_unit, tr_row, tr_unit;
-  uint32_t nt_tri, tr_tri;  // the same inside a block of a triangular tile
-  uint32_t nt_col;          // and of a column tile
-};
-__device__ __forceinline__ LaneMap lane_map(int lane) {
-  LaneMap m;
-  m.nt_row = (lane & 7) + ((lane & 16) >> 1);
-  m.nt_unit = (lane >> 3) & 1;
-  m.tr_row = (lane & 7) + (lane & 8);
-  m.tr_unit = lane >> 4;
-  m.nt_tri = tri_at(m.nt_row, m.nt_unit);
-  m.tr_tri = tri_at(m.tr_row, m.tr_unit);
-  m.nt_col = col_at(m.nt_row, m.nt_unit);
-  return m;
-}
-
-// acc[16 x 8 TT tokens] += x[16 x 64 tokens] B over a triangular tile, x as two
-// pieces, B as one or two. TR false: B[n][k], blocks n >= k, the accumulators
-// holding the tokens from 16 jp0 on; true: B[k][n] (TT = 8, jp0 = 0).
-template <bool TR, bool XLO, bool BLO, int TT>
-__device__ __forceinline__ void tri_product(float (&acc)[TT][4], const float (&x)[8][4], float s0,
-                                            float s1, uint32_t bhi, uint32_t blo, int jp0,
-                                            const LaneMap& m) {
-#pragma unroll
-  for (int kt = 0; kt < 4; ++kt) {
-    uint32_t hi[4], lo[4];
-    if (XLO)
-      split_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi, lo);
-    else
-      half_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi);
-    uint32_t bh[TT / 2][4], bl[TT / 2][4];
-#pragma unroll
-    for (int jj = 0; jj < TT / 2; ++jj) {
-      const int jp = jp0 + jj;
-      if (TR ? jp > kt : jp < kt) continue;  // warp-uniform
-      const uint32_t at = TR ? delta_tri_block(kt, jp) + m.tr_tri : delta_tri_block(jp, kt) + m.nt_tri;
-      if (TR) {
-        ldsm4t(bh[jj], bhi + at);
-        if (BLO) ldsm4t(bl[jj], blo + at);
-      } else {
-        ldsm4(bh[jj], bhi + at);
-        if (BLO) ldsm4(bl[jj], blo + at);
-      }
-    }
-#pragma unroll
-    for (int piece = 0; piece < 3; ++piece) {
-      if ((piece == 1 && !XLO) || (piece == 2 && !BLO)) continue;
-#pragma unroll
-      for (int jj = 0; jj < TT / 2; ++jj) {
-        const int jp = jp0 + jj;
-        if (TR ? jp > kt : jp < kt) continue;
-        const uint32_t(&a)[4] = piece == 1 ? lo : hi;
-        const uint32_t(&b)[4] = piece == 2 ? bl[jj] : bh[jj];
-        mma_f16(acc[2 * jj], a, b[0], b[1]);
-        mma_f16(acc[2 * jj + 1], a, b[2], b[3]);
-      }
-    }
-  }
-}
-
-// s[16 x NS] += x[16 x 64 tokens] tile[64 tokens x N], columns from 8 u0 on, x
-// as two pieces.
-template <int N, int NS>
-__device__ __forceinline__ void state_product(float (&s)[NS / 8][4], const float (&x)[8][4],
-                                              float s0, float s1, uint32_t tile, int u0,
-                                              const LaneMap& m) {
-#pragma unroll
-  for (int kt = 0; kt < 4; ++kt) {
-    uint32_t hi[4], lo[4];
-    split_a(x[2 * kt], x[2 * kt + 1], s0, s1, hi, lo);
-#pragma unroll
-    for (int jn = 0; jn < NS / 16; jn += 2) {
-      uint32_t b[2][4];
-      ldsm4t(b[0], tile + kq_at(16 * kt + m.tr_row, u0 + 2 * jn + m.tr_unit));
-      ldsm4t(b[1], tile + kq_at(16 * kt + m.tr_row, u0 + 2 * jn + 2 + m.tr_unit));
-      mma_tiles(s, hi, b, 2 * jn);
-      mma_tiles(s, lo, b, 2 * jn);
-    }
-  }
+// Byte offset of the lane's row in a fragment load (ldmatrix, stmatrix) of 16
+// tokens of a column tile.
+__device__ __forceinline__ uint32_t lane_col(int lane) {
+  return col_at((lane & 7) + ((lane & 16) >> 1), (lane >> 3) & 1);
 }
 
 // x *= per-row factors (rows g and g + 8)
@@ -179,28 +91,14 @@ __device__ __forceinline__ void add_tiles(float (&x)[T][4], const float (&y)[T][
     x[j][2] = b.x; x[j][3] = b.y;
   }
 }
-template <int T>
-__device__ __forceinline__ void zero(float (&x)[T][4]) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-}
-// The warp's tiles out of all eight: the half `hf` of them when TT is 4.
-template <int TT>
-__device__ __forceinline__ void own(float (&d)[TT][4], const float (&x)[8][4], int hf) {
-#pragma unroll
-  for (int j = 0; j < TT; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) d[j][q] = TT == 8 ? x[j][q] : (hf ? x[4 + (j & 3)][q] : x[j & 3][q]);
-}
-
 // The 16 columns of a column tile [token][p] as fp32 accumulator-shaped values
 // [p][token], tokens t0 .. t0 + 8 T - 1.
 template <int T>
-__device__ __forceinline__ void load_rows(float (&x)[T][4], uint32_t tile, int t0, const LaneMap& m) {
+__device__ __forceinline__ void load_rows(float (&x)[T][4], uint32_t tile, int t0, uint32_t lc) {
 #pragma unroll
   for (int jp = 0; jp < T / 2; ++jp) {
     uint32_t r[4];
-    ldsm4t(r, tile + (t0 + 16 * jp) * 32 + m.nt_col);
+    ldsm4t(r, tile + (t0 + 16 * jp) * 32 + lc);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = 2 * jp + (q >> 1), e = (q & 1) * 2;
@@ -215,7 +113,7 @@ __device__ __forceinline__ void load_rows(float (&x)[T][4], uint32_t tile, int t
 template <int T>
 __device__ __forceinline__ void store_rows(const float (&x)[T][4], uint32_t tile, int t0,
                                            uint16_t* out, size_t out_stride, int valid, int lane,
-                                           const LaneMap& m) {
+                                           uint32_t lc) {
 #pragma unroll
   for (int jp = 0; jp < T / 2; ++jp) {
     uint32_t r[4];
@@ -224,7 +122,7 @@ __device__ __forceinline__ void store_rows(const float (&x)[T][4], uint32_t tile
       const int j = 2 * jp + (q >> 1), e = (q & 1) * 2;
       r[q] = pack_bf16x2(x[j][e], x[j][e + 1]);
     }
-    stsm4t(tile + (t0 + 16 * jp) * 32 + m.nt_col, r);
+    stsm4t(tile + (t0 + 16 * jp) * 32 + lc, r);
   }
   __syncwarp();
 #pragma unroll
@@ -271,55 +169,40 @@ __device__ __forceinline__ void row_dots(const float (&x)[T][4], const float (&y
   }
 }
 
-// The carried rows: s = true value / inv, inv a power of two per row.
+// The warp's 16 rows of NS columns of a state of N columns (zero without src).
 template <int N, int NS>
-__device__ __forceinline__ void load_state(float (&s)[NS / 8][4], const float* src, float& inv0,
-                                           float& inv1, int lane) {
-  if (!src) {
-    zero(s);
-    inv0 = inv1 = 1.f;
-    return;
-  }
+__device__ __forceinline__ void load_state(float (&s)[NS / 8][4], const float* src, int lane) {
   const float* r0 = src + (lane >> 2) * N + 2 * (lane & 3);
 #pragma unroll
   for (int j = 0; j < NS / 8; ++j) {
-    const float2 a = *reinterpret_cast<const float2*>(r0 + 8 * j);
-    const float2 b = *reinterpret_cast<const float2*>(r0 + 8 * N + 8 * j);
+    const float2 z = make_float2(0.f, 0.f);
+    const float2 a = src ? *reinterpret_cast<const float2*>(r0 + 8 * j) : z;
+    const float2 b = src ? *reinterpret_cast<const float2*>(r0 + 8 * N + 8 * j) : z;
     s[j][0] = a.x; s[j][1] = a.y; s[j][2] = b.x; s[j][3] = b.y;
   }
-  float m0, m1;
-  row_max(s, m0, m1);
-  const RowScale a = row_scale<6>(exponent_of(m0)), b = row_scale<6>(exponent_of(m1));
-  scale_rows(s, a.s, b.s);
-  inv0 = a.inv;
-  inv1 = b.inv;
 }
 template <int N, int NS>
-__device__ __forceinline__ void store_state(const float (&s)[NS / 8][4], float* dst, float inv0,
-                                            float inv1, int lane) {
+__device__ __forceinline__ void store_state(const float (&s)[NS / 8][4], float* dst, int lane) {
   float* r0 = dst + (lane >> 2) * N + 2 * (lane & 3);
 #pragma unroll
   for (int j = 0; j < NS / 8; ++j) {
-    *reinterpret_cast<float2*>(r0 + 8 * j) = mul2(make_float2(s[j][0], s[j][1]), make_float2(inv0, inv0));
-    *reinterpret_cast<float2*>(r0 + 8 * N + 8 * j) =
-        mul2(make_float2(s[j][2], s[j][3]), make_float2(inv1, inv1));
+    *reinterpret_cast<float2*>(r0 + 8 * j) = make_float2(s[j][0], s[j][1]);
+    *reinterpret_cast<float2*>(r0 + 8 * N + 8 * j) = make_float2(s[j][2], s[j][3]);
   }
 }
 // The rows as bf16 (for products whose results are bf16).
 template <int N, int NS>
-__device__ __forceinline__ void store_state16(const float (&s)[NS / 8][4], uint16_t* dst, float inv0,
-                                              float inv1, int lane) {
+__device__ __forceinline__ void store_state16(const float (&s)[NS / 8][4], uint16_t* dst, int lane) {
   uint16_t* r0 = dst + (lane >> 2) * N + 2 * (lane & 3);
 #pragma unroll
   for (int j = 0; j < NS / 8; ++j) {
-    *reinterpret_cast<uint32_t*>(r0 + 8 * j) = pack_bf16x2(s[j][0] * inv0, s[j][1] * inv0);
-    *reinterpret_cast<uint32_t*>(r0 + 8 * N + 8 * j) = pack_bf16x2(s[j][2] * inv1, s[j][3] * inv1);
+    *reinterpret_cast<uint32_t*>(r0 + 8 * j) = pack_bf16x2(s[j][0], s[j][1]);
+    *reinterpret_cast<uint32_t*>(r0 + 8 * N + 8 * j) = pack_bf16x2(s[j][2], s[j][3]);
   }
 }
-// <s, src> over the warp's part of the state, src fp32 (all lanes).
+// <s, src> over the warp's part of the state (all lanes).
 template <int N, int NS>
-__device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const float* src, float inv0,
-                                           float inv1, int lane) {
+__device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const float* src, int lane) {
   const float* r0 = src + (lane >> 2) * N + 2 * (lane & 3);
   float2 d0 = make_float2(0.f, 0.f), d1 = d0;
 #pragma unroll
@@ -327,32 +210,10 @@ __device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const fl
     d0 = fma2(make_float2(s[j][0], s[j][1]), *reinterpret_cast<const float2*>(r0 + 8 * j), d0);
     d1 = fma2(make_float2(s[j][2], s[j][3]), *reinterpret_cast<const float2*>(r0 + 8 * N + 8 * j), d1);
   }
-  float d = (d0.x + d0.y) * inv0 + (d1.x + d1.y) * inv1;
+  float d = (d0.x + d0.y) + (d1.x + d1.y);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   return d;
-}
-// Decays the state and brings it under the scale of max(state, terms of
-// largest exponents e0, e1): the sum of 64 terms of k rows below 2 then stays
-// below 2^15.
-struct NewScale {
-  float s0, s1;
-};
-template <int T>
-__device__ __forceinline__ NewScale rescale(float (&s)[T][4], float& inv0, float& inv1,
-                                            uint32_t e0, uint32_t e1, float end) {
-  float m0, m1;
-  row_max(s, m0, m1);
-  const RowScale a = row_scale<6>(max(e0, exponent_of(m0 * inv0)));
-  const RowScale b = row_scale<6>(max(e1, exponent_of(m1 * inv1)));
-  // 2^100: a row that is all zero has no exponent of its own
-  scale_rows(s, end * fminf(inv0 * a.s, 1.2676506e30f), end * fminf(inv1 * b.s, 1.2676506e30f));
-  inv0 = a.inv;
-  inv1 = b.inv;
-  NewScale n;
-  n.s0 = a.s;
-  n.s1 = b.s;
-  return n;
 }
 
 // ---------------------------------------------------------------- the CTA ----
@@ -382,26 +243,12 @@ __device__ __forceinline__ void issue(const DeltaChunkParams& p, const Cta& t, c
   const DeltaParams& d = p.d;
   const size_t bc = (size_t)t.b * p.nchunks + c;
   unsigned char* base = smem + (size_t)st * l.stage;
-  const uint32_t heads = (uint32_t)(t.nheads * l.head);
-  mbar_arrive_expect_tx(&full[st], (uint32_t)l.kq + heads);
+  mbar_arrive_expect_tx(&full[st], (uint32_t)(l.kq + t.nheads * l.head));
   bulk_load(smem_u32(base), p.ws_kq + (bc * d.nkheads + t.kh) * (size_t)l.kq, l.kq, &full[st]);
-  bulk_load(smem_u32(base + l.kq), p.ws_head + (bc * d.nheads + t.h0) * (size_t)p.head_bytes, heads,
-            &full[st]);
-}
-
-// The warp is done with a stage: true in the lane that is to refill it, lane 0
-// of the last of the CTA's warps.
-__device__ __forceinline__ bool last_of(unsigned* count, unsigned warps) {
-  __syncwarp();
-  if ((threadIdx.x & 31) != 0) return false;
-  __threadfence_block();
-  const bool last = atomicAdd(count, 1u) == warps - 1;
-  if (last) {
-    *count = 0;
-    __threadfence_block();
-    fence_async_smem();  // reads of the old tiles before the copies over them
-  }
-  return last;
+  for (int i = 0; i < t.nheads; ++i)
+    bulk_load(smem_u32(base + l.kq + i * l.head),
+              p.ws_head + (bc * d.nheads + t.h0 + i) * (size_t)p.head_bytes + l.head_off, l.head,
+              &full[st]);
 }
 
 // Both warps of a pair reach this; false for both if either's wait ran out.
@@ -418,13 +265,11 @@ __device__ __forceinline__ bool pair_and(int id, bool ok) {
 __device__ __forceinline__ void pair_sync(int id) {
   asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
 }
-template <int SP>
-__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, uint64_t limit,
-                                           int pair_id) {
-  cp_async_wait_group<0>();  // the warp's own column tiles (visible after the barriers below)
-  bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit));
+// The chunk's tiles and the warp's own column tiles are there.
+__device__ __forceinline__ bool wait_stage(uint64_t* bar, uint32_t parity, uint64_t limit) {
+  cp_async_wait_group<0>();
+  const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit));
   __syncwarp();
-  if (SP == 2) ok = pair_and(pair_id, ok);
   return ok;
 }
 // A wait ran out at step s: note it, and leave only when the copies already
@@ -433,23 +278,6 @@ __device__ __forceinline__ void give_up(const DeltaChunkParams& p, uint64_t* ful
   if ((threadIdx.x & 31) == 0) atomicExch(&g_delta_timeout, 1);
   for (int i = s; i < s + p.stages && i < p.nchunks; ++i)
     mbar_wait_bounded(&full[i % p.stages], (uint32_t)((i / p.stages) & 1), p.wait_limit_ns);
-}
-
-// x += the partner warp's x, through shared memory (after scaling to true values)
-template <int T>
-__device__ __forceinline__ void put_tiles(const float (&x)[T][4], float* buf, int lane) {
-#pragma unroll
-  for (int j = 0; j < T; ++j)
-    *reinterpret_cast<float4*>(buf + (j * 32 + lane) * 4) =
-        make_float4(x[j][0], x[j][1], x[j][2], x[j][3]);
-}
-template <int T>
-__device__ __forceinline__ void add_from(float (&x)[T][4], const float* buf, int lane) {
-#pragma unroll
-  for (int j = 0; j < T; ++j) {
-    const float4 v = *reinterpret_cast<const float4*>(buf + (j * 32 + lane) * 4);
-    x[j][0] += v.x; x[j][1] += v.y; x[j][2] += v.z; x[j][3] += v.w;
-  }
 }
 
 // Whether a wait of this file's kernels ran out since the last call.

@@ -1,12 +1,15 @@
 // ssm_delta_tc.cu -- the gated delta rule chunk by chunk on the fifth-generation
-// tensor cores (tcgen05; bf16 io, sm_100a): the forward pass over the chunks,
-// and the same walk for the gradients (BWD: it keeps the states, r and dy.y).
+// tensor cores (tcgen05; bf16 io, sm_100a): the walk over the chunks, alone or
+// for the gradients (BWD: it keeps the states, r and dy.y), and the walk back.
 //
 // Per head, with the operands of ssm_delta_prep.cu and the state S (headdim x
 // dstate) entering a chunk:
 //   R = V - (e^G K) S^T,  r = T R,  u = beta r
 //   Y = (e^G Q) S^T + P u
 //   S <- e^G_end S + u^T (e^(G_end - G) K)
+// and back, dS being the adjoint of the state after the chunk:
+//   dU = P^T dY + e^(G_end - G) K dS^T,  dV = dR = T^T (beta dU)
+//   dS <- e^G_end dS + dY^T (e^G Q) - dR^T (e^G K)
 // All products have the state's rows (output columns p) as their M axis, so
 // that none of them ever meets another row: a CTA takes up to 128 rows (eight
 // 16-row blocks of heads that share a key head), a warp 16 of them. S^T, r^T
@@ -30,9 +33,16 @@
 // P products are taken for both heads on all rows, and a row reads its own
 // head's columns.
 //
-// Tensor memory (512 columns): 0 S pieces, then u's pieces for P; 128 K S, R's
+// Precision: everything on the state's path is a product of two pieces per
+// operand (k and q are exact in one; lo lo is left out), so the carried state,
+// dh0 and the gate gradients keep fp32's accuracy; for y, rounded to bf16, one
+// fp16 piece (2^-12) of S, u and P is taken.
+//
+// Tensor memory (512 columns), forward: 0 S pieces, then u's pieces for P; 128 K S, R's
 // pieces, u's pieces for K^T; 192 Q S; 256 T R per head, then K^T u; 384 P u
-// per head.
+// per head. Back: 0 dS pieces; 128 K dS, dU's pieces, dR's pieces; 192 dY's
+// pieces, for P^T, then for Q^T; 256 P^T dY per head, then the sum for dS; 384
+// T^T dU per head.
 #include <stdlib.h>
 
 #include "ssm_delta_rows.cuh"
@@ -148,13 +158,13 @@ __device__ __forceinline__ void mma_state(uint32_t d, uint32_t a, uint32_t tile)
 }
 // D (rows x dstate) = X (64 tokens, pieces at a and a + 32) tile.
 template <int N>
-__device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t tile) {
+__device__ __forceinline__ void mma_tokens(uint32_t d, uint32_t a, uint32_t tile, bool acc = false) {
   const uint32_t b = (tile >> 4) | ((uint32_t)(kC * 128 / 16) << 16);  // to the next 64 columns
 #pragma unroll
   for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
     for (int ks = 0; ks < kC / 16; ++ks)
-      mma(d, a + piece * 32 + 8 * ks, b + ks * 128, kDescSw, idesc(N, 1), piece + ks > 0);
+      mma(d, a + piece * 32 + 8 * ks, b + ks * 128, kDescSw, idesc(N, 1), acc || piece + ks > 0);
 }
 // D (rows x 64 tokens) = X (64 tokens, pieces at a, a + 32) tri^T, the lower
 // triangular tile in one or two pieces (`lo` after `hi`); a step over 16 tokens
@@ -173,8 +183,24 @@ __device__ __forceinline__ void mma_tri(uint32_t d, uint32_t a, uint32_t tri) {
   }
 }
 
-// mbarriers of a CTA. Products done: K S, Q S, T R, K^T u, P u. Operands
-// written by the row warps: S, R, u for K^T, u for P. A failed CTA's drain.
+// D (rows x 64 tokens) = X (64 tokens, pieces at a, a + 32) tri, from the tile's
+// transpose in two pieces; a step over 16 rows of tri reaches its columns up to
+// them (the last step reaches all, and goes first).
+__device__ __forceinline__ void mma_tri_t(uint32_t d, uint32_t a, uint32_t tri_t) {
+  const uint32_t b = (tri_t >> 4) | ((128u >> 4) << 16);
+#pragma unroll
+  for (int piece = 0; piece < 3; ++piece)
+#pragma unroll
+    for (int kt = 3; kt >= 0; --kt)
+      mma(d, a + (piece == 1 ? 32 : 0) + 8 * kt,
+          b + (delta_tri_block_t(kt, 0) + (piece == 2 ? kDeltaTri : 0)) / 16, kDescTri,
+          idesc(16 * kt + 16, 0), piece > 0 || kt < 3);
+}
+
+// mbarriers of a CTA. Products done, forward: K S, Q S, T R, K^T u, P u; back: K
+// dS, P^T dY, T^T dU, the sum for dS. Operands written by the row warps,
+// forward: S, R, u for K^T, u for P; back: dS, dY for P^T, dU, dR and dY for dS.
+// A failed CTA's drain.
 enum { kBarK, kBarQ, kBarT, kBarU, kBarP, kPutS, kPutR, kPutU, kPutP, kBarDrain, kBars };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -300,7 +326,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pb = d.headdim / 16;
   const Cta t = cta_of(p);
-  const Layout l = layout(N, p.blocks, pb, kTiles, BWD ? kDeltaHeadBwd : kDeltaHeadFwd);
+  const Layout l = layout(N, p.blocks, pb, kTiles, BWD ? kDeltaLoadBwd : kDeltaHeadFwd, 0);
   if (threadIdx.x == 0) {
     const uint32_t warps = (uint32_t)t.active * SP;
     for (int i = 0; i < p.stages; ++i) {
@@ -328,7 +354,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (SP == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     if (blk < t.active) {
       const uint32_t row = tm + ((uint32_t)(32 * (warp & 3) + (SP == 1 ? 16 * (warp >> 2) : 0)) << 16);
-      const LaneMap m = lane_map(lane);
+      const uint32_t lc = lane_col(lane);
       const int rb = t.rb0 + blk, hx = rb / pb;  // row block in the group, its head
       const int h = t.kh * (d.nheads / d.nkheads) + hx, pw = (rb - hx * pb) * 16;
       const int tk = 32 * hf, tcol = 32 * hf;  // first token and its column of an accumulator
@@ -349,9 +375,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         cp_async_commit_group();
       };
       fetch(0);
-      float S[NS / 8][4], inv0, inv1;  // the state's rows, the inverse of its pieces' scale
-      load_state<N, NS>(S, d.h0 ? d.h0 + state_at : nullptr, inv0, inv1, lane);
-      scale_rows(S, inv0, inv1);
+      float S[NS / 8][4], inv0 = 1.f, inv1 = 1.f;  // the state's rows, the inverse of its pieces' scale
+      load_state<N, NS>(S, d.h0 ? d.h0 + state_at : nullptr, lane);
       auto meet = [&](float& m0, float& m1, int use) {
         if (SP == 1) return;
         put_max(m0, m1, mx + use * kRowWarps * 16, lane);
@@ -394,10 +419,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
         // ---- R = V - (e^G K) S^T; T R
         float x[TT][4], u[TT][4], y[TT][4];
-        ok = wait_stage<1>(&full[st], fpar, p.wait_limit_ns, 0);
+        ok = wait_stage(&full[st], fpar, p.wait_limit_ns);
         ok = wait_warp(&bars[kBarK], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmX + tcol, x);
-        load_rows(u, vrow, tk, m);
+        load_rows(u, vrow, tk, lc);
         scale_rows(x, -inv0, -inv1);
         scale_cols(x, sc + kScSk * kC + tk, lane);
         add_tiles(x, u);
@@ -414,7 +439,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_load(row + kTmO + tcol, y);
         scale_rows(y, inv0, inv1);
         scale_cols(y, sc + kScSq * kC + tk, lane);
-        if (BWD) store_state16<N, NS>(S, p.ws_state16 + st_at, 1.f, 1.f, lane);
+        if (BWD) store_state16<N, NS>(S, p.ws_state16 + st_at, lane);
 
         // ---- u = beta T R; K^T (e^(G_end - G) u)
         ok = wait_warp(&bars[kBarT], par, ok ? p.wait_limit_ns : 0) && ok;
@@ -422,7 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         scale_rows(x, r0.inv, r1.inv);
         if (BWD) {  // r leaves by the rows of v
           scale_cols(x, sc + kScT * kC + tk, lane);
-          store_rows(x, vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane, m);
+          store_rows(x, vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane, lc);
         }
         scale_cols(x, sc + (BWD ? kScBeta : kScU) * kC + tk, lane);
 #pragma unroll
@@ -466,7 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t ycol = row + kTmY + hcol;
         if (c + 1 < p.nchunks) ok = put_state(ok);
         if (!ok) break;
-        if (BWD) store_state<N, NS>(S, p.ws_state + st_at, 1.f, 1.f, lane);
+        if (BWD) store_state<N, NS>(S, p.ws_state + st_at, lane);
 
         // ---- Y
         tm_load(ycol, x);
@@ -474,10 +499,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         scale_cols(x, sc + kScP * kC + tk, lane);
         add_tiles(y, x);
         if (BWD) {
-          load_rows(x, vrow + kCol, tk, m);
+          load_rows(x, vrow + kCol, tk, lc);
           row_dots(x, y, p.ws_doto + (bch * pb + pw / 16) * kC + tk, lane);
         } else if (d.y) {
-          store_rows(y, vrow, tk, static_cast<uint16_t*>(d.y) + col_at0 + t0 * vs, vs, valid, lane, m);
+          store_rows(y, vrow, tk, static_cast<uint16_t*>(d.y) + col_at0 + t0 * vs, vs, valid, lane, lc);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&freed[st]);
@@ -489,7 +514,301 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!ok) {
         if (lane == 0) atomicExch(&g_delta_timeout, 1);
       } else if (!BWD && d.h_last) {
-        store_state<N, NS>(S, d.h_last + state_at, 1.f, 1.f, lane);
+        store_state<N, NS>(S, d.h_last + state_at, lane);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tm, kTmemCols);
+}
+
+// The issuing warp of the walk back; step s is chunk nchunks - 1 - s.
+template <int N>
+__device__ __forceinline__ void issue_back(const DeltaChunkParams& p, const Cta& t, const Layout& l,
+                                           unsigned char* smem, uint64_t* full, uint64_t* freed,
+                                           uint64_t* bars, uint32_t tm) {
+  if (elect_one()) {
+    for (int s = 0; s < p.stages && s < p.nchunks; ++s)
+      issue(p, t, l, smem, full, p.nchunks - 1 - s, s);
+  }
+  __syncwarp();
+  const uint32_t s0 = smem_u32(smem);
+  bool ok = true;
+  int s = 0, st = 0, prev = 0;
+  uint32_t fpar = 0, ppar = 0;
+  for (; s < p.nchunks; ++s) {
+    const uint32_t par = (uint32_t)(s & 1);
+    const uint32_t ks = s0 + (uint32_t)(st * l.stage);
+    const uint32_t tiles = ks + (uint32_t)l.kq + (uint32_t)kDeltaScalBwd;  // T^T hi, lo, P^T hi, lo
+    ok = wait_warp(&full[st], fpar, p.wait_limit_ns) && wait_warp(&bars[kPutS], par, p.wait_limit_ns);
+    if (!ok) break;
+    if (elect_one()) {
+      mma_state<N, true>(tm + kTmX, tm + kTmS, ks);
+      tc::commit(&bars[kBarK]);
+    }
+    __syncwarp();
+    ok = wait_warp(&bars[kPutP], par, p.wait_limit_ns);
+    if (!ok) break;
+    if (elect_one()) {
+      mma_tri_t(tm + kTmU, tm + kTmO, tiles + 2 * kDeltaTri);
+      if (t.nheads > 1) mma_tri_t(tm + kTmU + kC, tm + kTmO, tiles + (uint32_t)l.head + 2 * kDeltaTri);
+      tc::commit(&bars[kBarQ]);
+    }
+    __syncwarp();
+    ok = wait_warp(&bars[kPutU], par, p.wait_limit_ns);
+    if (!ok) break;
+    if (elect_one()) {
+      mma_tri_t(tm + kTmY, tm + kTmX, tiles);
+      if (t.nheads > 1) mma_tri_t(tm + kTmY + kC, tm + kTmX, tiles + (uint32_t)l.head);
+      tc::commit(&bars[kBarT]);
+    }
+    __syncwarp();
+    if (s > 0 && s - 1 + p.stages < p.nchunks) {
+      ok = wait_warp(&freed[prev], ppar, p.wait_limit_ns);
+      if (!ok) break;
+      if (elect_one()) {
+        fence_async_smem();
+        issue(p, t, l, smem, full, p.nchunks - (s + p.stages), prev);
+      }
+      __syncwarp();
+    }
+    ok = wait_warp(&bars[kPutR], par, p.wait_limit_ns);
+    if (!ok) break;
+    if (elect_one()) {
+      mma_tokens<N>(tm + kTmU, tm + kTmO, ks + (uint32_t)(l.kq / 2));
+      mma_tokens<N>(tm + kTmU, tm + kTmX, ks, true);
+      tc::commit(&bars[kBarU]);
+    }
+    __syncwarp();
+    prev = st;
+    ppar = fpar;
+    if (++st == p.stages) {
+      st = 0;
+      fpar ^= 1u;
+    }
+  }
+  if (!ok) {
+    if (elect_one()) tc::commit(&bars[kBarDrain]);
+    __syncwarp();
+    mbar_wait_bounded(&bars[kBarDrain], 0, p.wait_limit_ns);
+    give_up(p, full, s);
+  }
+}
+
+template <int N, int SP>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    delta_back_kernel(const __grid_constant__ DeltaChunkParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], freed[kMaxStages], bars[kBars];
+  __shared__ float maxima[4][kRowWarps][16];
+  __shared__ uint32_t slot;
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  constexpr int NS = N / SP, TT = 8 / SP, kTiles = 3;  // column tiles: v, dy, r
+  const DeltaParams& d = p.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pb = d.headdim / 16;
+  const Cta t = cta_of(p);
+  const Layout l = layout(N, p.blocks, pb, kTiles, kDeltaLoadBwd, 4 * kDeltaTri);
+  if (threadIdx.x == 0) {
+    const uint32_t warps = (uint32_t)t.active * SP;
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&freed[i], warps);
+    }
+    for (int i = 0; i < kBars; ++i)
+      mbar_init(&bars[i], (i >= kPutS && i <= kPutP) ? warps : 1u);
+    fence_mbar_init();
+  }
+  if (warp == 0) tc::tmem_alloc(&slot, kTmemCols);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tm = __shfl_sync(0xffffffffu, slot, 0);
+
+  const int blk = SP == 2 ? warp & 3 : warp, hf = SP == 2 ? (warp >> 2) & 1 : 0;
+  if (warp >= kRowWarps) {
+    if (SP == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");  // as in the walk forward
+    if (warp == kRowWarps) issue_back<N>(p, t, l, smem, full, freed, bars, tm);
+  } else {
+    if (SP == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if (blk < t.active) {
+      const uint32_t row = tm + ((uint32_t)(32 * (warp & 3) + (SP == 1 ? 16 * (warp >> 2) : 0)) << 16);
+      const uint32_t lc = lane_col(lane);
+      const int rb = t.rb0 + blk, hx = rb / pb;
+      const int h = t.kh * (d.nheads / d.nkheads) + hx, pw = (rb - hx * pb) * 16;
+      const int tk = 32 * hf, tcol = 32 * hf;
+      const uint32_t hcol = (uint32_t)(h - t.h0) * kC + tcol;
+      const size_t part = (size_t)pw * N + hf * NS;
+      const size_t state_at = ((size_t)t.b * d.nheads + h) * ((size_t)d.headdim * N) + part;
+      const size_t vs = (size_t)d.nheads * d.headdim;
+      const uint32_t col0 = smem_u32(smem + (size_t)p.stages * l.stage) + blk * 2 * kTiles * kCol;
+      const size_t col_at0 = (size_t)t.b * d.seqlen * vs + (size_t)h * d.headdim + pw;
+      float* const mx = &maxima[0][warp][0];
+      const float* const ox = &maxima[0][warp ^ 4][0];
+      auto fetch = [&](int c) {
+        const int valid = (int)min((int64_t)kC, d.seqlen - (int64_t)c * kC);
+        const size_t at = col_at0 + (size_t)c * kC * vs;
+        const uint32_t to = col0 + (c & 1) * kTiles * kCol;
+        fetch_rows<TT>(to, static_cast<const uint16_t*>(d.v) + at, vs, tk, valid, lane);
+        fetch_rows<TT>(to + kCol, p.dy + at, vs, tk, valid, lane);
+        fetch_rows<TT>(to + 2 * kCol, p.ws_r + at, vs, tk, valid, lane);
+        cp_async_commit_group();
+      };
+      fetch(p.nchunks - 1);
+      float S[NS / 8][4], inv0 = 1.f, inv1 = 1.f;  // the rows of dS
+      load_state<N, NS>(S, p.dh_last ? p.dh_last + state_at : nullptr, lane);
+      auto meet = [&](float& m0, float& m1, int use) {
+        if (SP == 1) return;
+        put_max(m0, m1, mx + use * kRowWarps * 16, lane);
+        pair_sync(1 + (warp & 3));
+        get_max(m0, m1, ox + use * kRowWarps * 16, lane);
+      };
+      auto put_state = [&](bool ok) {
+        float m0, m1;
+        row_max(S, m0, m1);
+        if (SP == 2) {
+          put_max(m0, m1, mx, lane);
+          ok = pair_and(1 + (warp & 3), ok);
+          get_max(m0, m1, ox, lane);
+        }
+        if (!ok) return false;
+        const RowScale a = row_scale(exponent_of(m0)), b = row_scale(exponent_of(m1));
+        inv0 = a.inv;
+        inv1 = b.inv;
+        constexpr int G = NS / 8 < 8 ? NS / 8 : 8;
+#pragma unroll
+        for (int i = 0; i < NS / 8; i += G)
+          tm_pieces<true, G>(&S[i], a.s, b.s, row + kTmS + hf * (NS / 2) + 4 * i,
+                             row + kTmS + N / 2 + hf * (NS / 2) + 4 * i);
+        wrote(&bars[kPutS]);
+        return true;
+      };
+      bool ok = put_state(true);
+      int st = 0;
+      uint32_t fpar = 0;
+      for (int s = 0; ok && s < p.nchunks; ++s) {
+        const int c = p.nchunks - 1 - s;
+        const uint32_t par = (uint32_t)(s & 1);
+        const size_t bch = ((size_t)t.b * p.nchunks + c) * d.nheads + h;
+        const size_t st_at = bch * ((size_t)d.headdim * N) + part;
+        const size_t dot_at = (bch * pb + pw / 16) * kC + tk;
+        const int64_t t0 = (int64_t)c * kC;
+        const int valid = (int)min((int64_t)kC, d.seqlen - t0);
+        const float* sc = reinterpret_cast<const float*>(smem + (size_t)st * l.stage + l.kq +
+                                                         (h - t.h0) * l.head);
+        const uint32_t vrow = col0 + (c & 1) * kTiles * kCol;
+
+        // ---- dY for P^T
+        float x[TT][4], u[TT][4], y[TT][4], m0, m1;
+        ok = wait_stage(&full[st], fpar, p.wait_limit_ns);
+        load_rows(y, vrow + kCol, tk, lc);
+        scale_cols(y, sc + kScP * kC + tk, lane);
+        row_max(y, m0, m1);
+        meet(m0, m1, 1);
+        RowScale r0 = row_scale(exponent_of(m0)), r1 = row_scale(exponent_of(m1));
+        tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
+        wrote(&bars[kPutP]);
+
+        // ---- dU = P^T dY + e^(G_end - G) K dS^T
+        ok = wait_warp(&bars[kBarK], par, ok ? p.wait_limit_ns : 0) && ok;
+        tm_load(row + kTmX + tcol, x);
+        scale_rows(x, inv0, inv1);
+        scale_cols(x, sc + kScKend * kC + tk, lane);
+        ok = wait_warp(&bars[kBarQ], par, ok ? p.wait_limit_ns : 0) && ok;
+        tm_load(row + kTmU + hcol, u);
+        scale_rows(u, r0.inv, r1.inv);
+        scale_cols(u, sc + kScK * kC + tk, lane);
+        add_tiles(u, x);
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x[j][q] = u[j][q];
+        scale_cols(x, sc + kScU * kC + tk, lane);
+        row_max(x, m0, m1);
+        meet(m0, m1, 2);
+        r0 = row_scale(exponent_of(m0));
+        r1 = row_scale(exponent_of(m1));
+        tm_pieces<true, TT>(x, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
+        wrote(&bars[kPutU]);
+
+        // ---- meanwhile: the next chunk's rows, du.r, dS for the gradients, <S, dS>
+        if (c > 0) fetch(c - 1);
+        load_rows(x, vrow + 2 * kCol, tk, lc);
+        row_dots(u, x, p.ws_dotu + dot_at, lane);
+        store_state16<N, NS>(S, p.ws_dstate16 + st_at, lane);
+        const float dot = state_dot<N, NS>(S, p.ws_state + st_at, lane);
+        if (lane == 0) {
+          p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
+          if (SP == 1) p.ws_end[(bch * pb + pw / 16) * 2 + 1] = 0.f;
+        }
+        load_rows(y, vrow + kCol, tk, lc);
+        scale_cols(y, sc + kScSq * kC + tk, lane);
+
+        // ---- dV = dR = T^T (beta dU); dY and -dR under one scale for the sum of dS
+        ok = wait_warp(&bars[kBarT], par, ok ? p.wait_limit_ns : 0) && ok;
+        tm_load(row + kTmY + hcol, x);
+        scale_rows(x, r0.inv, r1.inv);
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) u[j][q] = -x[j][q];
+        scale_cols(u, sc + kScSk * kC + tk, lane);
+        float n0, n1;
+        row_max(y, n0, n1);
+        row_max(u, m0, m1);
+        m0 = fmaxf(m0, n0);
+        m1 = fmaxf(m1, n1);
+        meet(m0, m1, 3);
+        r0 = row_scale(exponent_of(m0));
+        r1 = row_scale(exponent_of(m1));
+        tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
+        tm_pieces<true, TT>(u, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
+        wrote(&bars[kPutR]);
+        load_rows(u, vrow, tk, lc);
+        row_dots(x, u, p.ws_dotv + dot_at, lane);
+        __syncwarp();
+        store_rows(x, vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane, lc);
+        if (c > 0) {  // the next chunk's state on its way from DRAM: 128 bytes per prefetch
+          const float* nx = p.ws_state + (st_at - (size_t)d.nheads * d.headdim * N);
+#pragma unroll
+          for (int i = 0; i < 16 * NS / 32; i += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + (size_t)((i + lane) / (NS / 32)) * N +
+                                                          (i + lane) % (NS / 32) * 32));
+        }
+
+        // ---- dS <- e^G_end dS + dY^T (e^G Q) - dR^T (e^G K), and its pieces for the next chunk
+        const float end = sc[kScEnd * kC];
+        ok = wait_warp(&bars[kBarU], par, ok ? p.wait_limit_ns : 0) && ok;
+        constexpr int G = NS / 8 < 8 ? NS / 8 : 8;
+#pragma unroll
+        for (int i = 0; i < NS / 8; i += G) {
+          float ds[G][4];
+          tm_load(row + kTmU + hf * NS + 8 * i, ds);
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            float(&q)[4] = S[i + j];
+            const float2 a = fma2(make_float2(q[0], q[1]), make_float2(end, end),
+                                  mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
+            const float2 b = fma2(make_float2(q[2], q[3]), make_float2(end, end),
+                                  mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
+            q[0] = a.x; q[1] = a.y; q[2] = b.x; q[3] = b.y;
+          }
+        }
+        if (c > 0) ok = put_state(ok);
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&freed[st]);
+        if (++st == p.stages) {
+          st = 0;
+          fpar ^= 1u;
+        }
+      }
+      if (!ok) {
+        if (lane == 0) atomicExch(&g_delta_timeout, 1);
+      } else if (p.dh0) {
+        store_state<N, NS>(S, p.dh0 + state_at, lane);
       }
     }
   }
@@ -502,12 +821,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // The largest number of row blocks per CTA (one CTA fills an SM) of at most two
 // heads and two stages, halved while the grid then still is no larger than the
 // SMs: the chain is shorter with fewer warps per scheduler.
-template <int N, bool BWD>
-cudaError_t run(DeltaChunkParams p, cudaStream_t stream) {
+template <int N, typename K1, typename K2>
+cudaError_t run(K1* one, K2* two, DeltaChunkParams p, int tiles, int head_bytes, cudaStream_t stream) {
   const int per_head = p.d.headdim / 16, group = p.d.nheads / p.d.nkheads * per_head;
   const int64_t groups = (int64_t)p.d.batch * p.d.nkheads;
-  const int tiles = BWD ? 2 : 1, head_bytes = BWD ? kDeltaHeadBwd : kDeltaHeadFwd;
-  auto lay = [&](int blocks) { return layout(N, blocks, per_head, tiles, head_bytes); };
+  auto lay = [&](int blocks) { return layout(N, blocks, per_head, tiles, head_bytes, 0); };
   auto extra = [&](int blocks) { return blocks * 2 * tiles * kCol + 1024; };
   auto stages_of = [&](int blocks) {
     return std::min(kMaxStages, (224 * 1024 - extra(blocks)) / lay(blocks).stage);
@@ -530,17 +848,34 @@ cudaError_t run(DeltaChunkParams p, cudaStream_t stream) {
     kern<<<(unsigned)ctas(blocks), kTcThreads, bytes, stream>>>(p);
     return cudaGetLastError();
   };
-  return blocks <= 4 ? go(delta_tc_kernel<N, 2, BWD>) : go(delta_tc_kernel<N, 1, BWD>);
+  return blocks <= 4 ? go(two) : go(one);
+}
+template <int N, bool BWD>
+cudaError_t fwd(const DeltaChunkParams& p, cudaStream_t stream) {
+  return run<N>(delta_tc_kernel<N, 1, BWD>, delta_tc_kernel<N, 2, BWD>, p, BWD ? 2 : 1,
+                BWD ? kDeltaLoadBwd : kDeltaHeadFwd, stream);
+}
+template <int N>
+cudaError_t rev(const DeltaChunkParams& p, cudaStream_t stream) {
+  return run<N>(delta_back_kernel<N, 1>, delta_back_kernel<N, 2>, p, 3, kDeltaLoadBwd, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_tc(const DeltaChunkParams& p, bool bwd, cudaStream_t stream) {
-  if (bwd) return p.d.dstate == 64 ? run<64, true>(p, stream) : run<128, true>(p, stream);
-  return p.d.dstate == 64 ? run<64, false>(p, stream) : run<128, false>(p, stream);
+bool delta_chunk_supported(int dstate, int headdim) {
+  return (dstate == 64 || dstate == 128) && headdim % 16 == 0 && headdim >= 16;
 }
 
-cudaError_t delta_tc_status(cudaStream_t stream, int* timed_out) {
+cudaError_t launch_delta_fwd(const DeltaChunkParams& p, bool bwd, cudaStream_t stream) {
+  if (bwd) return p.d.dstate == 64 ? fwd<64, true>(p, stream) : fwd<128, true>(p, stream);
+  return p.d.dstate == 64 ? fwd<64, false>(p, stream) : fwd<128, false>(p, stream);
+}
+
+cudaError_t launch_delta_rev(const DeltaChunkParams& p, cudaStream_t stream) {
+  return p.d.dstate == 64 ? rev<64>(p, stream) : rev<128>(p, stream);
+}
+
+cudaError_t delta_chunk_status(cudaStream_t stream, int* timed_out) {
   return timeout_status(stream, timed_out);
 }
 
