@@ -109,11 +109,9 @@ __device__ __forceinline__ void load_rows(float (&x)[T][4], uint32_t tile, int t
 }
 
 // Accumulator-shaped values [p][token] of tokens t0 .. -> bf16 rows of a column
-// tile, then to global memory (32 bytes a token).
+// tile, and (after it) those rows to global memory, 32 bytes a token.
 template <int T>
-__device__ __forceinline__ void store_rows(const float (&x)[T][4], uint32_t tile, int t0,
-                                           uint16_t* out, size_t out_stride, int valid, int lane,
-                                           uint32_t lc) {
+__device__ __forceinline__ void stage_rows(const float (&x)[T][4], uint32_t tile, int t0, uint32_t lc) {
 #pragma unroll
   for (int jp = 0; jp < T / 2; ++jp) {
     uint32_t r[4];
@@ -125,6 +123,10 @@ __device__ __forceinline__ void store_rows(const float (&x)[T][4], uint32_t tile
     stsm4t(tile + (t0 + 16 * jp) * 32 + lc, r);
   }
   __syncwarp();
+}
+template <int T>
+__device__ __forceinline__ void store_rows(uint32_t tile, int t0, uint16_t* out, size_t out_stride,
+                                           int valid, int lane) {
 #pragma unroll
   for (int it = 0; it < T / 2; ++it) {
     const int tk = t0 + it * 16 + (lane >> 1), u = lane & 1;
@@ -200,15 +202,27 @@ __device__ __forceinline__ void store_state16(const float (&s)[NS / 8][4], uint1
     *reinterpret_cast<uint32_t*>(r0 + 8 * N + 8 * j) = pack_bf16x2(s[j][2], s[j][3]);
   }
 }
-// <s, src> over the warp's part of the state (all lanes).
+// The warp's part of a state (16 rows of NS columns of N), asynchronously into
+// rows of NS + 8 floats in shared memory, and <s, it> (all lanes).
 template <int N, int NS>
-__device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const float* src, int lane) {
-  const float* r0 = src + (lane >> 2) * N + 2 * (lane & 3);
+__device__ __forceinline__ void fetch_state(uint32_t to, const float* src, int lane) {
+#pragma unroll
+  for (int i = lane; i < 16 * NS / 4; i += 32) {
+    const int row = i / (NS / 4), u = i % (NS / 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + row * (NS + 8) * 4 + u * 16),
+                 "l"(src + (size_t)row * N + u * 4)
+                 : "memory");
+  }
+}
+template <int NS>
+__device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const float* rows, int lane) {
+  const float* r0 = rows + (lane >> 2) * (NS + 8) + 2 * (lane & 3);
   float2 d0 = make_float2(0.f, 0.f), d1 = d0;
 #pragma unroll
   for (int j = 0; j < NS / 8; ++j) {
     d0 = fma2(make_float2(s[j][0], s[j][1]), *reinterpret_cast<const float2*>(r0 + 8 * j), d0);
-    d1 = fma2(make_float2(s[j][2], s[j][3]), *reinterpret_cast<const float2*>(r0 + 8 * N + 8 * j), d1);
+    d1 = fma2(make_float2(s[j][2], s[j][3]),
+              *reinterpret_cast<const float2*>(r0 + 8 * (NS + 8) + 8 * j), d1);
   }
   float d = (d0.x + d0.y) + (d1.x + d1.y);
 #pragma unroll

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         scale_rows(x, r0.inv, r1.inv);
         if (BWD) {  // r leaves by the rows of v
           scale_cols(x, sc + kScT * kC + tk, lane);
-          store_rows(x, vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane, lc);
+          stage_rows(x, vrow, tk, lc);
         }
         scale_cols(x, sc + (BWD ? kScBeta : kScU) * kC + tk, lane);
 #pragma unroll
@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- P u
         tm_pieces<BWD, TT>(x, r0.s, r1.s, row + kTmS + tcol / 2, row + kTmS + 32 + tcol / 2);
         wrote(&bars[kPutP]);
+        if (BWD) store_rows<TT>(vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane);
 
         // ---- S <- e^G_end S + K^T u, and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
@@ -502,7 +503,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           load_rows(x, vrow + kCol, tk, lc);
           row_dots(x, y, p.ws_doto + (bch * pb + pw / 16) * kC + tk, lane);
         } else if (d.y) {
-          store_rows(y, vrow, tk, static_cast<uint16_t*>(d.y) + col_at0 + t0 * vs, vs, valid, lane, lc);
+          stage_rows(y, vrow, tk, lc);
+          store_rows<TT>(vrow, tk, static_cast<uint16_t*>(d.y) + col_at0 + t0 * vs, vs, valid, lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&freed[st]);
@@ -597,7 +599,8 @@ __device__ __forceinline__ void issue_back(const DeltaChunkParams& p, const Cta&
   }
 }
 
-template <int N, int SP>
+// Two warps share a block of 16 rows; up to four blocks.
+template <int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
     delta_back_kernel(const __grid_constant__ DeltaChunkParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -605,14 +608,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ float maxima[4][kRowWarps][16];
   __shared__ uint32_t slot;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  constexpr int NS = N / SP, TT = 8 / SP, kTiles = 3;  // column tiles: v, dy, r
+  constexpr int NS = N / 2, TT = 4, kTiles = 3;  // column tiles: v, dy, r
   const DeltaParams& d = p.d;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pb = d.headdim / 16;
   const Cta t = cta_of(p);
   const Layout l = layout(N, p.blocks, pb, kTiles, kDeltaLoadBwd, 4 * kDeltaTri);
   if (threadIdx.x == 0) {
-    const uint32_t warps = (uint32_t)t.active * SP;
+    const uint32_t warps = (uint32_t)t.active * 2;
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&freed[i], warps);
@@ -627,14 +630,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_after_sync();
   const uint32_t tm = __shfl_sync(0xffffffffu, slot, 0);
 
-  const int blk = SP == 2 ? warp & 3 : warp, hf = SP == 2 ? (warp >> 2) & 1 : 0;
+  const int blk = warp & 3, hf = (warp >> 2) & 1;
   if (warp >= kRowWarps) {
-    if (SP == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");  // as in the walk forward
     if (warp == kRowWarps) issue_back<N>(p, t, l, smem, full, freed, bars, tm);
   } else {
-    if (SP == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     if (blk < t.active) {
-      const uint32_t row = tm + ((uint32_t)(32 * (warp & 3) + (SP == 1 ? 16 * (warp >> 2) : 0)) << 16);
+      const uint32_t row = tm + ((uint32_t)(32 * blk) << 16);
       const uint32_t lc = lane_col(lane);
       const int rb = t.rb0 + blk, hx = rb / pb;
       const int h = t.kh * (d.nheads / d.nkheads) + hx, pw = (rb - hx * pb) * 16;
@@ -647,7 +648,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const size_t col_at0 = (size_t)t.b * d.seqlen * vs + (size_t)h * d.headdim + pw;
       float* const mx = &maxima[0][warp][0];
       const float* const ox = &maxima[0][warp ^ 4][0];
+      // the state after the chunk, for its product with dS
+      float* const rows = reinterpret_cast<float*>(smem + (size_t)p.stages * l.stage +
+                                                   p.blocks * 2 * kTiles * kCol) + (blk * 2 + hf) * 16 * (NS + 8);
       auto fetch = [&](int c) {
+        fetch_state<N, NS>(smem_u32(rows), p.ws_state + (((size_t)t.b * p.nchunks + c) * d.nheads + h) *
+                                                            ((size_t)d.headdim * N) + part, lane);
         const int valid = (int)min((int64_t)kC, d.seqlen - (int64_t)c * kC);
         const size_t at = col_at0 + (size_t)c * kC * vs;
         const uint32_t to = col0 + (c & 1) * kTiles * kCol;
@@ -660,19 +666,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float S[NS / 8][4], inv0 = 1.f, inv1 = 1.f;  // the rows of dS
       load_state<N, NS>(S, p.dh_last ? p.dh_last + state_at : nullptr, lane);
       auto meet = [&](float& m0, float& m1, int use) {
-        if (SP == 1) return;
         put_max(m0, m1, mx + use * kRowWarps * 16, lane);
-        pair_sync(1 + (warp & 3));
+        pair_sync(1 + blk);
         get_max(m0, m1, ox + use * kRowWarps * 16, lane);
       };
       auto put_state = [&](bool ok) {
         float m0, m1;
         row_max(S, m0, m1);
-        if (SP == 2) {
-          put_max(m0, m1, mx, lane);
-          ok = pair_and(1 + (warp & 3), ok);
-          get_max(m0, m1, ox, lane);
-        }
+        put_max(m0, m1, mx, lane);
+        ok = pair_and(1 + blk, ok);
+        get_max(m0, m1, ox, lane);
         if (!ok) return false;
         const RowScale a = row_scale(exponent_of(m0)), b = row_scale(exponent_of(m1));
         inv0 = a.inv;
@@ -734,15 +737,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wrote(&bars[kPutU]);
 
         // ---- meanwhile: the next chunk's rows, du.r, dS for the gradients, <S, dS>
+        const float dot = state_dot<NS>(S, rows, lane);
+        if (lane == 0) p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
+        __syncwarp();
         if (c > 0) fetch(c - 1);
         load_rows(x, vrow + 2 * kCol, tk, lc);
         row_dots(u, x, p.ws_dotu + dot_at, lane);
         store_state16<N, NS>(S, p.ws_dstate16 + st_at, lane);
-        const float dot = state_dot<N, NS>(S, p.ws_state + st_at, lane);
-        if (lane == 0) {
-          p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
-          if (SP == 1) p.ws_end[(bch * pb + pw / 16) * 2 + 1] = 0.f;
-        }
         load_rows(y, vrow + kCol, tk, lc);
         scale_cols(y, sc + kScSq * kC + tk, lane);
 
@@ -769,15 +770,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         load_rows(u, vrow, tk, lc);
         row_dots(x, u, p.ws_dotv + dot_at, lane);
         __syncwarp();
-        store_rows(x, vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane, lc);
-        if (c > 0) {  // the next chunk's state on its way from DRAM: 128 bytes per prefetch
-          const float* nx = p.ws_state + (st_at - (size_t)d.nheads * d.headdim * N);
-#pragma unroll
-          for (int i = 0; i < 16 * NS / 32; i += 32)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(nx + (size_t)((i + lane) / (NS / 32)) * N +
-                                                          (i + lane) % (NS / 32) * 32));
-        }
-
+        stage_rows(x, vrow, tk, lc);
+        store_rows<TT>(vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane);
         // ---- dS <- e^G_end dS + dY^T (e^G Q) - dR^T (e^G K), and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
         ok = wait_warp(&bars[kBarU], par, ok ? p.wait_limit_ns : 0) && ok;
@@ -820,44 +814,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // The largest number of row blocks per CTA (one CTA fills an SM) of at most two
 // heads and two stages, halved while the grid then still is no larger than the
-// SMs: the chain is shorter with fewer warps per scheduler.
-template <int N, typename K1, typename K2>
-cudaError_t run(K1* one, K2* two, DeltaChunkParams p, int tiles, int head_bytes, cudaStream_t stream) {
+// SMs: the chain is shorter with fewer warps per scheduler. `one`: the kernel of
+// one warp per block, taken above four blocks; null where there is none.
+// block_bytes: shared memory per row block beside its column tiles.
+template <int N, typename K>
+cudaError_t run(K* one, K* two, DeltaChunkParams p, int tiles, int head_bytes, int block_bytes,
+                cudaStream_t stream) {
   const int per_head = p.d.headdim / 16, group = p.d.nheads / p.d.nkheads * per_head;
   const int64_t groups = (int64_t)p.d.batch * p.d.nkheads;
   auto lay = [&](int blocks) { return layout(N, blocks, per_head, tiles, head_bytes, 0); };
-  auto extra = [&](int blocks) { return blocks * 2 * tiles * kCol + 1024; };
+  auto extra = [&](int blocks) { return blocks * (2 * tiles * kCol + block_bytes) + 1024; };
   auto stages_of = [&](int blocks) {
     return std::min(kMaxStages, (224 * 1024 - extra(blocks)) / lay(blocks).stage);
   };
   auto ctas = [&](int blocks) { return groups * ((group + blocks - 1) / blocks); };
-  int blocks = kMaxBlocks;
+  int blocks = one ? kMaxBlocks : 4;
   while (blocks > 1 && (blocks / 2 >= group || lay(blocks).heads > kTcHeads || stages_of(blocks) < 2 ||
                         ctas(blocks / 2) <= 148))
     blocks /= 2;
   const char* force = getenv("SSM_DELTA_BLOCKS");
-  if (force && *force && lay(atoi(force)).heads <= kTcHeads && stages_of(atoi(force)) >= 2) blocks = atoi(force);
+  if (force && *force && (one || atoi(force) <= 4) && lay(atoi(force)).heads <= kTcHeads && stages_of(atoi(force)) >= 2) blocks = atoi(force);
   p.blocks = blocks;
   p.stages = stages_of(blocks);
   if (p.stages < 2) return cudaErrorInvalidValue;
   const int bytes = lay(blocks).stage * p.stages + extra(blocks);
-  auto go = [&](auto* kern) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    kern<<<(unsigned)ctas(blocks), kTcThreads, bytes, stream>>>(p);
-    return cudaGetLastError();
-  };
-  return blocks <= 4 ? go(two) : go(one);
+  K* kern = blocks <= 4 ? two : one;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)ctas(blocks), kTcThreads, bytes, stream>>>(p);
+  return cudaGetLastError();
 }
 template <int N, bool BWD>
 cudaError_t fwd(const DeltaChunkParams& p, cudaStream_t stream) {
   return run<N>(delta_tc_kernel<N, 1, BWD>, delta_tc_kernel<N, 2, BWD>, p, BWD ? 2 : 1,
-                BWD ? kDeltaLoadBwd : kDeltaHeadFwd, stream);
+                BWD ? kDeltaLoadBwd : kDeltaHeadFwd, 0, stream);
 }
 template <int N>
 cudaError_t rev(const DeltaChunkParams& p, cudaStream_t stream) {
-  return run<N>(delta_back_kernel<N, 1>, delta_back_kernel<N, 2>, p, 3, kDeltaLoadBwd, stream);
+  return run<N, void(DeltaChunkParams)>(nullptr, delta_back_kernel<N>, p, 3, kDeltaLoadBwd,
+                                        2 * 16 * (N / 2 + 8) * 4, stream);
 }
 
 }  // namespace
