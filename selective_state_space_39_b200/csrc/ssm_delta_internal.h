@@ -85,8 +85,8 @@ struct DeltaChunkParams {
   // backward only
   const uint16_t* dy;    // (batch, seqlen, nheads, headdim)
   const float* dh_last;  // or null
-  float* ws_state;       // (batch, nchunks, nheads, headdim, dstate): state after each chunk
-  uint16_t* ws_state16;  // ... before each chunk, bf16
+  float* ws_state;       // (batch, nchunks, nheads, headdim x dstate): state after each chunk, in fragments
+  uint16_t* ws_state16;  // (..., headdim, dstate): before each chunk, bf16
   uint16_t* ws_dstate16; // ... its adjoint after each chunk, bf16
   float* ws_end;         // (batch, nchunks, nheads, headdim/16, 2): <state, adjoint> after each chunk
   uint16_t* ws_r;        // (batch, seqlen, nheads, headdim): v minus the state's prediction

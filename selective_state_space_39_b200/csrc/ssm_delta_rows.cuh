@@ -192,42 +192,66 @@ __device__ __forceinline__ void store_state(const float (&s)[NS / 8][4], float* 
     *reinterpret_cast<float2*>(r0 + 8 * N + 8 * j) = make_float2(s[j][2], s[j][3]);
   }
 }
-// The rows as bf16 (for products whose results are bf16).
-template <int N, int NS>
-__device__ __forceinline__ void store_state16(const float (&s)[NS / 8][4], uint16_t* dst, int lane) {
-  uint16_t* r0 = dst + (lane >> 2) * N + 2 * (lane & 3);
+// The warp's part of a state for the walk back, whose warps hold the same
+// fragments: fragment by fragment, 512 contiguous bytes of a tile (row-major
+// stores, 32 bytes of a row at a time, took longer than the chunk's arithmetic).
+template <int NS>
+__device__ __forceinline__ void store_tiles(const float (&s)[NS / 8][4], float* dst, int lane) {
 #pragma unroll
-  for (int j = 0; j < NS / 8; ++j) {
-    *reinterpret_cast<uint32_t*>(r0 + 8 * j) = pack_bf16x2(s[j][0], s[j][1]);
-    *reinterpret_cast<uint32_t*>(r0 + 8 * N + 8 * j) = pack_bf16x2(s[j][2], s[j][3]);
-  }
+  for (int j = 0; j < NS / 8; ++j)
+    *reinterpret_cast<float4*>(dst + (j * 32 + lane) * 4) =
+        make_float4(s[j][0], s[j][1], s[j][2], s[j][3]);
 }
-// The warp's part of a state (16 rows of NS columns of N), asynchronously into
-// rows of NS + 8 floats in shared memory, and <s, it> (all lanes).
-template <int N, int NS>
-__device__ __forceinline__ void fetch_state(uint32_t to, const float* src, int lane) {
+// Such a part, asynchronously into shared memory (a lane reads what it copied),
+// and <s, it> (all lanes).
+template <int NS>
+__device__ __forceinline__ void fetch_tiles(uint32_t to, const float* src, int lane) {
 #pragma unroll
-  for (int i = lane; i < 16 * NS / 4; i += 32) {
-    const int row = i / (NS / 4), u = i % (NS / 4);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + row * (NS + 8) * 4 + u * 16),
-                 "l"(src + (size_t)row * N + u * 4)
+  for (int j = 0; j < NS / 8; ++j)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (j * 32 + lane) * 16),
+                 "l"(src + (j * 32 + lane) * 4)
                  : "memory");
-  }
 }
 template <int NS>
-__device__ __forceinline__ float state_dot(const float (&s)[NS / 8][4], const float* rows, int lane) {
-  const float* r0 = rows + (lane >> 2) * (NS + 8) + 2 * (lane & 3);
+__device__ __forceinline__ float tiles_dot(const float (&s)[NS / 8][4], const float* tiles, int lane) {
   float2 d0 = make_float2(0.f, 0.f), d1 = d0;
 #pragma unroll
   for (int j = 0; j < NS / 8; ++j) {
-    d0 = fma2(make_float2(s[j][0], s[j][1]), *reinterpret_cast<const float2*>(r0 + 8 * j), d0);
-    d1 = fma2(make_float2(s[j][2], s[j][3]),
-              *reinterpret_cast<const float2*>(r0 + 8 * (NS + 8) + 8 * j), d1);
+    const float4 v = *reinterpret_cast<const float4*>(tiles + (j * 32 + lane) * 4);
+    d0 = fma2(make_float2(s[j][0], s[j][1]), make_float2(v.x, v.y), d0);
+    d1 = fma2(make_float2(s[j][2], s[j][3]), make_float2(v.z, v.w), d1);
   }
   float d = (d0.x + d0.y) + (d1.x + d1.y);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   return d;
+}
+// The rows as bf16, row-major (for the products of ssm_delta_grad.cu, whose
+// results are bf16): through shared memory (rows of NS + 8 values), whole rows
+// of NS values to global memory.
+template <int N, int NS>
+__device__ __forceinline__ void store_state16(const float (&s)[NS / 8][4], uint32_t rows, uint16_t* dst,
+                                              int lane) {
+  constexpr int kRow = (NS + 8) * 2;
+  const uint32_t at = rows + ((lane & 7) + (lane & 8)) * kRow + (lane >> 4) * 16;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < NS / 8; j += 2)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at + j * 16),
+                 "r"(pack_bf16x2(s[j][0], s[j][1])), "r"(pack_bf16x2(s[j][2], s[j][3])),
+                 "r"(pack_bf16x2(s[j + 1][0], s[j + 1][1])), "r"(pack_bf16x2(s[j + 1][2], s[j + 1][3]))
+                 : "memory");
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16 * NS / 8; i += 32) {
+    const int row = (i + lane) / (NS / 8), u = (i + lane) % (NS / 8);
+    uint4 w;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "r"(rows + row * kRow + u * 16)
+                 : "memory");
+    *reinterpret_cast<uint4*>(dst + (size_t)row * N + u * 8) = w;
+  }
 }
 
 // ---------------------------------------------------------------- the CTA ----

@@ -311,7 +311,7 @@ __device__ __forceinline__ void get_max(float& m0, float& m1, const float* other
 
 constexpr int kRowWarps = 8, kTcThreads = kRowWarps * 32 + 128;
 
-// SP warps share a block of 16 rows.
+// SP warps share a block of 16 rows (BWD: two).
 template <int N, int SP, bool BWD>
 __global__ void __launch_bounds__(kTcThreads, 1)
     delta_tc_kernel(const __grid_constant__ DeltaChunkParams p) {
@@ -366,6 +366,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const size_t col_at0 = (size_t)t.b * d.seqlen * vs + (size_t)h * d.headdim + pw;
       float* const mx = &maxima[0][warp][0];
       const float* const ox = &maxima[0][warp ^ 4][0];
+      // BWD: the warp's rows of the state on their way out
+      const uint32_t out16 = smem_u32(smem + (size_t)p.stages * l.stage) + p.blocks * 2 * kTiles * kCol +
+                             (blk * SP + hf) * 16 * (NS + 8) * 2;
       auto fetch = [&](int c) {  // the warp's tokens of its block's columns
         const int valid = (int)min((int64_t)kC, d.seqlen - (int64_t)c * kC);
         const size_t at = col_at0 + (size_t)c * kC * vs;
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_load(row + kTmO + tcol, y);
         scale_rows(y, inv0, inv1);
         scale_cols(y, sc + kScSq * kC + tk, lane);
-        if (BWD) store_state16<N, NS>(S, p.ws_state16 + st_at, lane);
+        if (BWD) store_state16<N, NS>(S, out16, p.ws_state16 + st_at, lane);
 
         // ---- u = beta T R; K^T (e^(G_end - G) u)
         ok = wait_warp(&bars[kBarT], par, ok ? p.wait_limit_ns : 0) && ok;
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t ycol = row + kTmY + hcol;
         if (c + 1 < p.nchunks) ok = put_state(ok);
         if (!ok) break;
-        if (BWD) store_state<N, NS>(S, p.ws_state + st_at, lane);
+        if (BWD) store_tiles<NS>(S, p.ws_state + (st_at - part) + (size_t)pw * N + hf * 16 * NS, lane);
 
         // ---- Y
         tm_load(ycol, x);
@@ -648,12 +651,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const size_t col_at0 = (size_t)t.b * d.seqlen * vs + (size_t)h * d.headdim + pw;
       float* const mx = &maxima[0][warp][0];
       const float* const ox = &maxima[0][warp ^ 4][0];
-      // the state after the chunk, for its product with dS
-      float* const rows = reinterpret_cast<float*>(smem + (size_t)p.stages * l.stage +
-                                                   p.blocks * 2 * kTiles * kCol) + (blk * 2 + hf) * 16 * (NS + 8);
+      // the state after the chunk, for its product with dS; dS on its way out
+      float* const after = reinterpret_cast<float*>(smem + (size_t)p.stages * l.stage +
+                                                    p.blocks * 2 * kTiles * kCol) + (blk * 2 + hf) * 16 * NS;
+      const uint32_t out16 = smem_u32(smem + (size_t)p.stages * l.stage) + p.blocks * 2 * kTiles * kCol +
+                             p.blocks * 2 * 16 * NS * 4 + (blk * 2 + hf) * 16 * (NS + 8) * 2;
       auto fetch = [&](int c) {
-        fetch_state<N, NS>(smem_u32(rows), p.ws_state + (((size_t)t.b * p.nchunks + c) * d.nheads + h) *
-                                                            ((size_t)d.headdim * N) + part, lane);
+        fetch_tiles<NS>(smem_u32(after), p.ws_state + (((size_t)t.b * p.nchunks + c) * d.nheads + h) *
+                                                          ((size_t)d.headdim * N) + (size_t)pw * N +
+                                             hf * 16 * NS, lane);
         const int valid = (int)min((int64_t)kC, d.seqlen - (int64_t)c * kC);
         const size_t at = col_at0 + (size_t)c * kC * vs;
         const uint32_t to = col0 + (c & 1) * kTiles * kCol;
@@ -737,13 +743,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wrote(&bars[kPutU]);
 
         // ---- meanwhile: the next chunk's rows, du.r, dS for the gradients, <S, dS>
-        const float dot = state_dot<NS>(S, rows, lane);
+        const float dot = tiles_dot<NS>(S, after, lane);
         if (lane == 0) p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
         __syncwarp();
         if (c > 0) fetch(c - 1);
         load_rows(x, vrow + 2 * kCol, tk, lc);
         row_dots(u, x, p.ws_dotu + dot_at, lane);
-        store_state16<N, NS>(S, p.ws_dstate16 + st_at, lane);
+        store_state16<N, NS>(S, out16, p.ws_dstate16 + st_at, lane);
         load_rows(y, vrow + kCol, tk, lc);
         scale_cols(y, sc + kScSq * kC + tk, lane);
 
@@ -847,13 +853,18 @@ cudaError_t run(K* one, K* two, DeltaChunkParams p, int tiles, int head_bytes, i
 }
 template <int N, bool BWD>
 cudaError_t fwd(const DeltaChunkParams& p, cudaStream_t stream) {
-  return run<N>(delta_tc_kernel<N, 1, BWD>, delta_tc_kernel<N, 2, BWD>, p, BWD ? 2 : 1,
-                BWD ? kDeltaLoadBwd : kDeltaHeadFwd, 0, stream);
+  constexpr int state16 = 2 * 16 * (N / 2 + 8) * 2;
+  if constexpr (BWD)
+    return run<N, void(DeltaChunkParams)>(nullptr, delta_tc_kernel<N, 2, true>, p, 2, kDeltaLoadBwd,
+                                          state16, stream);
+  else
+    return run<N>(delta_tc_kernel<N, 1, false>, delta_tc_kernel<N, 2, false>, p, 1, kDeltaHeadFwd, 0,
+                  stream);
 }
 template <int N>
 cudaError_t rev(const DeltaChunkParams& p, cudaStream_t stream) {
   return run<N, void(DeltaChunkParams)>(nullptr, delta_back_kernel<N>, p, 3, kDeltaLoadBwd,
-                                        2 * 16 * (N / 2 + 8) * 4, stream);
+                                        2 * 16 * ((N / 2) * 4 + (N / 2 + 8) * 2), stream);
 }
 
 }  // namespace
