@@ -90,8 +90,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 
   // ---- raw k and q
   constexpr int LPR = N / 8;
+#pragma unroll
   for (int i = tid; i < 2 * kC * LPR; i += kThreads) {
-    const int w = i / (kC * LPR), j = i - w * kC * LPR, row = j / LPR, u = j % LPR;
+    const int w = i / (kC * LPR), j = i % (kC * LPR), row = j / LPR, u = j % LPR;
     const uint16_t* src = static_cast<const uint16_t*>(w ? d.q : d.k) +
                           ((row0 + (row < valid ? row : 0)) * d.nkheads + kh) * N + u * 8;
     copy16(sm + (w ? g.q : g.k) + row * g.xs + u * 16, src, row < valid);
@@ -114,21 +115,52 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       F[kfKn * kC + tid] = sc[kScKn * kC + tid];
       F[kfQn * kC + tid] = sc[kScQn * kC + tid];
     }
-    const int ppr = P / 8;
-    for (int i = tid; i < 3 * kC * ppr; i += kThreads) {
-      const int w = i / (kC * ppr), j = i - w * kC * ppr, row = j / ppr, u = j - row * ppr;
-      const uint16_t* src = (w == 0 ? p.dy : (w == 1 ? p.ws_r : p.dv)) +
-                            ((row0 + (row < valid ? row : 0)) * d.nheads + h) * P + u * 8;
-      copy16(sm + (w == 0 ? g.dy : (w == 1 ? g.r : g.dr)) + row * g.ps + u * 16, src, row < valid);
+    {  // half a warp per row of headdim (at most 16 units), two rows per thread and tensor
+      const int u = lane & 15;
+#pragma unroll
+      for (int w = 0; w < 3; ++w) {
+        const uint16_t* src = (w == 0 ? p.dy : (w == 1 ? p.ws_r : p.dv)) + (row0 * d.nheads + h) * P + u * 8;
+        const uint32_t to = sm + (w == 0 ? g.dy : (w == 1 ? g.r : g.dr)) + u * 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 32 * i + 2 * warp + (lane >> 4);
+          if (u < P / 8)
+            copy16(to + row * g.ps, src + (size_t)(row < valid ? row : 0) * d.nheads * P, row < valid);
+        }
+      }
     }
     cp_async_commit_group();
-    const size_t sz = (size_t)P * N;
-    for (int i = tid; i < 2 * P * LPR; i += kThreads) {
-      const int w = i / (P * LPR), j = i - w * P * LPR, row = j / LPR, u = j % LPR;
-      copy16(sm + (w ? g.ds : g.s) + row * g.xs + u * 16,
-             (w ? p.ws_dstate16 : p.ws_state16) + bch * sz + (size_t)j * 8, true);
+    {
+      const size_t at = bch * ((size_t)P * N) + tid * 8;
+      for (int j = tid; j < P * LPR; j += kThreads) {
+        const uint32_t to = sm + (j / LPR) * g.xs + (j % LPR) * 16;
+        copy16(to + g.s, p.ws_state16 + at + (size_t)(j - tid) * 8, true);
+        copy16(to + g.ds, p.ws_dstate16 + at + (size_t)(j - tid) * 8, true);
+      }
     }
     cp_async_commit_group();
+    // the gates' operands (first two warps), on their way meanwhile
+    float su = 0.f, so = 0.f, sv = 0.f, end = 0.f, raw = 0.f, beta_raw = 0.f;
+    const size_t gate_at = (row0 + tid) * d.nheads + h;
+    if (tid < kC) {
+      const int sl = P / 16;  // at most 8
+      const float* du = p.ws_dotu + bch * sl * kC + tid;
+      const float* dO = p.ws_doto + bch * sl * kC + tid;
+      const float* dv = p.ws_dotv + bch * sl * kC + tid;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        su += i < sl ? du[i * kC] : 0.f;
+        so += i < sl ? dO[i * kC] : 0.f;
+        sv += i < sl ? dv[i * kC] : 0.f;
+      }
+      // <S_end, dS_end>, over the reverse pass's warps
+      end = lane < 2 * sl ? p.ws_end[bch * 2 * sl + lane] : 0.f;
+      if (tid < valid) {
+        raw = bf16_to_f32(static_cast<const uint16_t*>(d.dt)[gate_at]) +
+              (d.dt_bias ? d.dt_bias[h] : 0.f);
+        beta_raw = bf16_to_f32(static_cast<const uint16_t*>(d.beta)[gate_at]);
+      }
+    }
     cp_async_wait_group<1>();
     __syncthreads();
 
@@ -266,23 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 
     // ---- the gates: one token per thread of the first two warps
     if (tid < kC) {
-      const int sl = P / 16;
-      const float* du = p.ws_dotu + bch * sl * kC + tid;
-      const float* dO = p.ws_doto + bch * sl * kC + tid;
-      const float* dv = p.ws_dotv + bch * sl * kC + tid;
-      float su = 0.f, so = 0.f, sv = 0.f;
-      for (int i = 0; i < sl; ++i) {
-        su += du[i * kC];
-        so += dO[i * kC];
-        sv += dv[i * kC];
-      }
-      float raw = 0.f, beta_raw = 0.f;
-      const size_t gate_at = (row0 + tid) * d.nheads + h;
-      if (tid < valid) {
-        raw = bf16_to_f32(static_cast<const uint16_t*>(d.dt)[gate_at]) +
-              (d.dt_bias ? d.dt_bias[h] : 0.f);
-        beta_raw = bf16_to_f32(static_cast<const uint16_t*>(d.beta)[gate_at]);
-      }
       float db = su;
 #pragma unroll
       for (int i = 0; i < 4; ++i) db -= F[(kfCol + i) * kC + tid];
@@ -300,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       F[(kfRow)*kC + tid] = dg;
       asm volatile("bar.sync 1, 64;" ::: "memory");
       if (warp == 0) dg += F[(kfRow)*kC + 32];
-      float end = 0.f;  // <S_end, dS_end>, over the reverse pass's warps in order
-      for (int i = 0; i < 2 * sl; ++i) end += p.ws_end[bch * 2 * sl + i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
       dg += end;
       float dA = 0.f, dbias = 0.f;
       if (tid < valid) {
