@@ -9,6 +9,7 @@ a GPU) calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -597,7 +598,8 @@ def _at(t, name, dtype, shape, dev):
     if t is None:
         return None
     try:
-        if t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev.index
+                and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         pass
@@ -617,6 +619,20 @@ def _stream_of(stream, dev):
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev.index)
     return _stream_ptr(stream, dev)
+
+
+def _streamed(fn):
+    """Runs a call given a stream with that stream current, so that its results
+    and its workspace are allocated there too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _on(dev, fn, *args):
@@ -660,6 +676,7 @@ def gated_delta_bwd_workspace_bytes(batch, seqlen, nheads, nkheads, headdim, dst
                                                          dstate, _io_code(dtype)))
 
 
+@_streamed
 def ssm_gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, softplus=True, beta_sigmoid=True,
                         qk_norm=True, scale=None, h0=None, y=None, h_last=None, workspace=None,
                         return_last_state=True, stream=None):
@@ -693,6 +710,7 @@ def ssm_gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, softplus=True, beta_
     return y, h_last
 
 
+@_streamed
 def ssm_gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, softplus=True,
                            beta_sigmoid=True, qk_norm=True, scale=None, y=None, stream=None):
     """One decode step of the gated delta rule through ssm_gated_delta_update
@@ -714,6 +732,7 @@ def ssm_gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, softplus=T
     return y
 
 
+@_streamed
 def ssm_gated_delta_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, softplus=True, beta_sigmoid=True,
                         qk_norm=True, scale=None, h0=None, dh_last=None, workspace=None,
                         want_dA=True, want_ddt_bias=True, want_dh0=True, stream=None):
@@ -760,6 +779,7 @@ def gated_norm_bwd_workspace_bytes(rows, dim, groups=1, dtype=torch.bfloat16) ->
     return int(lib().ssm_gated_norm_bwd_workspace_bytes(rows, dim, groups, _io_code(dtype)))
 
 
+@_streamed
 def ssm_gated_norm_fwd(x, w, z=None, norm_before_gate=False, residual=None, residual_scale=1.0,
                        groups=1, eps=1e-5, y=None, h=None, stream=None):
     """The norm before and after a block through ssm_gated_norm_fwd of
@@ -791,6 +811,7 @@ def ssm_gated_norm_fwd(x, w, z=None, norm_before_gate=False, residual=None, resi
     return y, (x if residual is None else h)
 
 
+@_streamed
 def ssm_gated_norm_bwd(h, w, dy, z=None, norm_before_gate=False, dh=None, residual=False,
                        residual_scale=1.0, groups=1, eps=1e-5, workspace=None, want_dw=True,
                        stream=None):

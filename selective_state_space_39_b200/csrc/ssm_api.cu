@@ -926,10 +926,6 @@ struct DeltaDims {
   int io;
 };
 
-// Tokens from which the chunk kernels are taken; shorter sequences go token by
-// token, without a workspace.
-constexpr int64_t kDeltaMinChunked = 32;
-
 static int delta_dims_status(const DeltaDims& d) {
   if (d.io != SSM_DTYPE_F32 && d.io != SSM_DTYPE_BF16) return SSM_ERR_UNSUPPORTED;
   if (d.batch < 0 || d.seqlen < 0 || d.nheads < 0 || d.nkheads < 0 || d.headdim < 0 ||
@@ -948,9 +944,17 @@ static int delta_dims_status(const DeltaDims& d) {
   return SSM_OK;
 }
 
+// Chunk by chunk, or token by token (without a workspace)? A chunk costs 16 to
+// 54 us whatever its tokens, a token 0.3 us while the state's rows leave the GPU
+// empty and then its share of the rows' arithmetic. Measured, chunks against
+// tokens: 1024 rows of 128 x 64, 48 tokens 16.0 / 15.2 us; 8192 rows of 128 (here
+// and below), 24 tokens 26.5 / 27.4; 16384 rows, 10 and 12 tokens 25.5 / 26.4 and
+// 28.8 / 29.9; 32768 rows, 6 and 8 tokens 37.3 / 30.6 and 37.5 / 36.5; 65536 rows,
+// 4 and 8 tokens 53.8 / 51.2 and 53.4 / 75.6.
 static bool delta_chunked(const DeltaDims& d) {
-  return d.io == SSM_DTYPE_BF16 && d.seqlen >= kDeltaMinChunked &&
-         delta_chunk_supported((int)d.dstate, (int)d.headdim);
+  const int64_t rows = d.batch * d.nheads * d.headdim;
+  return d.io == SSM_DTYPE_BF16 && delta_chunk_supported((int)d.dstate, (int)d.headdim) &&
+         (d.seqlen >= 48 || (d.seqlen >= 8 && d.seqlen * rows >= 3 << 16));
 }
 
 struct DeltaWs {
@@ -978,7 +982,7 @@ static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
     w.doto = take(dots);
     w.dotv = take(dots);
     w.dotu = take(dots);
-    w.part = take(bc * d.nheads * 2 * 4);
+    w.part = take(bc * d.nheads * 2 * 8);
   }
   w.bytes = off;
   return w;
@@ -1026,7 +1030,7 @@ static DeltaChunkParams delta_chunk_params(const DeltaParams& dp, const DeltaDim
     p.ws_doto = reinterpret_cast<float*>(ws + w.doto);
     p.ws_dotv = reinterpret_cast<float*>(ws + w.dotv);
     p.ws_dotu = reinterpret_cast<float*>(ws + w.dotu);
-    p.ws_part = reinterpret_cast<float*>(ws + w.part);
+    p.ws_part = reinterpret_cast<double*>(ws + w.part);
   }
   return p;
 }
@@ -1191,8 +1195,11 @@ int ssm_gated_delta_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t n
                   {{q, nqk}, {k, nqk}, {v, nv}, {dt, ng}, {beta, ng}, {A, nh}, {dt_bias, nh},
                    {h0, ns}, {dy, nv}, {dh_last, ns}}))
     return fail(SSM_ERR_INVALID_ARG, "ssm_gated_delta_bwd: an output overlaps an input or another");
-  if (none) {  // no token: the state's gradient passes through, the others are zero
+  if (none) {  // no token or no row: the state's gradient passes through, the others are zero
     cudaError_t e = dA ? cudaMemsetAsync(dA, 0, nh, s) : cudaSuccess;
+    const Buf zero[] = {{dq, nqk}, {dk, nqk}, {ddt, ng}, {dbeta, ng}};
+    for (const Buf& z : zero)
+      if (e == cudaSuccess && z.p && z.n) e = cudaMemsetAsync(const_cast<void*>(z.p), 0, z.n, s);
     if (e == cudaSuccess && ddt_bias) e = cudaMemsetAsync(ddt_bias, 0, nh, s);
     if (e == cudaSuccess && dh0 && ns)
       e = dh_last ? cudaMemcpyAsync(dh0, dh_last, ns, cudaMemcpyDeviceToDevice, s)

@@ -125,27 +125,5 @@ __device__ __forceinline__ void split2(float x, float y, float s, uint32_t& hi, 
   const float2 v = mul2(make_float2(x, y), make_float2(s, s));
   pieces2(v.x, v.y, hi, lo);
 }
-__device__ __forceinline__ void pieces_a(const float (&c0)[4], const float (&c1)[4],
-                                         uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  pieces2(c0[0], c0[1], hi[0], lo[0]);
-  pieces2(c0[2], c0[3], hi[1], lo[1]);
-  pieces2(c1[0], c1[1], hi[2], lo[2]);
-  pieces2(c1[2], c1[3], hi[3], lo[3]);
-}
-// A fragments (16 rows x 16 of k) of accumulator tiles c0 (k 0..7) and c1 (k 8..15).
-__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], float s0,
-                                        float s1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  split2(c0[0], c0[1], s0, hi[0], lo[0]);
-  split2(c0[2], c0[3], s1, hi[1], lo[1]);
-  split2(c1[0], c1[1], s0, hi[2], lo[2]);
-  split2(c1[2], c1[3], s1, hi[3], lo[3]);
-}
-__device__ __forceinline__ void half_a(const float (&c0)[4], const float (&c1)[4], float s0,
-                                       float s1, uint32_t (&hi)[4]) {
-  hi[0] = h2_bits(__floats2half2_rn(c0[0] * s0, c0[1] * s0));
-  hi[1] = h2_bits(__floats2half2_rn(c0[2] * s1, c0[3] * s1));
-  hi[2] = h2_bits(__floats2half2_rn(c1[0] * s0, c1[1] * s0));
-  hi[3] = h2_bits(__floats2half2_rn(c1[2] * s1, c1[3] * s1));
-}
 
 }  // namespace ssm

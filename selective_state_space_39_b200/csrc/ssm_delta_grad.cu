@@ -34,7 +34,7 @@ struct GradLayout {
   int xs, ps;  // row strides (bytes) of the dstate-wide and headdim-wide tiles
   int k, q, s, ds, dy, r, dr, w1, w2, ns, f, bytes;
 };
-enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfDelta, kfSig, kfCol, kfRow = kfCol + 4, kfCount = kfRow + 2 };
+enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfCol, kfRow = kfCol + 4, kfCount };
 
 __host__ __device__ inline GradLayout grad_layout(int N, int P) {
   GradLayout g;
@@ -305,20 +305,22 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         const float be = delta_beta(beta_raw, 1);
         db *= be * (1.f - be);
       }
-      // suffix sums over the chunk's 64 tokens
-      float dg = so - sv;
+      // suffix sums over the chunk's 64 tokens, in 64 bits: their terms cancel
+      double sum = (double)so - (double)sv, all = end;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float up = __shfl_down_sync(0xffffffffu, dg, o);
-        if (lane + o < 32) dg += up;
+        const double up = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += up;
+        all += __shfl_xor_sync(0xffffffffu, all, o);
       }
-      F[(kfRow)*kC + tid] = dg;
+      double* R = reinterpret_cast<double*>(F + kfRow * kC);
+      if (tid == 32) R[0] = sum;
       asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (warp == 0) dg += F[(kfRow)*kC + 32];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) end += __shfl_xor_sync(0xffffffffu, end, o);
-      dg += end;
-      float dA = 0.f, dbias = 0.f;
+      if (warp == 0) sum += R[0];
+      float dg = (float)(sum + all);
+      // the first token's decay has nothing to act on without an initial state
+      if (!d.h0 && t0 + tid == 0) dg = 0.f;
+      double dA = 0.0, dbias = 0.0;
       if (tid < valid) {
         const float step = delta_step_size(raw, d.softplus);
         // dg = a <S_before, dS'>: after a decay below e^-20 it is less than the
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         if (step * d.A[h] < -20.f) dg = 0.f;
         const float sig = (d.softplus && raw <= kSoftplusCut) ? 1.f / (1.f + expf(-raw)) : 1.f;
         const float ddt = dg * d.A[h] * sig;
-        dA = dg * step;
+        dA = (double)dg * step;
         dbias = ddt;
         p.ddt[gate_at] = f32_to_bf16(ddt);
         p.dbeta[gate_at] = f32_to_bf16(db);
@@ -337,12 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
       }
       if (lane == 0) {
-        F[(kfRow + 1) * kC + 2 * warp] = dA;
-        F[(kfRow + 1) * kC + 2 * warp + 1] = dbias;
+        R[2 + 2 * warp] = dA;
+        R[2 + 2 * warp + 1] = dbias;
       }
       asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (tid < 2)
-        p.ws_part[bch * 2 + tid] = F[(kfRow + 1) * kC + tid] + F[(kfRow + 1) * kC + 2 + tid];
+      if (tid < 2) p.ws_part[bch * 2 + tid] = R[2 + tid] + R[4 + tid];
     }
   }
 
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 }
 
 // dA, ddt_bias: the chunks' sums of one head, in a fixed order.
-__global__ void __launch_bounds__(128) delta_grad_reduce(const float* part, int64_t rows, int nheads,
+__global__ void __launch_bounds__(128) delta_grad_reduce(const double* part, int64_t rows, int nheads,
                                                          float* dA, float* dbias) {
   __shared__ double sh[2][128];
   const int h = blockIdx.x, tid = threadIdx.x;
@@ -428,8 +429,7 @@ __global__ void __launch_bounds__(128) delta_grad_reduce(const float* part, int6
 template <int N>
 cudaError_t launch(const DeltaChunkParams& p, cudaStream_t stream) {
   const int bytes = grad_layout(N, p.d.headdim).bytes;
-  cudaError_t e = cudaFuncSetAttribute(delta_grad_kernel<N>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = allow_shared(delta_grad_kernel<N>);
   if (e != cudaSuccess) return e;
   delta_grad_kernel<N><<<dim3(p.nchunks, p.d.nkheads, p.d.batch), kThreads, bytes, stream>>>(p);
   e = cudaGetLastError();

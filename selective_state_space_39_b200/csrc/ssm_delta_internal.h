@@ -11,6 +11,7 @@
 namespace ssm {
 
 constexpr int kDeltaChunk = 64;        // tokens per chunk
+constexpr int kMaxShared = 220 * 1024;  // dynamic, beside a few KB of static shared memory
 constexpr float kDeltaQkEps = 1e-6f;   // |x|^2 + eps under the unit-length scaling
 
 struct DeltaParams {
@@ -29,6 +30,13 @@ struct DeltaParams {
   void* y;               // (batch, seqlen, nheads, headdim) io or null
   float* h_last;         // (batch, nheads, headdim, dstate) or null
 };
+
+// Lets a kernel take kMaxShared: one limit for every launch, so that calls from
+// several threads cannot lower it under one another.
+template <typename K>
+inline cudaError_t allow_shared(K* kern) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+}
 
 // dstate values of the token-by-token kernel (any headdim, fp32 or bf16 io).
 bool delta_step_dstate_supported(int dstate);
@@ -93,7 +101,7 @@ struct DeltaChunkParams {
   float* ws_doto;        // (batch, nchunks, nheads, headdim/16, 64): dy.y over 16 rows
   float* ws_dotv;        //   ... dv.v
   float* ws_dotu;        //   ... du.r
-  float* ws_part;        // (batch, nchunks, nheads, 2): partial dA, ddt_bias
+  double* ws_part;       // (batch, nchunks, nheads, 2): partial dA, ddt_bias
   uint16_t *dq, *dk, *dv, *ddt, *dbeta;
   float *dA, *ddt_bias, *dh0;
 };

@@ -448,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
 template <int N, bool BWD>
 cudaError_t launch(const DeltaChunkParams& p, cudaStream_t stream) {
   auto* kern = delta_prep_kernel<N, BWD>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             PrepSmem<N>::kBytes);
+  const cudaError_t e = allow_shared(kern);
   if (e != cudaSuccess) return e;
   const int rep = p.d.nheads / p.d.nkheads, subs = (rep + kHeads - 1) / kHeads;
   kern<<<dim3(p.nchunks, p.d.nkheads * subs, p.d.batch), kThreads, PrepSmem<N>::kBytes, stream>>>(

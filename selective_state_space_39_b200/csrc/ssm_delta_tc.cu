@@ -43,8 +43,6 @@
 // per head. Back: 0 dS pieces; 128 K dS, dU's pieces, dR's pieces; 192 dY's
 // pieces, for P^T, then for Q^T; 256 P^T dY per head, then the sum for dS; 384
 // T^T dU per head.
-#include <stdlib.h>
-
 #include "ssm_delta_rows.cuh"
 #include "ssm_tc.cuh"
 
@@ -831,22 +829,19 @@ cudaError_t run(K* one, K* two, DeltaChunkParams p, int tiles, int head_bytes, i
   auto lay = [&](int blocks) { return layout(N, blocks, per_head, tiles, head_bytes, 0); };
   auto extra = [&](int blocks) { return blocks * (2 * tiles * kCol + block_bytes) + 1024; };
   auto stages_of = [&](int blocks) {
-    return std::min(kMaxStages, (224 * 1024 - extra(blocks)) / lay(blocks).stage);
+    return std::min(kMaxStages, (kMaxShared - extra(blocks)) / lay(blocks).stage);
   };
   auto ctas = [&](int blocks) { return groups * ((group + blocks - 1) / blocks); };
   int blocks = one ? kMaxBlocks : 4;
   while (blocks > 1 && (blocks / 2 >= group || lay(blocks).heads > kTcHeads || stages_of(blocks) < 2 ||
                         ctas(blocks / 2) <= 148))
     blocks /= 2;
-  const char* force = getenv("SSM_DELTA_BLOCKS");
-  if (force && *force && (one || atoi(force) <= 4) && lay(atoi(force)).heads <= kTcHeads && stages_of(atoi(force)) >= 2) blocks = atoi(force);
   p.blocks = blocks;
   p.stages = stages_of(blocks);
   if (p.stages < 2) return cudaErrorInvalidValue;
   const int bytes = lay(blocks).stage * p.stages + extra(blocks);
   K* kern = blocks <= 4 ? two : one;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  const cudaError_t e = allow_shared<K>(kern);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)ctas(blocks), kTcThreads, bytes, stream>>>(p);
   return cudaGetLastError();
