@@ -643,6 +643,17 @@ def _on(dev, fn, *args):
         return fn(*args)
 
 
+@functools.lru_cache(maxsize=256)
+def _bytes_of(fn, *sizes):
+    """What a C function of sizes alone answers (the call costs as much as a
+    third of a launch)."""
+    return int(getattr(lib(), fn)(*sizes))
+
+
+def _scratch(like, need):
+    return like.new_empty(need, dtype=torch.uint8)
+
+
 def _delta_sizes(q, v, tokens):
     """(batch, L, heads, key heads, headdim, dstate) of v (batch[, L], heads,
     headdim) and q (batch[, L], key heads, dstate)."""
@@ -695,10 +706,10 @@ def ssm_gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, softplus=True, beta_
     if y is None:
         y = torch.empty_like(v)
     if h_last is None and return_last_state:
-        h_last = torch.empty(st, dtype=f32, device=dev)
+        h_last = torch.empty_like(h0) if h0 is not None else torch.empty(st, dtype=f32, device=dev)
     if workspace is None:
-        need = _on(dev, lib().ssm_gated_delta_workspace_bytes, *sizes, io)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        need = _bytes_of("ssm_gated_delta_workspace_bytes", *sizes, io)
+        workspace = _scratch(v, need) if need else None
     rc = _on(dev, lib().ssm_gated_delta_fwd, *sizes, io, *ins, 1 if softplus else 0,
              1 if beta_sigmoid else 0, 1 if qk_norm else 0, N ** -0.5 if scale is None else scale,
              ph0, _at(y, "y", v.dtype, v.shape, dev), _at(h_last, "h_last", f32, st, dev),
@@ -752,8 +763,8 @@ def ssm_gated_delta_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, softplus=True, b
          "ddt_bias": torch.empty((H,), dtype=f32, device=dev) if want_ddt_bias else None,
          "dh0": torch.empty(st, dtype=f32, device=dev) if want_dh0 else None}
     if workspace is None:
-        need = _on(dev, lib().ssm_gated_delta_bwd_workspace_bytes, *sizes, io)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        need = _bytes_of("ssm_gated_delta_bwd_workspace_bytes", *sizes, io)
+        workspace = _scratch(v, max(need, 1))
     rc = _on(dev, lib().ssm_gated_delta_bwd, *sizes, io, *ins, 1 if softplus else 0,
              1 if beta_sigmoid else 0, 1 if qk_norm else 0, N ** -0.5 if scale is None else scale,
              _at(h0, "h0", f32, st, dev), _at(dy, "dy", v.dtype, v.shape, dev),
@@ -830,10 +841,10 @@ def ssm_gated_norm_bwd(h, w, dy, z=None, norm_before_gate=False, dh=None, residu
     rows, io = (h.numel() // dim if dim else 0), _io_code(ty)
     g = {"dx": torch.empty_like(dy), "dz": torch.empty_like(dy) if z is not None else None,
          "dresidual": torch.empty_like(h) if residual else None,
-         "dw": torch.empty((dim,), dtype=torch.float32, device=dev) if want_dw else None}
+         "dw": torch.empty_like(w) if want_dw else None}
     if workspace is None and want_dw:
-        need = lib().ssm_gated_norm_bwd_workspace_bytes(rows, dim, groups, io)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        need = _bytes_of("ssm_gated_norm_bwd_workspace_bytes", rows, dim, groups, io)
+        workspace = _scratch(dy, max(need, 1))
     P = [t.data_ptr() if t is not None else None for t in g.values()]
     rc = _on(dev, lib().ssm_gated_norm_bwd, rows, dim, groups, io, _io_code(ht),
              _at(h, "h", ht, shape, dev), residual_scale, _at(z, "z", ty, shape, dev),
