@@ -11,7 +11,7 @@
 namespace ssm {
 
 constexpr int kDeltaChunk = 64;        // tokens per chunk
-constexpr int kMaxShared = 220 * 1024;  // dynamic, beside a few KB of static shared memory
+constexpr int kMaxShared = 224 * 1024;  // dynamic, beside 3 KB of static shared memory
 constexpr float kDeltaQkEps = 1e-6f;   // |x|^2 + eps under the unit-length scaling
 
 struct DeltaParams {

@@ -5,9 +5,9 @@
 //   M_ij = (k_i . k_j) e^(G_i - G_j)  (j < i),   P_ij = (q_i . k_j) e^(G_i - G_j)  (j <= i)
 // the chunk's residuals r (u = beta r) solve (I + M diag(beta)) r = v - e^G S k,
 // so the kernel writes T = (I + M diag(beta))^-1, P, and the per-token factors
-// (DeltaScal). T is inverted block by block: the four 16 x 16 diagonal blocks by
+// (DeltaScal). T is inverted block by block: the eight 8 x 8 diagonal blocks by
 // forward substitution (one column per lane, fp32), then
-//   T_10 = -T_11 (L_10 T_00) and T_32 likewise, then the 32 x 32 block below them,
+//   T_10 = -T_11 (L_10 T_00) over blocks of 8, of 16 and of 32 rows,
 // the products as tf32 MMAs of two pieces (21 bits; the rest of fp32's range
 // needs no scale). k and q are written as fp16 rows scaled by a power of two
 // (exact for every element within 2^14 of the row's largest), T as two fp16
@@ -22,6 +22,12 @@
 // diagonal blocks the decay is a product of a row's and a column's factor
 // around the start of the row's block, e^(G_i - G_s) e^(G_s - G_j), neither
 // above 1; inside them it is taken from the difference itself.
+//
+// Bound: the latencies of about 1900 instructions per warp and head (issue slots
+// 53 % busy, shared memory 57 %, DRAM 33 %) at four CTAs per SM; five, with 96
+// registers, took 233 us where four take 219 (4 x 4096 tokens, 64 heads, 16 key
+// heads, dstate 128; 550 MB read and written). 8192 tokens of 32 heads and 16 key
+// heads: 77 us; for the backward pass 2 x 2048 tokens of 32 heads: 46 us.
 #include "ssm_delta.cuh"
 
 namespace ssm {
@@ -31,15 +37,19 @@ namespace {
 constexpr int kC = kDeltaChunk;
 constexpr int kThreads = 128;
 constexpr int kHeads = 4;        // value heads per CTA, at most
-constexpr int kLs = kC + 4;      // row stride (floats) of the fp32 matrices
+// The fp32 matrix of a head: rows of kLs floats, in which the rows with bit 2 set
+// swap the two quads of every eight columns. MMA operands (rows or columns along a
+// quad), float2 fragments and float4 rows then all meet every bank once.
+constexpr int kLs = kC + 8;
 constexpr float kMinLogDecay = -100.f;
 
 template <int N>
 struct PrepSmem {
   static constexpr int kTile = kC * N * 2;
   static constexpr int kL = kC * kLs * 4;                  // L, then T, of one head
-  static constexpr int kA = 2 * kTile > kL ? 2 * kTile : kL;  // over the k/q tiles
-  static constexpr int kScal = kHeads * kDeltaScalBwd;
+  static constexpr int kKK = 20 * 512;                     // k k^T, in fragments
+  static constexpr int kA = 2 * kTile > kL + kKK ? 2 * kTile : kL + kKK;  // over the k/q tiles
+  static constexpr int kScal = 2 * kDeltaScalBwd;          // of two heads
   static constexpr int kTok = 4 * kC * 4;
   static constexpr int kCols = 2 * 3 * kC * 4;             // column factors per row block
   static constexpr int kBytes = kA + kScal + kTok + kCols + 64;
@@ -64,10 +74,10 @@ __device__ __forceinline__ void tf32_pieces(float x, uint32_t& hi, uint32_t& lo)
   hi = __float_as_uint(x) & 0xFFFFE000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
-// d[16 x 16] = A[16 x n] B[n x 16] over k0 <= n < k1, both fp32 with row stride kLs.
+// d[16 x 16] = A[16 x n] B[n x 16] over k0 <= n < k1, both in the matrix.
 __device__ __forceinline__ void block_product(float (&d)[2][4], const float* A, const float* B,
                                               int k0, int k1, int lane) {
-  const int g = lane >> 2, t = lane & 3;
+  const int g = lane >> 2, t = lane & 3, flip = g & 4;
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -75,28 +85,41 @@ __device__ __forceinline__ void block_product(float (&d)[2][4], const float* A, 
 #pragma unroll 2
   for (int k = k0; k < k1; k += 8) {
     uint32_t ah[4], al[4];
-    tf32_pieces(A[g * kLs + k + t], ah[0], al[0]);
-    tf32_pieces(A[(g + 8) * kLs + k + t], ah[1], al[1]);
-    tf32_pieces(A[g * kLs + k + t + 4], ah[2], al[2]);
-    tf32_pieces(A[(g + 8) * kLs + k + t + 4], ah[3], al[3]);
+    tf32_pieces(A[g * kLs + k + t + flip], ah[0], al[0]);
+    tf32_pieces(A[(g + 8) * kLs + k + t + flip], ah[1], al[1]);
+    tf32_pieces(A[g * kLs + k + t + 4 - flip], ah[2], al[2]);
+    tf32_pieces(A[(g + 8) * kLs + k + t + 4 - flip], ah[3], al[3]);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       uint32_t bh0, bl0, bh1, bl1;
       tf32_pieces(B[(k + t) * kLs + 8 * n + g], bh0, bl0);
-      tf32_pieces(B[(k + t + 4) * kLs + 8 * n + g], bh1, bl1);
+      tf32_pieces(B[(k + t + 4) * kLs + 8 * n + (g ^ 4)], bh1, bl1);
       mma_tf32(d[n], al, bh0, bh1);
       mma_tf32(d[n], ah, bl0, bl1);
       mma_tf32(d[n], ah, bh0, bh1);
     }
   }
 }
+// d[8 x 8] = A B, 8 x 8 blocks of the matrix (rows 8 .. 15 of the MMA are empty).
+__device__ __forceinline__ void small_product(float (&d)[4], const float* A, const float* B, int lane) {
+  const int g = lane >> 2, t = lane & 3, flip = g & 4;
+  uint32_t ah[4] = {}, al[4] = {}, bh0, bl0, bh1, bl1;
+  tf32_pieces(A[g * kLs + t + flip], ah[0], al[0]);
+  tf32_pieces(A[g * kLs + t + 4 - flip], ah[2], al[2]);
+  tf32_pieces(B[t * kLs + g], bh0, bl0);
+  tf32_pieces(B[(t + 4) * kLs + (g ^ 4)], bh1, bl1);
+  d[0] = d[1] = d[2] = d[3] = 0.f;
+  mma_tf32(d, al, bh0, bh1);
+  mma_tf32(d, ah, bl0, bl1);
+  mma_tf32(d, ah, bh0, bh1);
+}
 __device__ __forceinline__ void block_store(const float (&d)[2][4], float* D, float sign, int lane) {
-  const int g = lane >> 2, t = lane & 3;
+  const int g = lane >> 2, col = (2 * (lane & 3)) ^ (g & 4);
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
-    *reinterpret_cast<float2*>(D + g * kLs + 8 * n + 2 * t) =
+    *reinterpret_cast<float2*>(D + g * kLs + 8 * n + col) =
         make_float2(sign * d[n][0], sign * d[n][1]);
-    *reinterpret_cast<float2*>(D + (g + 8) * kLs + 8 * n + 2 * t) =
+    *reinterpret_cast<float2*>(D + (g + 8) * kLs + 8 * n + col) =
         make_float2(sign * d[n][2], sign * d[n][3]);
   }
 }
@@ -179,51 +202,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
     }
   }
 
-  // ---- gates: two warps per head, one token per thread
-  const int nh = min(kHeads, rep - sub * kHeads);
-  for (int x0 = 0; x0 < nh; x0 += 2) {
-    const int x = x0 + (warp >> 1), i = tid & 63;
-    double g = 0.0;
-    float beta = 0.f;
-    if (x < nh && i < valid) {
-      const int h = kh * rep + sub * kHeads + x;
-      const size_t at = ((size_t)b * d_.seqlen + t0 + i) * d_.nheads + h;
-      const float raw = bf16_to_f32(static_cast<const uint16_t*>(d_.dt)[at]) +
-                        (d_.dt_bias ? d_.dt_bias[h] : 0.f);
-      float gf = delta_step_size(raw, d_.softplus) * d_.A[h];
-      gf = gf < kMinLogDecay ? kMinLogDecay : gf;
-      g = (double)gf * 1.4426950408889634;  // log2 units
-      beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d_.beta)[at]), d_.beta_sigmoid);
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, g, o);
-      if (lane >= o) g += up;
-    }
-    if ((warp & 1) == 0 && lane == 31) carry[warp >> 1] = g;
-    __syncthreads();
-    if (warp & 1) g += carry[warp >> 1];
-    float* sc = scal + (x < nh ? x : 0) * (kDeltaScalBwd / 4);
-    const float hi = (float)g;
-    if (x < nh) {
-      sc[kScGhi * kC + i] = hi;
-      sc[kScGlo * kC + i] = (float)(g - (double)hi);
-      sc[kScBeta * kC + i] = beta;
-    }
-    __syncthreads();
-    if (x < nh) {
-      const float ehi = sc[kScGhi * kC + kC - 1], elo = sc[kScGlo * kC + kC - 1];
-      const float lo = sc[kScGlo * kC + i];
-      const float D = ex2_approx(hi + lo), E = ex2_approx((ehi - hi) + (elo - lo));
-      sc[kScSk * kC + i] = D * tok[i];
-      sc[kScKend * kC + i] = tok[i] * E;
-      sc[kScK * kC + i] = tok[i];
-      sc[kScSq * kC + i] = D * tok[kC + i];
-      sc[kScEnd * kC + i] = ex2_approx(ehi + elo);
-      sc[kScKn * kC + i] = tok[2 * kC + i];
-      sc[kScQn * kC + i] = tok[3 * kC + i];
-    }
-  }
+  __syncthreads();
 
   // ---- k k^T and q k^T: warp w takes rows 16 w .. 16 w + 15, columns up to them
   float kk[8][4] = {}, qk[8][4] = {};
@@ -247,12 +226,66 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       }
     }
   }
+  // each warp keeps its part of k k^T in shared memory, out of its registers
+  __syncthreads();  // the k/q tiles are free
+  float4* kk_at = reinterpret_cast<float4*>(smem + Sm::kL) + warp * (warp + 1) * 32 + lane;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j <= 2 * warp + 1) kk_at[j * 32] = make_float4(kk[j][0], kk[j][1], kk[j][2], kk[j][3]);
+
+  const int nh = min(kHeads, rep - sub * kHeads);
   const int r0 = warp * 16 + (lane >> 2), r1 = r0 + 8;
   constexpr int kTiles = BWD ? 4 : 3;
   for (int x = 0; x < nh; ++x) {
-    __syncthreads();  // the k/q tiles, or the previous head's matrix, are free
+    __syncthreads();  // the previous head's matrix and factors are free
+
+    // ---- gates of two heads: two warps per head, one token per thread
+    if ((x & 1) == 0) {
+      const int xg = x + (warp >> 1), i = tid & 63;
+      double g = 0.0;
+      float beta = 0.f;
+      if (xg < nh && i < valid) {
+        const int h = kh * rep + sub * kHeads + xg;
+        const size_t at = ((size_t)b * d_.seqlen + t0 + i) * d_.nheads + h;
+        const float raw = bf16_to_f32(static_cast<const uint16_t*>(d_.dt)[at]) +
+                          (d_.dt_bias ? d_.dt_bias[h] : 0.f);
+        float gf = delta_step_size(raw, d_.softplus) * d_.A[h];
+        gf = gf < kMinLogDecay ? kMinLogDecay : gf;
+        g = (double)gf * 1.4426950408889634;  // log2 units
+        beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d_.beta)[at]), d_.beta_sigmoid);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, g, o);
+        if (lane >= o) g += up;
+      }
+      if ((warp & 1) == 0 && lane == 31) carry[warp >> 1] = g;
+      __syncthreads();
+      if (warp & 1) g += carry[warp >> 1];
+      float* sc = scal + (warp >> 1) * (kDeltaScalBwd / 4);
+      const float hi = (float)g;
+      if (xg < nh) {
+        sc[kScGhi * kC + i] = hi;
+        sc[kScGlo * kC + i] = (float)(g - (double)hi);
+        sc[kScBeta * kC + i] = beta;
+      }
+      __syncthreads();
+      if (xg < nh) {
+        const float ehi = sc[kScGhi * kC + kC - 1], elo = sc[kScGlo * kC + kC - 1];
+        const float lo = sc[kScGlo * kC + i];
+        const float D = ex2_approx(hi + lo), E = ex2_approx((ehi - hi) + (elo - lo));
+        sc[kScSk * kC + i] = D * tok[i];
+        sc[kScKend * kC + i] = tok[i] * E;
+        sc[kScK * kC + i] = tok[i];
+        sc[kScSq * kC + i] = D * tok[kC + i];
+        sc[kScEnd * kC + i] = ex2_approx(ehi + elo);
+        sc[kScKn * kC + i] = tok[2 * kC + i];
+        sc[kScQn * kC + i] = tok[3 * kC + i];
+      }
+      __syncthreads();
+    }
     unsigned char* tri = p.ws_head + (bc * d_.nheads + kh * rep + sub * kHeads + x) * (size_t)p.head_bytes;
-    float* sc = scal + x * (kDeltaScalBwd / 4);
+    float* sc = scal + (x & 1) * (kDeltaScalBwd / 4);
     const float gh0 = sc[kScGhi * kC + r0], gl0 = sc[kScGlo * kC + r0];
     const float gh1 = sc[kScGhi * kC + r1], gl1 = sc[kScGlo * kC + r1];
     const float km0 = tok[r0], km1 = tok[r1];
@@ -277,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       for (int q = 0; q < 4; ++q) pv[j][q] = 0.f;
       if (j > 2 * warp + 1) continue;
       const int col = 8 * j + 2 * (lane & 3);
+      const float4 kkj = kk_at[j * 32];
       float lv[4];
       if (j < 2 * warp) {
         const float2 cp = *reinterpret_cast<const float2*>(cols + (warp - 1) * 2 * kC + col);
@@ -285,10 +319,10 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
         pv[j][1] = qk[j][1] * cp.y * a0;
         pv[j][2] = qk[j][2] * cp.x * a1;
         pv[j][3] = qk[j][3] * cp.y * a1;
-        lv[0] = kk[j][0] * cl.x * (a0 * km0);
-        lv[1] = kk[j][1] * cl.y * (a0 * km0);
-        lv[2] = kk[j][2] * cl.x * (a1 * km1);
-        lv[3] = kk[j][3] * cl.y * (a1 * km1);
+        lv[0] = kkj.x * cl.x * (a0 * km0);
+        lv[1] = kkj.y * cl.y * (a0 * km0);
+        lv[2] = kkj.z * cl.x * (a1 * km1);
+        lv[3] = kkj.w * cl.y * (a1 * km1);
       } else {
         const float2 ch = *reinterpret_cast<const float2*>(sc + kScGhi * kC + col);
         const float2 cl = *reinterpret_cast<const float2*>(sc + kScGlo * kC + col);
@@ -300,13 +334,14 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
           const float gm = ex2_approx(((q < 2 ? gh0 : gh1) - ((q & 1) ? ch.y : ch.x)) +
                                       ((q < 2 ? gl0 : gl1) - ((q & 1) ? cl.y : cl.x)));
           if (cc <= row) pv[j][q] = qk[j][q] * gm;
-          lv[q] = cc < row ? kk[j][q] * gm * (q < 2 ? km0 : km1) *
+          lv[q] = cc < row ? (q < 2 ? (q ? kkj.y : kkj.x) : (q == 3 ? kkj.w : kkj.z)) * gm * (q < 2 ? km0 : km1) *
                                  ((q & 1) ? ck.y * cb.y : ck.x * cb.x)
                            : 0.f;
         }
       }
-      *reinterpret_cast<float2*>(L + r0 * kLs + col) = make_float2(lv[0], lv[1]);
-      *reinterpret_cast<float2*>(L + r1 * kLs + col) = make_float2(lv[2], lv[3]);
+      const int at = col ^ (r0 & 4);
+      *reinterpret_cast<float2*>(L + r0 * kLs + at) = make_float2(lv[0], lv[1]);
+      *reinterpret_cast<float2*>(L + r1 * kLs + at) = make_float2(lv[2], lv[3]);
     }
     float m0, m1;
     row_max(pv, m0, m1);
@@ -340,18 +375,20 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
     }
     __syncwarp();
 
-    // ---- T, the diagonal block of the warp's rows: column `lane` by forward
-    // substitution (lanes 16 .. 31 repeat lanes 0 .. 15)
+    // ---- T, the diagonal block of the warp's rows: its 8 x 8 diagonal blocks by
+    // forward substitution (eight lanes each, a column per lane; lanes 16 .. 31
+    // repeat lanes 0 .. 15), then the block below them
     {
       float* Ld = L + (warp * 16) * kLs + warp * 16;
-      const int col = lane & 15;
-      float xs[16];
+      float* Lb = Ld + ((lane >> 3) & 1) * (8 * kLs + 8);
+      const int col = lane & 7;
+      float xs[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         float acc0 = i == col ? 1.f : 0.f, acc1 = 0.f;
 #pragma unroll
         for (int j = 0; j < i; j += 4) {
-          const float4 l = *reinterpret_cast<const float4*>(Ld + i * kLs + j);
+          const float4 l = *reinterpret_cast<const float4*>(Lb + i * kLs + (j ^ (i & 4)));
           acc0 = fmaf(-l.x, xs[j], acc0);
           if (j + 1 < i) acc1 = fmaf(-l.y, xs[j + 1], acc1);
           if (j + 2 < i) acc0 = fmaf(-l.z, xs[j + 2], acc0);
@@ -362,8 +399,19 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       __syncwarp();
       if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) Ld[i * kLs + col] = xs[i];
+        for (int i = 0; i < 8; ++i) Lb[i * kLs + (col ^ (i & 4))] = xs[i];
       }
+      __syncwarp();
+      float e[4];
+      float* Lo = Ld + 8 * kLs;
+      float2* to = reinterpret_cast<float2*>(Lo + (lane >> 2) * kLs + ((2 * (lane & 3)) ^ ((lane >> 2) & 4)));
+      small_product(e, Lo, Ld, lane);
+      __syncwarp();
+      *to = make_float2(e[0], e[1]);
+      __syncwarp();
+      small_product(e, Lo + 8, Lo, lane);
+      __syncwarp();
+      *to = make_float2(-e[0], -e[1]);
     }
     __syncthreads();
 
@@ -391,28 +439,33 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
     block_store(d, Lba + bi * 16 * kLs + bj * 16, -1.f, lane);
     __syncthreads();
 
-    // ---- T's rows as two pieces: two threads per row
+    // ---- T's rows as two pieces: half of every 16-column block per thread
     {
-      const int row = tid >> 1, half = tid & 1, nb = row / 16 + 1;  // blocks of this row
-      const float* Lr = L + row * kLs;
+      const int row = warp * 16 + (lane & 15), half = lane >> 4;
+      const float* Lr = L + row * kLs + half * 8;
+      float4 v[4][2];
       float m = 0.f;
-      for (int j = half; j < 2 * nb; j += 2) {
-        const float4 a = *reinterpret_cast<const float4*>(Lr + j * 8);
-        const float4 b = *reinterpret_cast<const float4*>(Lr + j * 8 + 4);
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))));
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j > warp) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          v[j][i] = *reinterpret_cast<const float4*>(Lr + j * 16 + ((4 * i) ^ (row & 4)));
+          m = fmaxf(m, fmaxf(fmaxf(fabsf(v[j][i].x), fabsf(v[j][i].y)),
+                             fmaxf(fabsf(v[j][i].z), fabsf(v[j][i].w))));
+        }
       }
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
       const RowScale s = row_scale(exponent_of(m));
-      for (int j = 0; j < nb; ++j) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j > warp) continue;
         uint4 hi, lo;
-        const float4 v0 = *reinterpret_cast<const float4*>(Lr + j * 16 + half * 8);
-        const float4 v1 = *reinterpret_cast<const float4*>(Lr + j * 16 + half * 8 + 4);
-        split2(v0.x, v0.y, s.s, hi.x, lo.x);
-        split2(v0.z, v0.w, s.s, hi.y, lo.y);
-        split2(v1.x, v1.y, s.s, hi.z, lo.z);
-        split2(v1.z, v1.w, s.s, hi.w, lo.w);
-        unsigned char* at = tri + delta_tri_block(row / 16, j) + tri_at(row & 15, half);
+        split2(v[j][0].x, v[j][0].y, s.s, hi.x, lo.x);
+        split2(v[j][0].z, v[j][0].w, s.s, hi.y, lo.y);
+        split2(v[j][1].x, v[j][1].y, s.s, hi.z, lo.z);
+        split2(v[j][1].z, v[j][1].w, s.s, hi.w, lo.w);
+        unsigned char* at = tri + delta_tri_block(warp, j) + tri_at(row & 15, half);
         *reinterpret_cast<uint4*>(at) = hi;
         *reinterpret_cast<uint4*>(at + kDeltaTri) = lo;
       }
@@ -430,7 +483,8 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int r = i * 16 + half * 8 + 2 * q;
-          pieces2(L[r * kLs + row] * rows_s[r], L[(r + 1) * kLs + row] * rows_s[r + 1], hi[q], lo[q]);
+          const int at = row ^ (r & 4);  // r and r + 1 swap alike
+          pieces2(L[r * kLs + at] * rows_s[r], L[(r + 1) * kLs + at] * rows_s[r + 1], hi[q], lo[q]);
         }
         unsigned char* at = tri + kDeltaLoadBwd + delta_tri_block_t(i, row / 16) + tri_at(row & 15, half);
         *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
