@@ -28,11 +28,12 @@ namespace {
 
 constexpr int kC = kDeltaChunk;
 constexpr int kThreads = 512;
+constexpr int kGateWarp = 12;     // and the next: row blocks 0 and 1, columns behind them
 constexpr int kWs = kC * 2 + 16;  // row stride (bytes) of the 64 x 64 tiles
 
 struct GradLayout {
   int xs, ps;  // row strides (bytes) of the dstate-wide and headdim-wide tiles
-  int k, q, s, ds, dy, r, dr, w1, w2, ns, f, bytes;
+  int k, q, s, ds, dy, r, dr, w1, w2, ns, dots, f, bytes;
 };
 enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfCol, kfRow = kfCol + 4, kfCount };
 
@@ -51,6 +52,7 @@ __host__ __device__ inline GradLayout grad_layout(int N, int P) {
   g.w1 = at; at += kC * kWs;
   g.w2 = at; at += kC * kWs;
   g.ns = at; at += kC * kWs;
+  g.dots = at; at += 3 * (P / 16) * kC * 4;
   g.f = at; at += kfCount * kC * 4;
   g.bytes = at;
   return g;
@@ -98,22 +100,27 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     copy16(sm + (w ? g.q : g.k) + row * g.xs + u * 16, src, row < valid);
   }
 
-  float kk[2][4] = {};
-  float tq[T][4] = {}, tk[T][4] = {};
-  for (int hx = 0; hx < rep; ++hx) {
+  // ---- a head's tiles on their way: factors, row products and the rows of dy, r
+  // and dv first, then the states; the gates' operands into registers
+  const int gt = tid - kGateWarp * 32;  // the token of a gate thread
+  const bool gate = gt >= 0 && gt < kC;
+  const int sl = P / 16;  // at most 8
+  uint16_t dt_raw = 0, beta_raw = 0;
+  float A_h = 0.f, bias_h = 0.f, end = 0.f;
+  auto load = [&](int hx) {
     const int h = kh * rep + hx;
     const size_t bch = bc * d.nheads + h;
-    __syncthreads();  // the previous head's tiles are free
-
-    // ---- this head's tiles: dy, r and dv rows first, then the states
     const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes +
-                                                        4 * kDeltaTri);
-    if (tid < kC) {
-      F[kfGhi * kC + tid] = sc[kScGhi * kC + tid];
-      F[kfGlo * kC + tid] = sc[kScGlo * kC + tid];
-      F[kfBeta * kC + tid] = sc[kScBeta * kC + tid];
-      F[kfKn * kC + tid] = sc[kScKn * kC + tid];
-      F[kfQn * kC + tid] = sc[kScQn * kC + tid];
+                                                     4 * kDeltaTri);
+    if (tid < 5 * 16) {  // Ghi, Glo, beta, kn, qn
+      const int w = tid >> 4, u = tid & 15;
+      const int from = w == 0 ? kScGhi : (w == 1 ? kScGlo : (w == 2 ? kScBeta : (w == 3 ? kScKn : kScQn)));
+      copy16(sm + g.f + (w * kC + u * 4) * 4, sc + from * kC + u * 4, true);
+    }
+    if (tid < 3 * 16 * sl) {
+      const int w = tid / (16 * sl), u = tid - w * 16 * sl;
+      const float* src = (w == 0 ? p.ws_dotu : (w == 1 ? p.ws_doto : p.ws_dotv)) + bch * sl * kC;
+      copy16(sm + g.dots + tid * 16, src + u * 4, true);
     }
     {  // half a warp per row of headdim (at most 16 units), two rows per thread and tensor
       const int u = lane & 15;
@@ -139,28 +146,25 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       }
     }
     cp_async_commit_group();
-    // the gates' operands (first two warps), on their way meanwhile
-    float su = 0.f, so = 0.f, sv = 0.f, end = 0.f, raw = 0.f, beta_raw = 0.f;
-    const size_t gate_at = (row0 + tid) * d.nheads + h;
-    if (tid < kC) {
-      const int sl = P / 16;  // at most 8
-      const float* du = p.ws_dotu + bch * sl * kC + tid;
-      const float* dO = p.ws_doto + bch * sl * kC + tid;
-      const float* dv = p.ws_dotv + bch * sl * kC + tid;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        su += i < sl ? du[i * kC] : 0.f;
-        so += i < sl ? dO[i * kC] : 0.f;
-        sv += i < sl ? dv[i * kC] : 0.f;
-      }
+    if (gate) {
       // <S_end, dS_end>, over the reverse pass's warps
       end = lane < 2 * sl ? p.ws_end[bch * 2 * sl + lane] : 0.f;
-      if (tid < valid) {
-        raw = bf16_to_f32(static_cast<const uint16_t*>(d.dt)[gate_at]) +
-              (d.dt_bias ? d.dt_bias[h] : 0.f);
-        beta_raw = bf16_to_f32(static_cast<const uint16_t*>(d.beta)[gate_at]);
+      A_h = d.A[h];
+      bias_h = d.dt_bias ? d.dt_bias[h] : 0.f;
+      if (gt < valid) {
+        dt_raw = static_cast<const uint16_t*>(d.dt)[(row0 + gt) * d.nheads + h];
+        beta_raw = static_cast<const uint16_t*>(d.beta)[(row0 + gt) * d.nheads + h];
       }
     }
+  };
+
+  float kk[2][4] = {};
+  float tq[T][4] = {}, tk[T][4] = {};
+  load(0);
+  for (int hx = 0; hx < rep; ++hx) {
+    const int h = kh * rep + hx;
+    const size_t bch = bc * d.nheads + h;
+    const size_t gate_at = (row0 + gt) * d.nheads + h;  // of a gate thread
     cp_async_wait_group<1>();
     __syncthreads();
 
@@ -191,6 +195,55 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
           mma_bf16(kk[1], a, bb[2], bb[3]);
         }
       }
+    }
+
+    // ---- the gates, one token per thread of two warps that have no weights below
+    if (gate) {
+      const float* dots = reinterpret_cast<const float*>(smem + g.dots) + gt;
+      float so = 0.f, sv = 0.f;
+      for (int i = 0; i < sl; ++i) {
+        so += dots[(sl + i) * kC];
+        sv += dots[(2 * sl + i) * kC];
+      }
+      // suffix sums over the chunk's 64 tokens, in 64 bits: their terms cancel
+      double sum = (double)so - (double)sv, all = end;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += up;
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+      }
+      double* R = reinterpret_cast<double*>(F + kfRow * kC);
+      if (gt == 32) R[0] = sum;
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (gt < 32) sum += R[0];
+      float dg = (float)(sum + all);
+      // the first token's decay has nothing to act on without an initial state
+      if (!d.h0 && t0 + gt == 0) dg = 0.f;
+      double dA = 0.0, dbias = 0.0;
+      if (gt < valid) {
+        const float raw = bf16_to_f32(dt_raw) + bias_h;
+        const float step = delta_step_size(raw, d.softplus);
+        // dg = a <S_before, dS'>: after a decay below e^-20 it is less than the
+        // rounding of the sum above (2^-22 of its terms), so it is taken as 0
+        if (step * A_h < -20.f) dg = 0.f;
+        const float sig = (d.softplus && raw <= kSoftplusCut) ? 1.f / (1.f + expf(-raw)) : 1.f;
+        const float ddt = dg * A_h * sig;
+        dA = (double)dg * step;
+        dbias = ddt;
+        p.ddt[gate_at] = f32_to_bf16(ddt);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        dA += __shfl_xor_sync(0xffffffffu, dA, o);
+        dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+      }
+      if (lane == 0) {
+        R[2 + 2 * (gt >> 5)] = dA;
+        R[2 + 2 * (gt >> 5) + 1] = dbias;
+      }
+      asm volatile("bar.sync 1, 64;" ::: "memory");
+      if (gt < 2) p.ws_part[bch * 2 + gt] = R[2 + gt] + R[4 + gt];
     }
 
     // ---- dy r^T and dv r^T -> W, N + N^T, and the column sums of dbeta: rows of
@@ -241,6 +294,19 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     cp_async_wait_group<0>();
     __syncthreads();
 
+    if (gate && gt < valid) {
+      const float* du = reinterpret_cast<const float*>(smem + g.dots) + gt;
+      float db = 0.f;
+      for (int i = 0; i < sl; ++i) db += du[i * kC];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) db -= F[(kfCol + i) * kC + gt];
+      if (d.beta_sigmoid) {
+        const float be = delta_beta(bf16_to_f32(beta_raw), 1);
+        db *= be * (1.f - be);
+      }
+      p.dbeta[gate_at] = f32_to_bf16(db);
+    }
+
     // ---- dq += e^G dy S + W k;  dk += beta e^(G_end - G) r dS - e^G dv S + W^T q + (N + N^T) k
     const float g0 = F[kfGhi * kC + r0], l0 = F[kfGlo * kC + r0];
     const float g1 = F[kfGhi * kC + r1], l1 = F[kfGlo * kC + r1];
@@ -272,6 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
           o = fmaf(q < 2 ? f0 : f1, t[j][q], o);
         }
     }
+    if (hx + 1 < rep) {  // rows, states and factors are read: the next head's, meanwhile
+      __syncthreads();
+      load(hx + 1);
+    }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
       uint32_t a[4], e[4], f[4];
@@ -296,55 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       }
     }
 
-    // ---- the gates: one token per thread of the first two warps
-    if (tid < kC) {
-      float db = su;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) db -= F[(kfCol + i) * kC + tid];
-      if (d.beta_sigmoid) {
-        const float be = delta_beta(beta_raw, 1);
-        db *= be * (1.f - be);
-      }
-      // suffix sums over the chunk's 64 tokens, in 64 bits: their terms cancel
-      double sum = (double)so - (double)sv, all = end;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += up;
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-      }
-      double* R = reinterpret_cast<double*>(F + kfRow * kC);
-      if (tid == 32) R[0] = sum;
-      asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (warp == 0) sum += R[0];
-      float dg = (float)(sum + all);
-      // the first token's decay has nothing to act on without an initial state
-      if (!d.h0 && t0 + tid == 0) dg = 0.f;
-      double dA = 0.0, dbias = 0.0;
-      if (tid < valid) {
-        const float step = delta_step_size(raw, d.softplus);
-        // dg = a <S_before, dS'>: after a decay below e^-20 it is less than the
-        // rounding of the sum above (2^-22 of its terms), so it is taken as 0
-        if (step * d.A[h] < -20.f) dg = 0.f;
-        const float sig = (d.softplus && raw <= kSoftplusCut) ? 1.f / (1.f + expf(-raw)) : 1.f;
-        const float ddt = dg * d.A[h] * sig;
-        dA = (double)dg * step;
-        dbias = ddt;
-        p.ddt[gate_at] = f32_to_bf16(ddt);
-        p.dbeta[gate_at] = f32_to_bf16(db);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        dA += __shfl_xor_sync(0xffffffffu, dA, o);
-        dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
-      }
-      if (lane == 0) {
-        R[2 + 2 * warp] = dA;
-        R[2 + 2 * warp + 1] = dbias;
-      }
-      asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (tid < 2) p.ws_part[bch * 2 + tid] = R[2 + tid] + R[4 + tid];
-    }
   }
 
   // ---- through x / |x| (dx = n (t - x (x . t) / |x|^2)), then bf16 rows
