@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     float cs[2][2] = {};
     if (part <= mi) {
       float wv[2][4] = {}, xv[2][4] = {};
+#pragma unroll 4
       for (int kt = 0; kt < P / 16; ++kt) {
         uint32_t a[4], e[4], bb[4];
         ldsm4(a, sm + g.dy + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
@@ -314,29 +315,49 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     const float D0 = ex2_approx(g0 + l0), D1 = ex2_approx(g1 + l1);
     const float E0 = ex2_approx((ge - g0) + (le - l0)) * F[kfBeta * kC + r0];
     const float E1 = ex2_approx((ge - g1) + (le - l1)) * F[kfBeta * kC + r1];
-#pragma unroll
-    for (int w = 0; w < 3; ++w) {
-      const int at_a = w == 0 ? g.dy : (w == 1 ? g.r : g.dr), at_b = w == 1 ? g.ds : g.s;
-      float t[T][4] = {};
+    {
+      float t[T][4] = {}, x[T][4] = {};
+#pragma unroll 2
       for (int kt = 0; kt < P / 16; ++kt) {
-        uint32_t a[4];
-        ldsm4(a, sm + at_a + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+        uint32_t a[4], e[4];
+        ldsm4(a, sm + g.dy + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+        ldsm4(e, sm + g.dr + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
 #pragma unroll
         for (int j = 0; j < T / 2; ++j) {
           uint32_t bb[4];
-          ldsm4t(bb, sm + at_b + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
+          ldsm4t(bb, sm + g.s + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
           mma_bf16(t[2 * j], a, bb[0], bb[1]);
           mma_bf16(t[2 * j + 1], a, bb[2], bb[3]);
+          mma_bf16(x[2 * j], e, bb[0], bb[1]);
+          mma_bf16(x[2 * j + 1], e, bb[2], bb[3]);
         }
       }
-      const float f0 = w == 0 ? D0 : (w == 1 ? E0 : -D0), f1 = w == 0 ? D1 : (w == 1 ? E1 : -D1);
 #pragma unroll
       for (int j = 0; j < T; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          float& o = w == 0 ? tq[j][q] : tk[j][q];
-          o = fmaf(q < 2 ? f0 : f1, t[j][q], o);
+          tq[j][q] = fmaf(q < 2 ? D0 : D1, t[j][q], tq[j][q]);
+          tk[j][q] = fmaf(q < 2 ? -D0 : -D1, x[j][q], tk[j][q]);
         }
+    }
+    {
+      float t[T][4] = {};
+#pragma unroll 4
+      for (int kt = 0; kt < P / 16; ++kt) {
+        uint32_t a[4];
+        ldsm4(a, sm + g.r + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+#pragma unroll
+        for (int j = 0; j < T / 2; ++j) {
+          uint32_t bb[4];
+          ldsm4t(bb, sm + g.ds + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
+          mma_bf16(t[2 * j], a, bb[0], bb[1]);
+          mma_bf16(t[2 * j + 1], a, bb[2], bb[3]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < T; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tk[j][q] = fmaf(q < 2 ? E0 : E1, t[j][q], tk[j][q]);
     }
     if (hx + 1 < rep) {  // rows, states and factors are read: the next head's, meanwhile
       __syncthreads();
