@@ -112,6 +112,13 @@ __device__ __forceinline__ void row_max(const float (&x)[T][4], float& m0, float
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
 }
+// The transpose of the warp's 8 x 8 matrix of 16-bit values.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 // The pieces of two values that are in range already.
 __device__ __forceinline__ void pieces2(float x, float y, uint32_t& hi, uint32_t& lo) {

@@ -63,10 +63,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void st16(unsigned char* p, float v) {
-  *reinterpret_cast<uint16_t*>(p) = f32_to_bf16(v);
-}
-
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaChunkParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -262,24 +258,44 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         mma_bf16(xv[0], e, bb[0], bb[1]);
         mma_bf16(xv[1], e, bb[2], bb[3]);
       }
+      const float gh[2] = {F[kfGhi * kC + r0], F[kfGhi * kC + r1]};
+      const float gl[2] = {F[kfGlo * kC + r0], F[kfGlo * kC + r1]};
+      const float kn[2] = {F[kfKn * kC + r0], F[kfKn * kC + r1]};
+      const float qn[2] = {F[kfQn * kC + r0], F[kfQn * kC + r1]};
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
+        const int j0 = 16 * part + 8 * y + 2 * (lane & 3);
+        const float2 ch = *reinterpret_cast<const float2*>(F + kfGhi * kC + j0);
+        const float2 cl = *reinterpret_cast<const float2*>(F + kfGlo * kC + j0);
+        const float2 cb = *reinterpret_cast<const float2*>(F + kfBeta * kC + j0);
+        const float2 ck = *reinterpret_cast<const float2*>(F + kfKn * kC + j0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int i = q < 2 ? r0 : r1, j = 16 * part + 8 * y + 2 * (lane & 3) + (q & 1);
-          const float gm = j <= i ? ex2_approx((F[kfGhi * kC + i] - F[kfGhi * kC + j]) +
-                                               (F[kfGlo * kC + i] - F[kfGlo * kC + j]))
-                                  : 0.f;
-          const float kni = F[kfKn * kC + i], knj = F[kfKn * kC + j];
-          const float gb = gm * F[kfBeta * kC + j];
-          const float w = j <= i ? gb * wv[y][q] : 0.f;
-          const float n = j < i ? -gb * xv[y][q] : 0.f;
-          if (j < i) cs[y][q & 1] = fmaf(gm * kni * knj * kk[y][q], xv[y][q], cs[y][q & 1]);
-          st16(smem + g.w1 + i * kWs + j * 2, w * knj);
-          st16(smem + g.w2 + i * kWs + j * 2, w * F[kfQn * kC + i]);
-          if (j <= i) {
-            st16(smem + g.ns + i * kWs + j * 2, n * knj);
-            st16(smem + g.ns + j * kWs + i * 2, n * kni);
+        for (int x = 0; x < 2; ++x) {  // rows r0, r1: an 8 x 8 matrix each
+          const int i = x ? r1 : r0;
+          float w[2], n[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int j = j0 + q;
+            const float knj = q ? ck.y : ck.x, dv = xv[y][2 * x + q];
+            const float gm = j <= i ? ex2_approx((gh[x] - (q ? ch.y : ch.x)) + (gl[x] - (q ? cl.y : cl.x)))
+                                    : 0.f;
+            const float gb = gm * (q ? cb.y : cb.x);
+            w[q] = j <= i ? gb * wv[y][2 * x + q] : 0.f;
+            n[q] = j < i ? -gb * dv : 0.f;
+            if (j < i) cs[y][q] = fmaf(gm * kn[x] * knj * kk[y][2 * x + q], dv, cs[y][q]);
+          }
+          const int at = i * kWs + j0 * 2;
+          *reinterpret_cast<uint32_t*>(smem + g.w1 + at) = pack_bf16x2(w[0] * ck.x, w[1] * ck.y);
+          *reinterpret_cast<uint32_t*>(smem + g.w2 + at) = pack_bf16x2(w[0] * qn[x], w[1] * qn[x]);
+          // N and its mirror image; a matrix on the diagonal holds both
+          const uint32_t lo = pack_bf16x2(n[0] * ck.x, n[1] * ck.y);
+          const uint32_t up = transpose8(pack_bf16x2(n[0] * kn[x], n[1] * kn[x]));
+          if (part < mi || x > y) {
+            const int jt = 16 * part + 8 * y + (lane >> 2), it = 16 * mi + 8 * x + 2 * (lane & 3);
+            *reinterpret_cast<uint32_t*>(smem + g.ns + at) = lo;
+            *reinterpret_cast<uint32_t*>(smem + g.ns + jt * kWs + it * 2) = up;
+          } else if (x == y) {
+            *reinterpret_cast<uint32_t*>(smem + g.ns + at) = lo | up;
           }
         }
       }

@@ -55,13 +55,6 @@ struct PrepSmem {
   static constexpr int kBytes = kA + kScal + kTok + kCols + 64;
 };
 
-// The transpose of the warp's 8 x 8 matrix of 16-bit values.
-__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-
 // tf32 MMA of two-piece fp32 operands: d += a b, hi lo cross terms included.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
