@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   const int nt_row = (lane & 7) + ((lane & 16) >> 1), nt_u = (lane >> 3) & 1;
   const int tr_row = (lane & 7) + (lane & 8), tr_u = lane >> 4;
   const int r0 = mi * 16 + (lane >> 2), r1 = r0 + 8;
+  chain_go();
+  chain_wait();
 
   // ---- raw k and q
   constexpr int LPR = N / 8;
@@ -459,14 +461,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 }
 
 // dA, ddt_bias: the chunks' sums of one head, in a fixed order.
-__global__ void __launch_bounds__(128) delta_grad_reduce(const double* part, int64_t rows, int nheads,
-                                                         float* dA, float* dbias) {
+__global__ void __launch_bounds__(128) delta_grad_reduce(const DeltaChunkParams p) {
   __shared__ double sh[2][128];
+  const int64_t rows = (int64_t)p.d.batch * p.nchunks;
+  const int nheads = p.d.nheads;
+  chain_wait();
   const int h = blockIdx.x, tid = threadIdx.x;
   double a = 0.0, s = 0.0;
   for (int64_t i = tid; i < rows; i += 128) {
-    a += part[(i * nheads + h) * 2];
-    s += part[(i * nheads + h) * 2 + 1];
+    a += p.ws_part[(i * nheads + h) * 2];
+    s += p.ws_part[(i * nheads + h) * 2 + 1];
   }
   sh[0][tid] = a;
   sh[1][tid] = s;
@@ -479,8 +483,8 @@ __global__ void __launch_bounds__(128) delta_grad_reduce(const double* part, int
     __syncthreads();
   }
   if (tid == 0) {
-    if (dA) dA[h] = (float)sh[0][0];
-    if (dbias) dbias[h] = (float)sh[1][0];
+    if (p.dA) p.dA[h] = (float)sh[0][0];
+    if (p.ddt_bias) p.ddt_bias[h] = (float)sh[1][0];
   }
 }
 
@@ -489,12 +493,10 @@ cudaError_t launch(const DeltaChunkParams& p, cudaStream_t stream) {
   const int bytes = grad_layout(N, p.d.headdim).bytes;
   cudaError_t e = allow_shared(delta_grad_kernel<N>);
   if (e != cudaSuccess) return e;
-  delta_grad_kernel<N><<<dim3(p.nchunks, p.d.nkheads, p.d.batch), kThreads, bytes, stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_chained(delta_grad_kernel<N>, dim3(p.nchunks, p.d.nkheads, p.d.batch), kThreads, bytes,
+                     stream, p);
   if (e != cudaSuccess || (!p.dA && !p.ddt_bias)) return e;
-  delta_grad_reduce<<<p.d.nheads, 128, 0, stream>>>(p.ws_part, (int64_t)p.d.batch * p.nchunks,
-                                                    p.d.nheads, p.dA, p.ddt_bias);
-  return cudaGetLastError();
+  return launch_chained(delta_grad_reduce, dim3(p.d.nheads), 128, 0, stream, p);
 }
 
 }  // namespace

@@ -118,7 +118,8 @@ __device__ __forceinline__ void block_store(const float (&d)[2][4], float* D, fl
 }
 
 template <int N, bool BWD>
-__global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChunkParams p) {
+__global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChunkParams p, const int heads) {
+  chain_go();
   extern __shared__ __align__(128) unsigned char smem[];
   using Sm = PrepSmem<N>;
   constexpr int LPR = N / 8;       // lanes (16-byte units) per row
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
   const DeltaParams& d_ = p.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x, b = blockIdx.z;
-  const int rep = d_.nheads / d_.nkheads, subs = (rep + kHeads - 1) / kHeads;
+  const int rep = d_.nheads / d_.nkheads, subs = (rep + heads - 1) / heads;
   const int kh = blockIdx.y / subs, sub = blockIdx.y - kh * subs;
   const int64_t t0 = (int64_t)c * kC;
   const int valid = (int)min((int64_t)kC, d_.seqlen - t0);
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
   for (int j = 0; j < 8; ++j)
     if (j <= 2 * warp + 1) kk_at[j * 32] = make_float4(kk[j][0], kk[j][1], kk[j][2], kk[j][3]);
 
-  const int nh = min(kHeads, rep - sub * kHeads);
+  const int nh = min(heads, rep - sub * heads);
   const int r0 = warp * 16 + (lane >> 2), r1 = r0 + 8;
   constexpr int kTiles = BWD ? 4 : 3;
   for (int x = 0; x < nh; ++x) {
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       double g = 0.0;
       float beta = 0.f;
       if (xg < nh && i < valid) {
-        const int h = kh * rep + sub * kHeads + xg;
+        const int h = kh * rep + sub * heads + xg;
         const size_t at = ((size_t)b * d_.seqlen + t0 + i) * d_.nheads + h;
         const float raw = bf16_to_f32(static_cast<const uint16_t*>(d_.dt)[at]) +
                           (d_.dt_bias ? d_.dt_bias[h] : 0.f);
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       }
       __syncthreads();
     }
-    unsigned char* tri = p.ws_head + (bc * d_.nheads + kh * rep + sub * kHeads + x) * (size_t)p.head_bytes;
+    unsigned char* tri = p.ws_head + (bc * d_.nheads + kh * rep + sub * heads + x) * (size_t)p.head_bytes;
     float* sc = scal + (x & 1) * (kDeltaScalBwd / 4);
     const float gh0 = sc[kScGhi * kC + r0], gl0 = sc[kScGlo * kC + r0];
     const float gh1 = sc[kScGhi * kC + r1], gl1 = sc[kScGlo * kC + r1];
@@ -497,9 +498,15 @@ cudaError_t launch(const DeltaChunkParams& p, cudaStream_t stream) {
   auto* kern = delta_prep_kernel<N, BWD>;
   const cudaError_t e = allow_shared(kern);
   if (e != cudaSuccess) return e;
-  const int rep = p.d.nheads / p.d.nkheads, subs = (rep + kHeads - 1) / kHeads;
-  kern<<<dim3(p.nchunks, p.d.nkheads * subs, p.d.batch), kThreads, PrepSmem<N>::kBytes, stream>>>(
-      p);
+  // heads per CTA, halved while the grid then still fits the SMs at once
+  const int rep = p.d.nheads / p.d.nkheads;
+  auto ctas = [&](int heads) {
+    return (int64_t)p.nchunks * p.d.batch * p.d.nkheads * ((rep + heads - 1) / heads);
+  };
+  int heads = rep < kHeads ? rep : kHeads;
+  while (heads > 1 && ctas(heads / 2) <= 4 * 148) heads /= 2;
+  const dim3 grid(p.nchunks, p.d.nkheads * ((rep + heads - 1) / heads), p.d.batch);
+  kern<<<grid, kThreads, PrepSmem<N>::kBytes, stream>>>(p, heads);
   return cudaGetLastError();
 }
 

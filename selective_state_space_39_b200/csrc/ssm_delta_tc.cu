@@ -340,6 +340,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tm = __shfl_sync(0xffffffffu, slot, 0);
+  chain_go();
+  chain_wait();
 
   // a block's warps lie in one warpgroup column (warp % 4), which fixes the
   // tensor memory lanes they reach
@@ -630,6 +632,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tm = __shfl_sync(0xffffffffu, slot, 0);
+  chain_go();
+  chain_wait();
 
   const int blk = warp & 3, hf = (warp >> 2) & 1;
   if (warp >= kRowWarps) {
@@ -843,8 +847,7 @@ cudaError_t run(K* one, K* two, DeltaChunkParams p, int tiles, int head_bytes, i
   K* kern = blocks <= 4 ? two : one;
   const cudaError_t e = allow_shared<K>(kern);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)ctas(blocks), kTcThreads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(kern, dim3((unsigned)ctas(blocks)), kTcThreads, bytes, stream, p);
 }
 template <int N, bool BWD>
 cudaError_t fwd(const DeltaChunkParams& p, cudaStream_t stream) {
