@@ -447,7 +447,7 @@ int ssm_ssd_state_update(int64_t batch, int64_t nheads, int64_t headdim, int64_t
 
 /*
  * ssm_gated_delta_fwd -- the gated delta rule over a sequence. bf16 io with
- * dstate 64 or 128, headdim a multiple of 16, at least 48 tokens (from 8 on
+ * dstate 64 or 128, headdim a multiple of 16, at least 36 tokens (from 6 on
  * over a state of many rows) and 16-byte aligned q, k, v and y runs chunk by
  * chunk (64 tokens) on the tensor cores,
  * every product on the state's path in two fp16 pieces per fp32 operand, so

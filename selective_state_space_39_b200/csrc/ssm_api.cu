@@ -944,17 +944,17 @@ static int delta_dims_status(const DeltaDims& d) {
   return SSM_OK;
 }
 
-// Chunk by chunk, or token by token (without a workspace)? A chunk costs 16 to
-// 54 us whatever its tokens, a token 0.3 us while the state's rows leave the GPU
+// Chunk by chunk, or token by token (without a workspace)? One chunk costs 12 to
+// 57 us whatever its tokens, a token 0.25 us while the state's rows leave the GPU
 // empty and then its share of the rows' arithmetic. Measured, chunks against
-// tokens: 1024 rows of 128 x 64, 48 tokens 16.0 / 15.2 us; 8192 rows of 128 (here
-// and below), 24 tokens 26.5 / 27.4; 16384 rows, 10 and 12 tokens 25.5 / 26.4 and
-// 28.8 / 29.9; 32768 rows, 6 and 8 tokens 37.3 / 30.6 and 37.5 / 36.5; 65536 rows,
-// 4 and 8 tokens 53.8 / 51.2 and 53.4 / 75.6.
+// tokens (us): 512 rows of 64, 36 tokens 11.8 / 12.0; rows of 128: 4096, 28 tokens
+// 16.1 / 16.3 and 32 tokens 16.1 / 18.1; 8192, 16 tokens 17.0 / 19.3; 16384, 8
+// tokens 20.2 / 21.3; 32768, 6 tokens 29.6 / 30.5; 65536, 4 and 6 tokens 57.3 /
+// 46.8 and 59.2.
 static bool delta_chunked(const DeltaDims& d) {
   const int64_t rows = d.batch * d.nheads * d.headdim;
   return d.io == SSM_DTYPE_BF16 && delta_chunk_supported((int)d.dstate, (int)d.headdim) &&
-         (d.seqlen >= 48 || (d.seqlen >= 8 && d.seqlen * rows >= 3 << 16));
+         (d.seqlen >= 36 || (d.seqlen >= 6 && d.seqlen * rows >= 1 << 17));
 }
 
 struct DeltaWs {
