@@ -15,11 +15,20 @@
 // head adds its value heads in order, so dq and dk are written once, through
 // x / |x| when q and k were scaled to unit length. Operands are bf16 (q, k, dy
 // exactly; S, dS, r, dv and the weights rounded once), sums fp32: the outputs
-// are bf16 themselves. <S_end, dS_end> comes from the reverse pass, in fp32.
+// are bf16 themselves (dq, dk: 3.0e-3 from the exact ones in the 2-norm, 1.7e-3
+// of it the last rounding). <S_end, dS_end> comes from the reverse pass, in fp32.
 //
 // One CTA of sixteen warps fills an SM's shared memory: a warp takes 16 tokens
 // by a quarter of the columns; the head's tiles come by asynchronous copies,
-// the states' while the weights are computed.
+// the states' while the weights are computed, the next head's while the last
+// products run. Two warps without weights take the gates meanwhile.
+//
+// 2 x 2048 tokens, 32 heads of 128 on 16 key heads, dstate 128: 137 us for
+// 25.8 GFLOP and 300 MB. Bound: the phases of a head (copies, weights, products
+// with the states, products with the weights) follow one another with all warps:
+// tensor pipe 32 % busy, DRAM 34 %. It was 176 us with the gates after the
+// products, 148 with dy and dv meeting S one after the other and the weights
+// stored element by element.
 #include "ssm_delta.cuh"
 
 namespace ssm {

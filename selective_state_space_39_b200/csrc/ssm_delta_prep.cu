@@ -23,11 +23,11 @@
 // around the start of the row's block, e^(G_i - G_s) e^(G_s - G_j), neither
 // above 1; inside them it is taken from the difference itself.
 //
-// Bound: the latencies of about 1900 instructions per warp and head (issue slots
-// 53 % busy, shared memory 57 %, DRAM 33 %) at four CTAs per SM; five, with 96
-// registers, took 233 us where four take 219 (4 x 4096 tokens, 64 heads, 16 key
-// heads, dstate 128; 550 MB read and written). 8192 tokens of 32 heads and 16 key
-// heads: 77 us; for the backward pass 2 x 2048 tokens of 32 heads: 46 us.
+// Bound: the latencies of about 1900 instructions per warp and head, at four CTAs
+// per SM (issue slots 53 % busy, tensor pipe 20 %, DRAM 2.3 TB/s): 219 us for
+// 4 x 4096 tokens, 64 heads on 16 key heads, dstate 128 (550 MB read and
+// written); five CTAs of 96 registers took 233. 8192 tokens of 32 heads: 77 us; for
+// the backward pass, 2 x 2048 tokens of 32 heads: 46 us.
 #include "ssm_delta.cuh"
 
 namespace ssm {
@@ -498,7 +498,8 @@ cudaError_t launch(const DeltaChunkParams& p, cudaStream_t stream) {
   auto* kern = delta_prep_kernel<N, BWD>;
   const cudaError_t e = allow_shared(kern);
   if (e != cudaSuccess) return e;
-  // heads per CTA, halved while the grid then still fits the SMs at once
+  // heads per CTA, halved while the grid then still fits the SMs at once (2 x 203
+  // tokens of 8 heads on 4 key heads: 13.9 us with two heads per CTA, 11.2 with one)
   const int rep = p.d.nheads / p.d.nkheads;
   auto ctas = [&](int heads) {
     return (int64_t)p.nchunks * p.d.batch * p.d.nkheads * ((rep + heads - 1) / heads);

@@ -38,6 +38,14 @@
 // dh0 and the gate gradients keep fp32's accuracy; for y, rounded to bf16, one
 // fp16 piece (2^-12) of S, u and P is taken.
 //
+// Bound: the chain of a chunk (products, commits, tensor memory loads, row maxima,
+// splitting; 1.3 us of it in the two products from S to u), in every head at once:
+// 8192 tokens of 32 heads of 128, dstate 128 take 302 us, 2.4 us per chunk (128
+// CTAs of 32 rows; 126 MB); 4 x 4096 tokens of 64 heads of 64: 253 us, 4.0 us per
+// chunk (128 CTAs of 128 rows; tensor pipe 27 % busy, DRAM 2.4 TB/s). For the
+// backward pass, 2 x 2048 tokens of 32 heads of 128: 125 us, and 151 us back; both
+// move a state per chunk (2.6 TB/s).
+//
 // Tensor memory (512 columns), forward: 0 S pieces, then u's pieces for P; 128 K S, R's
 // pieces, u's pieces for K^T; 192 Q S; 256 T R per head, then K^T u; 384 P u
 // per head. Back: 0 dS pieces; 128 K dS, dU's pieces, dR's pieces; 192 dY's
@@ -822,8 +830,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // The largest number of row blocks per CTA (one CTA fills an SM) of at most two
 // heads and two stages, halved while the grid then still is no larger than the
-// SMs: the chain is shorter with fewer warps per scheduler. `one`: the kernel of
-// one warp per block, taken above four blocks; null where there is none.
+// SMs: the chain is shorter with fewer warps per scheduler. Whole calls with 1, 2,
+// 4 and 8 blocks: 8192 tokens of 32 heads of 128 (256, 128, 64, 32 CTAs) 688, 388,
+// 395, 534 us; 4 x 4096 of 64 heads of 64 (1024 .. 128 CTAs) 1295, 845, 548, 489.
+// `one`: the kernel of one warp per block, taken above four blocks; null where
+// there is none.
 // block_bytes: shared memory per row block beside its column tiles.
 template <int N, typename K>
 cudaError_t run(K* one, K* two, DeltaChunkParams p, int tiles, int head_bytes, int block_bytes,
