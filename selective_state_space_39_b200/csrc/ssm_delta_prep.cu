@@ -25,8 +25,8 @@
 //
 // Bound: the latencies of about 1900 instructions per warp and head, at four CTAs
 // per SM (issue slots 53 % busy, tensor pipe 20 %, DRAM 2.3 TB/s): 219 us for
-// 4 x 4096 tokens, 64 heads on 16 key heads, dstate 128 (550 MB read and
-// written); five CTAs of 96 registers took 233. 8192 tokens of 32 heads: 77 us; for
+// 4 x 4096 tokens, 64 heads on 16 key heads, dstate 128 (500 MB of DRAM
+// traffic); five CTAs of 96 registers took 233. 8192 tokens of 32 heads: 77 us; for
 // the backward pass, 2 x 2048 tokens of 32 heads: 46 us.
 #include "ssm_delta.cuh"
 

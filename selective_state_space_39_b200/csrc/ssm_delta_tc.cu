@@ -39,9 +39,8 @@
 // fp16 piece (2^-12) of S, u and P is taken.
 //
 // Bound: the chain of a chunk (products, commits, tensor memory loads, row maxima,
-// splitting; 1.3 us of it in the two products from S to u), in every head at once:
-// 8192 tokens of 32 heads of 128, dstate 128 take 302 us, 2.4 us per chunk (128
-// CTAs of 32 rows; 126 MB); 4 x 4096 tokens of 64 heads of 64: 253 us, 4.0 us per
+// splitting), in every head at once: 8192 tokens of 32 heads of 128, dstate 128
+// take 302 us, 2.4 us per chunk (128 CTAs of 32 rows); 4 x 4096 tokens of 64 heads of 64: 253 us, 4.0 us per
 // chunk (128 CTAs of 128 rows; tensor pipe 27 % busy, DRAM 2.4 TB/s). For the
 // backward pass, 2 x 2048 tokens of 32 heads of 128: 125 us, and 151 us back; both
 // move a state per chunk (2.6 TB/s).
