@@ -439,7 +439,7 @@ int ssm_ssd_state_update(int64_t batch, int64_t nheads, int64_t headdim, int64_t
  *   q, k     : (batch, seqlen, nkheads, dstate) io_dtype, nheads a multiple of nkheads
  *   v, y     : (batch, seqlen, nheads, headdim) io_dtype
  *   dt, beta : (batch, seqlen, nheads)          io_dtype
- *   A        : (nheads) fp32, not positive (A * Delta is a log decay);
+ *   A        : (nheads) fp32 (A * Delta is a log decay, meant not to be positive);
  *   dt_bias  : (nheads) fp32, nullable
  *   h0, h_last : (batch, nheads, headdim, dstate) fp32, nullable; 16-byte aligned
  * dstate 32, 64, 128 or 256; any headdim; q and k aligned to four elements.

@@ -272,7 +272,10 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
         sc[kScKend * kC + i] = tok[i] * E;
         sc[kScK * kC + i] = tok[i];
         sc[kScSq * kC + i] = D * tok[kC + i];
-        sc[kScEnd * kC + i] = ex2_approx(ehi + elo);
+        if (i == 0) sc[kScEnd * kC] = ex2_approx(ehi + elo);
+        // (1 where no decay is above 1)
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(E, 1.f)));
+        if (lane == 0) sc[kScEnd * kC + 1 + (warp & 1)] = __uint_as_float(most);
         sc[kScKn * kC + i] = tok[2 * kC + i];
         sc[kScQn * kC + i] = tok[3 * kC + i];
       }

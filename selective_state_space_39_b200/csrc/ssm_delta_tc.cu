@@ -465,9 +465,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) u[j][q] = x[j][q];
         scale_cols(u, sc + kScKend * kC + tk, lane);
-        // e^(G_end - G) <= 1: one scale serves u's pieces for K^T and for P
+        // one scale serves u's pieces for K^T and for P: e^(G_end - G) is at most
+        // `most`, 1 unless a log decay is positive
+        const float most = fmaxf(sc[kScEnd * kC + 1], sc[kScEnd * kC + 2]);
         scale_cols(x, sc + kScK * kC + tk, lane);
         row_max(x, m0, m1);
+        m0 *= most;
+        m1 *= most;
         meet(m0, m1, 2);
         r0 = row_scale(exponent_of(m0));
         r1 = row_scale(exponent_of(m1));

@@ -218,3 +218,54 @@ def test_shared_workspace_of_two_graphs():
     for i in (0, 1, 1, 0):
         graphs[i][0].replay()
         assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+
+
+def test_decays_above_one():
+    """Growing states (A > 0, and steps of either sign without softplus)."""
+    d = R.make_delta(1, 150, 4, 2, 64, 128, BF, 12)
+    d["A"] = d["A"].abs() * 0.02
+    check_fwd(d, BF, "A > 0")
+    check_bwd(d, "A > 0")
+    d = R.make_delta(1, 150, 4, 2, 64, 64, BF, 13)
+    d["dt"] = (d["dt"].float() * 0.1).to(BF)
+    d["A"], d["dt_bias"] = d["A"] * 0.1, None
+    check_fwd(d, BF, "signed steps", softplus=False)
+
+
+def big(B, L, Hh, Hk, Pp, Nn, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=BF)  # noqa: E731
+    return {"q": n(B, L, Hk, Nn), "k": n(B, L, Hk, Nn), "v": n(B, L, Hh, Pp),
+            "dt": n(B, L, Hh) - 3, "A": -1 - torch.arange(Hh, device="cuda") / 8.0,
+            "beta": n(B, L, Hh), "dt_bias": torch.zeros(Hh, device="cuda"), "h0": None}
+
+
+def row(d, b, lo, hi):
+    return {n: (t[b:b + 1, lo:hi].contiguous() if t is not None and t.dim() > 1 else t)
+            for n, t in d.items()}
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of v: the last batch row is that row's own call,
+    and its first tokens are the reference's."""
+    d = big(2, 131136, 64, 16, 128, 64, 1)
+    assert d["v"].numel() > 2 ** 31
+    y, S = fwd(d)
+    y1, S1 = fwd(row(d, 1, 0, 131136))
+    assert torch.equal(y[1], y1[0]) and torch.equal(S[1], S1[0])
+    c = {n: (t.cpu() if t is not None else None) for n, t in row(d, 1, 0, 70).items()}
+    yr, _ = R.delta(c["q"], c["k"], c["v"], c["dt"], c["A"], c["beta"], dt_bias=c["dt_bias"])
+    near(y[1:2, :70], yr, (3.5e-3, 8e-3), "y")
+
+
+def test_bwd_offsets_past_32_bits():
+    """More than 2^31 elements of states between the walks: the last batch row's
+    gradients are those of the row's own call."""
+    d = big(2, 65600, 64, 16, 128, 128, 2)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    d["dy"] = torch.randn(d["v"].shape, generator=g, device="cuda", dtype=BF)
+    assert 2 * 65600 // 64 * 64 * 128 * 128 > 2 ** 31
+    a = bwd(d)
+    b = bwd(row(d, 1, 0, 65600))
+    for n in ("dq", "dk", "dv", "ddt", "dbeta", "dh0"):
+        assert torch.isfinite(a[n][1].float()).all() and torch.equal(a[n][1], b[n][0]), n
