@@ -14,7 +14,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("ssm_scan_kernels.cu", "ssm_scan_bwd.
                                            "ssm_delta_step.cu", "ssm_delta_prep.cu",
                                            "ssm_delta_tc.cu", "ssm_delta_grad.cu", "ssm_norm.cu",
                                            "ssm_api.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in ("ssm_device.cuh", "ssm_internal.h",
+HEADERS = [os.path.join(CSRC, f) for f in ("ssm_device.cuh", "ssm_chain.cuh", "ssm_internal.h",
                                             "ssm_bwd_internal.h", "ssm_conv_internal.h",
                                             "ssm_seqpar_internal.h", "ssm_ssd_internal.h", "ssm_tc.cuh",
                                             "ssm_ssd_decode_internal.h",

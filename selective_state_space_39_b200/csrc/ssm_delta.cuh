@@ -4,6 +4,7 @@
 
 #include <cuda_fp16.h>
 
+#include "ssm_chain.cuh"
 #include "ssm_delta_internal.h"
 #include "ssm_device.cuh"
 
@@ -111,14 +112,6 @@ __device__ __forceinline__ void row_max(const float (&x)[T][4], float& m0, float
     m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
-}
-// Before the first read of what the preceding kernel of the call wrote.
-__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next kernel's blocks may take the places that this kernel's leave; only
-// called once a block holds its tensor memory, so that none of them can wait
-// for columns that a waiting successor has taken.
-__device__ __forceinline__ void chain_go() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 // The transpose of the warp's 8 x 8 matrix of 16-bit values.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {

@@ -38,25 +38,6 @@ inline cudaError_t allow_shared(K* kern) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
 }
 
-// A kernel of a call whose predecessor on the stream is the call's own: it may
-// start while that one's last blocks run, and waits for it (chain_wait) before
-// it reads anything.
-template <typename P>
-inline cudaError_t launch_chained(void (*kern)(P), dim3 grid, int threads, int bytes,
-                                  cudaStream_t stream, const P& p) {
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid;
-  c.blockDim = dim3((unsigned)threads);
-  c.dynamicSmemBytes = (size_t)bytes;
-  c.stream = stream;
-  c.attrs = &a;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, p);
-}
-
 // dstate values of the token-by-token kernel (any headdim, fp32 or bf16 io).
 bool delta_step_dstate_supported(int dstate);
 cudaError_t launch_delta_step(const DeltaParams& p, bool bf16, cudaStream_t stream);

@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "ssm_chain.cuh"
 #include "ssm_device.cuh"
 #include "ssm_norm_internal.h"
 
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormParams p, int T
 // loaded before the present ones are finished.
 template <typename IOT, typename RT, int V, int M, bool FIT, int GATE>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, int T) {
+  chain_go();
   extern __shared__ float dws[];  // dw sums of the block's row groups
   __shared__ float sh[64];
   using P = Pairs<V>;
@@ -417,9 +419,12 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormParams p, int T
 }
 
 // dw: 32 columns per block, the slices' sums by 32 warps in a fixed order.
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int slices, int dim,
-                                                       float* dw) {
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const NormParams p) {
   __shared__ float sh[32][33];
+  const float* part = p.ws;
+  const int slices = p.slices, dim = p.dim;
+  float* dw = p.dw;
+  chain_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (col < dim) {
@@ -463,19 +468,18 @@ cudaError_t fwd_m(const NormParams& p, const Shape& s, cudaStream_t stream) {
 }
 
 template <typename K>
-cudaError_t run_bwd(K* kern, const NormParams& p, const Shape& s, cudaStream_t stream) {
-  const int slices = norm_bwd_slices(p.rows, p.groups);
+cudaError_t run_bwd(K* kern, NormParams p, const Shape& s, cudaStream_t stream) {
+  p.slices = norm_bwd_slices(p.rows, p.groups);
   const size_t bytes = p.dw ? ((size_t)(s.M ? s.threads / s.T : 1) * p.width + 1) * 4 : 0;
   if (bytes > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
   }
-  kern<<<dim3(slices, p.groups), s.threads, bytes, stream>>>(p, s.T);
+  kern<<<dim3(p.slices, p.groups), s.threads, bytes, stream>>>(p, s.T);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.dw) return e;
-  norm_dw_kernel<<<(p.dim + 31) / 32, 1024, 0, stream>>>(p.ws, slices, p.dim, p.dw);
-  return cudaGetLastError();
+  return launch_chained(norm_dw_kernel, dim3((p.dim + 31) / 32), 1024, 0, stream, p);
 }
 
 template <typename IOT, typename RT, int V, int GATE>

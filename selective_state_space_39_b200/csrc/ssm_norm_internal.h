@@ -28,7 +28,8 @@ struct NormParams {
   void* dresidual;       // (rows, dim) like h, or null
   void* dz;              // (rows, dim) io, with a gate
   float* dw;             // (dim) or null
-  float* ws;             // (norm_bwd_slices, dim) partial dw
+  float* ws;             // (slices, dim) partial dw
+  int slices;            // norm_bwd_slices (set by the launch)
 };
 
 // types: 0 io bf16, h bf16; 1 io bf16, h fp32; 2 both fp32
