@@ -670,6 +670,23 @@ def _delta_inputs(sizes, dev, q, k, v, dt, A, beta, dt_bias, tokens):
     ty = v.dtype
     f32 = torch.float32
     qk, gate = ((B, L, Hk, N), (B, L, H)) if tokens else ((B, Hk, N), (B, H))
+    if dt_bias is not None:
+        try:  # one test of everything; what is wrong is found below
+            i = dev.index
+            if (q.shape == qk and k.shape == qk and dt.shape == gate and beta.shape == gate
+                    and A.shape == (H,) and dt_bias.shape == (H,)
+                    and q.dtype is ty and k.dtype is ty and dt.dtype is ty and beta.dtype is ty
+                    and A.dtype is f32 and dt_bias.dtype is f32
+                    and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+                    and dt.is_contiguous() and beta.is_contiguous() and A.is_contiguous()
+                    and dt_bias.is_contiguous()
+                    and q.get_device() == i and k.get_device() == i and dt.get_device() == i
+                    and beta.get_device() == i and A.get_device() == i
+                    and dt_bias.get_device() == i):
+                return (q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), A.data_ptr(),
+                        beta.data_ptr(), dt_bias.data_ptr())
+        except AttributeError:
+            pass
     return (_at(q, "q", ty, qk, dev), _at(k, "k", ty, qk, dev), _at(v, "v", ty, v.shape, dev),
             _at(dt, "dt", ty, gate, dev), _at(A, "A", f32, (H,), dev),
             _at(beta, "beta", ty, gate, dev), _at(dt_bias, "dt_bias", f32, (H,), dev))
