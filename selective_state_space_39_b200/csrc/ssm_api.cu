@@ -958,7 +958,7 @@ static bool delta_chunked(const DeltaDims& d) {
 }
 
 struct DeltaWs {
-  size_t kq, head, state, state16, dstate16, end, r, doto, dotv, dotu, part, bytes;
+  size_t kq, head, state, state16, dstate16, end, r, doto, dotv, dotb, part, bytes;
 };
 static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
   DeltaWs w{};
@@ -981,7 +981,7 @@ static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
     w.r = take((size_t)d.batch * d.seqlen * d.nheads * d.headdim * 2);
     w.doto = take(dots);
     w.dotv = take(dots);
-    w.dotu = take(dots);
+    w.dotb = take(dots);
     w.part = take(bc * d.nheads * 2 * 8);
   }
   w.bytes = off;
@@ -1029,7 +1029,7 @@ static DeltaChunkParams delta_chunk_params(const DeltaParams& dp, const DeltaDim
     p.ws_r = reinterpret_cast<uint16_t*>(ws + w.r);
     p.ws_doto = reinterpret_cast<float*>(ws + w.doto);
     p.ws_dotv = reinterpret_cast<float*>(ws + w.dotv);
-    p.ws_dotu = reinterpret_cast<float*>(ws + w.dotu);
+    p.ws_dotb = reinterpret_cast<float*>(ws + w.dotb);
     p.ws_part = reinterpret_cast<double*>(ws + w.part);
   }
   return p;

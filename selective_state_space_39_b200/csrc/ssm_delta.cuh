@@ -19,6 +19,10 @@ __device__ __forceinline__ float delta_beta(float raw, int sigmoid) {
   return sigmoid ? 1.f / (1.f + expf(-raw)) : raw;
 }
 
+__device__ __forceinline__ float delta_beta_floor(float beta) {
+  return fabsf(beta) < kBetaFloor ? copysignf(kBetaFloor, beta) : beta;
+}
+
 // ------------------------------------------------------ fragments and MMAs --
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"

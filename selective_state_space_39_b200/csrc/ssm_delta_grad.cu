@@ -7,8 +7,9 @@
 // N_ij = -(dv_i . u_j) e^(G_i - G_j) (j < i):
 //   dq_i = e^(G_i) S dy_i + sum_j W_ij k_j
 //   dk_j = e^(G_end - G_j) dS u_j - e^(G_j) S dv_j + sum_i W_ij q_i + sum_i (N + N^T)_ji k_i
-//   dbeta_j = du_j . r_j - sum_(i>j) (k_i . k_j) e^(G_i - G_j) (dv_i . r_j)
-// and, since a decay scales every later use of the state, the log decays'
+//   dbeta_j = dv_j . r_j / beta_j  (beta_j at least 2^-26)
+// (dv_j is beta_j times the adjoint of u_j, all its later uses included, so nothing
+// is left to subtract) and, since a decay scales every later use of the state, the log decays'
 // gradients need no matrix at all:
 //   dg_t = sum_(i >= t in the chunk) (dy_i . y_i - dv_i . v_i) + <S_end, dS_end>
 // whose row products the two passes took in fp32. One CTA per chunk and key
@@ -44,7 +45,7 @@ struct GradLayout {
   int xs, ps;  // row strides (bytes) of the dstate-wide and headdim-wide tiles
   int k, q, s, ds, dy, r, dr, w1, w2, ns, dots, f, bytes;
 };
-enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfCol, kfRow = kfCol + 4, kfCount };
+enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfRow, kfCount };
 
 __host__ __device__ inline GradLayout grad_layout(int N, int P) {
   GradLayout g;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     }
     if (tid < 3 * 16 * sl) {
       const int w = tid / (16 * sl), u = tid - w * 16 * sl;
-      const float* src = (w == 0 ? p.ws_dotu : (w == 1 ? p.ws_doto : p.ws_dotv)) + bch * sl * kC;
+      const float* src = (w == 0 ? p.ws_dotb : (w == 1 ? p.ws_doto : p.ws_dotv)) + bch * sl * kC;
       copy16(sm + g.dots + tid * 16, src + u * 4, true);
     }
     {  // half a warp per row of headdim (at most 16 units), two rows per thread and tensor
@@ -165,7 +166,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     }
   };
 
-  float kk[2][4] = {};
   float tq[T][4] = {}, tk[T][4] = {};
   load(0);
   for (int hx = 0; hx < rep; ++hx) {
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     cp_async_wait_group<1>();
     __syncthreads();
 
-    if (hx == 0) {  // 1 / (|x|^2 + eps) of every k and q row, and k k^T (for dbeta)
+    if (hx == 0) {  // 1 / (|x|^2 + eps) of every k and q row
       const int row = tid >> 3, l8 = tid & 7;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
@@ -191,16 +191,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (l8 == 0) F[(w ? kfLq : kfLk) * kC + row] = d.qk_norm ? 1.f / (ss + kDeltaQkEps) : 0.f;
-      }
-      if (part <= mi) {
-#pragma unroll
-        for (int kt = 0; kt < N / 16; ++kt) {
-          uint32_t a[4], bb[4];
-          ldsm4(a, sm + g.k + (mi * 16 + a_row) * g.xs + (2 * kt + a_u) * 16);
-          ldsm4(bb, sm + g.k + (16 * part + nt_row) * g.xs + (2 * kt + nt_u) * 16);
-          mma_bf16(kk[0], a, bb[0], bb[1]);
-          mma_bf16(kk[1], a, bb[2], bb[3]);
-        }
       }
     }
 
@@ -239,6 +229,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         dA = (double)dg * step;
         dbias = ddt;
         p.ddt[gate_at] = f32_to_bf16(ddt);
+        float db = 0.f;
+        for (int i = 0; i < sl; ++i) db += dots[i * kC];
+        db /= delta_beta_floor(F[kfBeta * kC + gt]);
+        if (d.beta_sigmoid) {
+          const float be = delta_beta(bf16_to_f32(beta_raw), 1);
+          db *= be * (1.f - be);
+        }
+        p.dbeta[gate_at] = f32_to_bf16(db);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -253,9 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       if (gt < 2) p.ws_part[bch * 2 + gt] = R[2 + gt] + R[4 + gt];
     }
 
-    // ---- dy r^T and dv r^T -> W, N + N^T, and the column sums of dbeta: rows of
-    // block mi, columns of block `part`
-    float cs[2][2] = {};
+    // ---- dy r^T and dv r^T -> W, N + N^T: rows of block mi, columns of block `part`
     if (part <= mi) {
       float wv[2][4] = {}, xv[2][4] = {};
 #pragma unroll 4
@@ -287,13 +283,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int j = j0 + q;
-            const float knj = q ? ck.y : ck.x, dv = xv[y][2 * x + q];
             const float gm = j <= i ? ex2_approx((gh[x] - (q ? ch.y : ch.x)) + (gl[x] - (q ? cl.y : cl.x)))
                                     : 0.f;
             const float gb = gm * (q ? cb.y : cb.x);
             w[q] = j <= i ? gb * wv[y][2 * x + q] : 0.f;
-            n[q] = j < i ? -gb * dv : 0.f;
-            if (j < i) cs[y][q] = fmaf(gm * kn[x] * knj * kk[y][2 * x + q], dv, cs[y][q]);
+            n[q] = j < i ? -gb * xv[y][2 * x + q] : 0.f;
           }
           const int at = i * kWs + j0 * 2;
           *reinterpret_cast<uint32_t*>(smem + g.w1 + at) = pack_bf16x2(w[0] * ck.x, w[1] * ck.y);
@@ -311,29 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         }
       }
     }
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) cs[y][q] += __shfl_xor_sync(0xffffffffu, cs[y][q], o);
-        if (lane < 4) F[(kfCol + mi) * kC + 16 * part + 8 * y + 2 * lane + q] = cs[y][q];
-      }
     cp_async_wait_group<0>();
     __syncthreads();
-
-    if (gate && gt < valid) {
-      const float* du = reinterpret_cast<const float*>(smem + g.dots) + gt;
-      float db = 0.f;
-      for (int i = 0; i < sl; ++i) db += du[i * kC];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) db -= F[(kfCol + i) * kC + gt];
-      if (d.beta_sigmoid) {
-        const float be = delta_beta(bf16_to_f32(beta_raw), 1);
-        db *= be * (1.f - be);
-      }
-      p.dbeta[gate_at] = f32_to_bf16(db);
-    }
 
     // ---- dq += e^G dy S + W k;  dk += beta e^(G_end - G) r dS - e^G dv S + W^T q + (N + N^T) k
     const float g0 = F[kfGhi * kC + r0], l0 = F[kfGlo * kC + r0];

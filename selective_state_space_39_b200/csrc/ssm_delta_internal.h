@@ -61,8 +61,13 @@ enum DeltaScal {       // arrays of 64 floats in a head block; the forward pass 
   kScGlo = 10,
   kScKn = 11,          // unit-length factor of k
   kScQn = 12,          // unit-length factor of q, times the readout scale
-  kScCount = 13,
+  kScRatio = 13,       // beta over its floored value (delta_beta_floor)
+  kScCount = 14,
 };
+// The backward pass takes a token's dbeta from its dv = beta du, so there T and dU
+// meet a beta of at least 2^-26 (r is then off by less than its own rounding), and dv
+// is scaled back afterwards.
+constexpr float kBetaFloor = 1.f / 67108864.f;
 // A lower triangular 64 x 64 fp16 tile: its ten 16 x 16 blocks (i, j <= i),
 // column of blocks by column, 512 bytes each, as 2 x 2 core matrices of eight
 // rows of 16 bytes (the tensor cores' layout without a swizzle; any eight rows
@@ -100,7 +105,7 @@ struct DeltaChunkParams {
   uint16_t* ws_r;        // (batch, seqlen, nheads, headdim): v minus the state's prediction
   float* ws_doto;        // (batch, nchunks, nheads, headdim/16, 64): dy.y over 16 rows
   float* ws_dotv;        //   ... dv.v
-  float* ws_dotu;        //   ... du.r
+  float* ws_dotb;        //   ... dv.r, before dv is scaled back to the token's own beta
   double* ws_part;       // (batch, nchunks, nheads, 2): partial dA, ddt_bias
   uint16_t *dq, *dk, *dv, *ddt, *dbeta;
   float *dA, *ddt_bias, *dh0;

@@ -258,6 +258,11 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       if (warp & 1) g += carry[warp >> 1];
       float* sc = scal + (warp >> 1) * (kDeltaScalBwd / 4);
       const float hi = (float)g;
+      if (BWD) {
+        const float use = delta_beta_floor(beta);
+        if (xg < nh) sc[kScRatio * kC + i] = use == beta ? 1.f : beta / use;
+        beta = use;
+      }
       if (xg < nh) {
         sc[kScGhi * kC + i] = hi;
         sc[kScGlo * kC + i] = (float)(g - (double)hi);
@@ -469,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       if (half == 0) {
         sc[kScU * kC + row] = sc[kScBeta * kC + row] * s.inv;
         sc[kScT * kC + row] = s.inv;
+        if (BWD) sc[kScBeta * kC + row] *= sc[kScRatio * kC + row];
         rows_s[row] = s.s;
       }
     }

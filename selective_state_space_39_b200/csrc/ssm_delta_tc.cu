@@ -755,13 +755,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_pieces<true, TT>(x, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
         wrote(&bars[kPutU]);
 
-        // ---- meanwhile: the next chunk's rows, du.r, dS for the gradients, <S, dS>
+        // ---- meanwhile: the next chunk's rows, dS for the gradients, <S, dS>
         const float dot = tiles_dot<NS>(S, after, lane);
         if (lane == 0) p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
         __syncwarp();
         if (c > 0) fetch(c - 1);
-        load_rows(x, vrow + 2 * kCol, tk, lc);
-        row_dots(u, x, p.ws_dotu + dot_at, lane);
         store_state16<N, NS>(S, out16, p.ws_dstate16 + st_at, lane);
         load_rows(y, vrow + kCol, tk, lc);
         scale_cols(y, sc + kScSq * kC + tk, lane);
@@ -786,6 +784,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
         tm_pieces<true, TT>(u, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
         wrote(&bars[kPutR]);
+        load_rows(u, vrow + 2 * kCol, tk, lc);
+        row_dots(x, u, p.ws_dotb + dot_at, lane);
+        scale_cols(x, sc + kScRatio * kC + tk, lane);
         load_rows(u, vrow, tk, lc);
         row_dots(x, u, p.ws_dotv + dot_at, lane);
         __syncwarp();
