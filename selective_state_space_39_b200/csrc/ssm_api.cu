@@ -958,7 +958,7 @@ static bool delta_chunked(const DeltaDims& d) {
 }
 
 struct DeltaWs {
-  size_t kq, head, state, state16, dstate16, end, r, doto, dotv, dotb, part, bytes;
+  size_t kq, head, state, state16, dstate16, end, first, r, rlo, dvlo, doto, dotv, doth, dotb, part, bytes;
 };
 static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
   DeltaWs w{};
@@ -978,9 +978,13 @@ static DeltaWs delta_ws(const DeltaDims& d, bool bwd) {
     w.state16 = take(bc * state / 2);
     w.dstate16 = take(bc * state / 2);
     w.end = take(bc * d.nheads * (d.headdim / 16) * 2 * 4);
+    w.first = take((size_t)d.batch * d.nheads * (d.headdim / 16) * 2 * 4);
     w.r = take((size_t)d.batch * d.seqlen * d.nheads * d.headdim * 2);
+    w.rlo = take((size_t)d.batch * d.seqlen * d.nheads * d.headdim * 2);
+    w.dvlo = take((size_t)d.batch * d.seqlen * d.nheads * d.headdim * 2);
     w.doto = take(dots);
     w.dotv = take(dots);
+    w.doth = take(dots);
     w.dotb = take(dots);
     w.part = take(bc * d.nheads * 2 * 8);
   }
@@ -1026,9 +1030,13 @@ static DeltaChunkParams delta_chunk_params(const DeltaParams& dp, const DeltaDim
     p.ws_state16 = reinterpret_cast<uint16_t*>(ws + w.state16);
     p.ws_dstate16 = reinterpret_cast<uint16_t*>(ws + w.dstate16);
     p.ws_end = reinterpret_cast<float*>(ws + w.end);
+    p.ws_first = reinterpret_cast<float*>(ws + w.first);
     p.ws_r = reinterpret_cast<uint16_t*>(ws + w.r);
+    p.ws_rlo = reinterpret_cast<uint16_t*>(ws + w.rlo);
+    p.ws_dvlo = reinterpret_cast<uint16_t*>(ws + w.dvlo);
     p.ws_doto = reinterpret_cast<float*>(ws + w.doto);
     p.ws_dotv = reinterpret_cast<float*>(ws + w.dotv);
+    p.ws_doth = reinterpret_cast<float*>(ws + w.doth);
     p.ws_dotb = reinterpret_cast<float*>(ws + w.dotb);
     p.ws_part = reinterpret_cast<double*>(ws + w.part);
   }

@@ -12,7 +12,16 @@
 // is left to subtract) and, since a decay scales every later use of the state, the log decays'
 // gradients need no matrix at all:
 //   dg_t = sum_(i >= t in the chunk) (dy_i . y_i - dv_i . v_i) + <S_end, dS_end>
-// whose row products the two passes took in fp32. One CTA per chunk and key
+// whose row products the two passes took in fp32. After a strong decay (kStrongDecay)
+// that sum is all cancellation, so there dg_t is taken from what passes over it,
+//   dg_t = sum_(j < t <= i) e^(G_i - G_j) [(dy_i . u_j)(q_i . k_j) - (dv_i . u_j)(k_i . k_j)]
+//        + sum_(i >= t) e^(G_i) [dy_i . S q_i - dv_i . S k_i]
+//        + sum_(j < t) e^(G_end - G_j) u_j . dS k_j + e^(G_end) <S, dS>,
+// every term with its decay, added up without a difference: row sums of a block's
+// pairs for the tokens of its rows, column sums for those of its columns. r and dv
+// then come as two bf16 pieces (2^-16); S and dS stay one, for they matter only to the
+// chunk's first and last tokens: the first one's dg is <S_end, dS_end> of the chunk
+// before, and the walk back takes the parts with dS in fp32. One CTA per chunk and key
 // head adds its value heads in order, so dq and dk are written once, through
 // x / |x| when q and k were scaled to unit length. Operands are bf16 (q, k, dy
 // exactly; S, dS, r, dv and the weights rounded once), sums fp32: the outputs
@@ -43,9 +52,15 @@ constexpr int kWs = kC * 2 + 16;  // row stride (bytes) of the 64 x 64 tiles
 
 struct GradLayout {
   int xs, ps;  // row strides (bytes) of the dstate-wide and headdim-wide tiles
-  int k, q, s, ds, dy, r, dr, w1, w2, ns, dots, f, bytes;
+  int k, q, s, ds, dy, r, dr, w1, w2, ns, dots, f, bytes;  // over w1 .. dots: the rests of r and dv
 };
-enum { kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfRow, kfCount };
+enum {
+  kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfRow,
+  // of a chunk with a strong decay: the tokens' parts with the entering state (a quarter
+  // of dstate each) and with dS, row sums by column block, column sums by row block,
+  // the pairs inside a token's own block; the warps' parts of <S, dS>
+  kfIn, kfOut = kfIn + 4, kfRows, kfCols = kfRows + 3, kfOwn = kfCols + 4, kfSum, kfCount
+};
 
 __host__ __device__ inline GradLayout grad_layout(int N, int P) {
   GradLayout g;
@@ -63,6 +78,7 @@ __host__ __device__ inline GradLayout grad_layout(int N, int P) {
   g.w2 = at; at += kC * kWs;
   g.ns = at; at += kC * kWs;
   g.dots = at; at += 3 * (P / 16) * kC * 4;
+  at = at - g.w1 < 2 * kC * g.ps ? g.w1 + 2 * kC * g.ps : at;
   g.f = at; at += kfCount * kC * 4;
   g.bytes = at;
   return g;
@@ -73,6 +89,337 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
                : "memory");
 }
+// <t, x> over a warp's quarter of dstate, rows r0 and r0 + 8 of a k or q tile (all lanes of a quad)
+template <int T>
+__device__ __forceinline__ void rows_dot(const float (&t)[T][4], const unsigned char* x, int xs, int r0,
+                                         int part, int lane, float& d0, float& d1) {
+  d0 = d1 = 0.f;
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    const int at = (part * T + j) * 16 + (lane & 3) * 4;
+    const uint32_t x0 = *reinterpret_cast<const uint32_t*>(x + r0 * xs + at);
+    const uint32_t x1 = *reinterpret_cast<const uint32_t*>(x + (r0 + 8) * xs + at);
+    d0 = fmaf(bf16_lo(x0), t[j][0], fmaf(bf16_hi(x0), t[j][1], d0));
+    d1 = fmaf(bf16_lo(x1), t[j][2], fmaf(bf16_hi(x1), t[j][3], d1));
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    d0 += __shfl_xor_sync(0xffffffffu, d0, o);
+    d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+  }
+}
+
+// The 64 gate threads: dg of the thread's token as a suffix sum over the chunk. so, sv:
+// the token's dy.y and dv.v; end: a part of <S_end, dS_end> per lane.
+__device__ __forceinline__ float suffix_sum(float so, float sv, float end, double* R, int gt) {
+  const int lane = gt & 31;
+  // in 64 bits: the terms cancel
+  double sum = (double)so - (double)sv, all = end;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double up = __shfl_down_sync(0xffffffffu, sum, o);
+    if (lane + o < 32) sum += up;
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (gt == 32) R[0] = sum;
+  asm volatile("bar.sync 1, 64;" ::: "memory");
+  if (gt < 32) sum += R[0];
+  return (float)(sum + all);
+}
+
+// The 64 gate threads: ddt of the thread's token from dg, and the chunk's parts of dA
+// and ddt_bias. `first`: the sequence's first token; `in`: a token of the sequence;
+// raw, A: its step before softplus, its head's A.
+__device__ __forceinline__ void write_gates(const DeltaChunkParams& p, double* R, float dg, int gt,
+                                            size_t gate_at, size_t bch, bool first, bool in, float raw,
+                                            float A) {
+  const DeltaParams& d = p.d;
+  // the first token's decay has nothing to act on without an initial state
+  if (!d.h0 && first) dg = 0.f;
+  double dA = 0.0, dbias = 0.0;
+  if (in) {
+    const float step = delta_step_size(raw, d.softplus);
+    const float sig = (d.softplus && raw <= kSoftplusCut) ? 1.f / (1.f + expf(-raw)) : 1.f;
+    const float ddt = dg * A * sig;
+    if (step * A < kStrongDecay) R[6] = 1.0;  // the chunk has work for strong_gates
+    dA = (double)dg * step;
+    dbias = ddt;
+    p.ddt[gate_at] = f32_to_bf16(ddt);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    dA += __shfl_xor_sync(0xffffffffu, dA, o);
+    dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+  }
+  if ((gt & 31) == 0) {
+    R[2 + 2 * (gt >> 5)] = dA;
+    R[2 + 2 * (gt >> 5) + 1] = dbias;
+  }
+  asm volatile("bar.sync 1, 64;" ::: "memory");
+  if (gt < 2) p.ws_part[bch * 2 + gt] = R[2 + gt] + R[4 + gt];
+}
+
+// Whether head h has a strong decay in the chunk.
+__device__ __forceinline__ bool strong_head(const DeltaChunkParams& p, size_t bch) {
+  const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri);
+  return sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
+}
+
+// The gates of a head with a strong decay in the chunk, over what write_gates left: dg of
+// the tokens behind one from the pairs on either side. All threads of the CTA, k and q in
+// place; its own function at the kernel's end, so that neither its registers nor its
+// instructions meet the others' products (inside the loop over the heads: 138 us in
+// place of 131 for the kernel where no decay is strong).
+template <int N>
+__device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned char* smem, int h) {
+  constexpr int LPR = N / 8;
+  const DeltaParams& d = p.d;
+  const int P = d.headdim, sl = P / 16;
+  const GradLayout g = grad_layout(N, P);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int mi = warp & 3, part = warp >> 2;
+  const int c = blockIdx.x, b = blockIdx.z;
+  const int64_t t0 = (int64_t)c * kC;
+  const int valid = (int)min((int64_t)kC, d.seqlen - t0);
+  const size_t bch = ((size_t)b * p.nchunks + c) * d.nheads + h, row0 = (size_t)b * d.seqlen + t0;
+  float* F = reinterpret_cast<float*>(smem + g.f);
+  const uint32_t sm = smem_u32(smem);
+  const int a_row = lane & 15, a_u = lane >> 4;
+  const int nt_row = (lane & 7) + ((lane & 16) >> 1), nt_u = (lane >> 3) & 1;
+  const int r0 = mi * 16 + (lane >> 2), r1 = r0 + 8;
+  const int gt = tid - kGateWarp * 32;
+  const bool gate = gt >= 0 && gt < kC;
+  const size_t gate_at = (row0 + gt) * d.nheads + h;
+  float* const red = F + kfSum * kC;
+  const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri);
+  if (tid < 5 * kC) {
+    const int w = tid / kC, i = tid % kC;
+    const int from = w == 0 ? kScGhi : (w == 1 ? kScGlo : (w == 2 ? kScBeta : (w == 3 ? kScKn : kScQn)));
+    F[w * kC + i] = sc[from * kC + i];
+  }
+  for (int i = tid; i < kC * (P / 8); i += kThreads) {
+    const int row = i / (P / 8), u = i % (P / 8);
+    const size_t from = ((row0 + (row < valid ? row : 0)) * d.nheads + h) * P + u * 8;
+    const uint32_t to = sm + row * g.ps + u * 16;
+    copy16(to + g.dy, p.dy + from, row < valid);
+    copy16(to + g.r, p.ws_r + from, row < valid);
+    copy16(to + g.dr, p.dv + from, row < valid);
+    copy16(to + g.w1, p.ws_rlo + from, row < valid);
+    copy16(to + g.w1 + kC * g.ps, p.ws_dvlo + from, row < valid);
+  }
+  for (int j = tid; j < P * LPR; j += kThreads) {
+    const uint32_t to = sm + (j / LPR) * g.xs + (j % LPR) * 16;
+    copy16(to + g.s, p.ws_state16 + bch * ((size_t)P * N) + (size_t)j * 8, true);
+    copy16(to + g.ds, p.ws_dstate16 + bch * ((size_t)P * N) + (size_t)j * 8, true);
+  }
+  cp_async_commit_group();
+  // a gate thread's operands meanwhile: its token's row products, <S_end, dS_end> and
+  // <S, dS> before the chunk, which is the first token's dg
+  float so = 0.f, sv = 0.f, out = 0.f, end = 0.f, before = 0.f, raw = 0.f, A = 0.f;
+  if (gate) {
+    A = d.A[h];
+    if (gt < valid)
+      raw = bf16_to_f32(static_cast<const uint16_t*>(d.dt)[gate_at]) + (d.dt_bias ? d.dt_bias[h] : 0.f);
+    for (int i = 0; i < sl; ++i) {
+      const size_t at = (bch * sl + i) * kC + gt;
+      so += p.ws_doto[at];
+      sv += p.ws_dotv[at];
+      out += p.ws_doth[at];
+    }
+    const float* prev = c > 0 ? p.ws_end + (bch - d.nheads) * 2 * sl
+                              : p.ws_first + ((size_t)b * d.nheads + h) * 2 * sl;
+    if (lane < 2 * sl) {
+      end = p.ws_end[bch * 2 * sl + lane];
+      if (c > 0 || d.h0) before = prev[lane];
+    }
+  }
+  cp_async_wait_group<0>();
+  __syncthreads();
+  {  // e^G (dy . S q - dv . S k), a quarter of dstate
+    constexpr int T = N / 32;
+    const int tr_row = (lane & 7) + (lane & 8), tr_u = lane >> 4;
+    float t[T][4] = {}, x[T][4] = {};
+    for (int kt = 0; kt < P / 16; ++kt) {
+      uint32_t a[4], e[4];
+      ldsm4(a, sm + g.dy + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+      ldsm4(e, sm + g.dr + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+#pragma unroll
+      for (int j = 0; j < T / 2; ++j) {
+        uint32_t bb[4];
+        ldsm4t(bb, sm + g.s + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
+        mma_bf16(t[2 * j], a, bb[0], bb[1]);
+        mma_bf16(t[2 * j + 1], a, bb[2], bb[3]);
+        mma_bf16(x[2 * j], e, bb[0], bb[1]);
+        mma_bf16(x[2 * j + 1], e, bb[2], bb[3]);
+      }
+    }
+    float i0, i1, v0, v1;
+    rows_dot<T>(t, smem + g.q, g.xs, r0, part, lane, i0, i1);
+    rows_dot<T>(x, smem + g.k, g.xs, r0, part, lane, v0, v1);
+    if ((lane & 3) == 0) {
+      F[(kfIn + part) * kC + r0] = ex2_approx(F[kfGhi * kC + r0] + F[kfGlo * kC + r0]) *
+                                   (F[kfQn * kC + r0] * i0 - F[kfKn * kC + r0] * v0);
+      F[(kfIn + part) * kC + r1] = ex2_approx(F[kfGhi * kC + r1] + F[kfGlo * kC + r1]) *
+                                   (F[kfQn * kC + r1] * i1 - F[kfKn * kC + r1] * v1);
+    }
+  }
+  {  // <S, dS>
+    float s = 0.f;
+    for (int j = tid; j < P * LPR; j += kThreads) {
+      const int at = (j / LPR) * g.xs + (j % LPR) * 16;
+      const uint4 a = *reinterpret_cast<const uint4*>(smem + g.s + at);
+      const uint4 b = *reinterpret_cast<const uint4*>(smem + g.ds + at);
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s = fmaf(bf16_lo(x[i]), bf16_lo(y[i]), fmaf(bf16_hi(x[i]), bf16_hi(y[i]), s));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[warp] = s;
+  }
+  if (part <= mi) {
+    float wv[2][4] = {}, xv[2][4] = {}, qk[2][4] = {}, kk[2][4] = {};
+    const uint32_t a_at = (mi * 16 + a_row) * g.ps + a_u * 16, b_at = (16 * part + nt_row) * g.ps + nt_u * 16;
+    for (int kt = 0; kt < P / 16; ++kt) {
+      uint32_t a[4], e[4], el[4], b[4], bl[4];
+      ldsm4(a, sm + g.dy + a_at + kt * 32);
+      ldsm4(e, sm + g.dr + a_at + kt * 32);
+      ldsm4(el, sm + g.w1 + kC * g.ps + a_at + kt * 32);
+      ldsm4(b, sm + g.r + b_at + kt * 32);
+      ldsm4(bl, sm + g.w1 + b_at + kt * 32);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        mma_bf16(wv[y], a, bl[2 * y], bl[2 * y + 1]);
+        mma_bf16(wv[y], a, b[2 * y], b[2 * y + 1]);
+        mma_bf16(xv[y], el, b[2 * y], b[2 * y + 1]);
+        mma_bf16(xv[y], e, bl[2 * y], bl[2 * y + 1]);
+        mma_bf16(xv[y], e, b[2 * y], b[2 * y + 1]);
+      }
+    }
+#pragma unroll
+    for (int kt = 0; kt < N / 16; ++kt) {
+      uint32_t a[4], e[4], b[4];
+      ldsm4(a, sm + g.q + (mi * 16 + a_row) * g.xs + (2 * kt + a_u) * 16);
+      ldsm4(e, sm + g.k + (mi * 16 + a_row) * g.xs + (2 * kt + a_u) * 16);
+      ldsm4(b, sm + g.k + (16 * part + nt_row) * g.xs + (2 * kt + nt_u) * 16);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        mma_bf16(qk[y], a, b[2 * y], b[2 * y + 1]);
+        mma_bf16(kk[y], e, b[2 * y], b[2 * y + 1]);
+      }
+    }
+    const int l4 = lane & 3;
+    float f[2][2][2];  // [column half y][row r0, r1][column]
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int i = x ? r1 : r0, j = 16 * part + 8 * y + 2 * l4 + q;
+          const float gm = ex2_approx((F[kfGhi * kC + i] - F[kfGhi * kC + j]) +
+                                      (F[kfGlo * kC + i] - F[kfGlo * kC + j]));
+          const float w = F[kfQn * kC + i] * qk[y][2 * x + q] * wv[y][2 * x + q] -
+                          F[kfKn * kC + i] * kk[y][2 * x + q] * xv[y][2 * x + q];
+          f[y][x][q] = j < i ? gm * F[kfBeta * kC + j] * F[kfKn * kC + j] * w : 0.f;
+        }
+    if (part < mi) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float s = (f[0][x][0] + f[0][x][1]) + (f[1][x][0] + f[1][x][1]);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (l4 == 0) F[(kfRows + part) * kC + (x ? r1 : r0)] = s;
+      }
+    }
+    // the block's own tokens: what a row has before each column
+    float c[2][2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float before = 0.f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float s = f[y][x][0] + f[y][x][1];
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          const float up = __shfl_up_sync(0xffffffffu, s, o, 4);
+          if (l4 >= o) s += up;
+        }
+        const float up = __shfl_up_sync(0xffffffffu, s, 1, 4);
+        c[y][x][0] = l4 ? before + up : before;
+        c[y][x][1] = c[y][x][0] + f[y][x][0];
+        before += __shfl_sync(0xffffffffu, s, 3, 4);
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int j = 16 * part + 8 * y + 2 * l4 + q;
+        float s = part < mi ? f[y][0][q] + f[y][1][q]
+                            : (r0 >= j ? c[y][0][q] : 0.f) + (r1 >= j ? c[y][1][q] : 0.f);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane < 4) F[(part < mi ? kfCols + mi : kfOwn) * kC + j] = s;
+      }
+  }
+  __syncthreads();
+  if (gate) {
+    // sums over rows from the token on and over columns before it, in its block of 16
+    // and, of the parts with the states, in the chunk; totals of whole blocks
+    const int K = gt >> 4, l16 = gt & 15;
+    float* const tot = red + kThreads / 32;  // [2 K + J]: rows of block K by column block J; in, out
+    float rs = 0.f, cs = 0.f, in = 0.f;
+#pragma unroll
+    for (int J = 0; J < 3; ++J) {
+      float r = J < K ? F[(kfRows + J) * kC + gt] : 0.f;
+      rs += r;
+      if (J < 2) {
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        if (l16 == 0) tot[2 * K + J] = r;
+      }
+    }
+#pragma unroll
+    for (int I = 1; I < 4; ++I) cs += I > K ? F[(kfCols + I) * kC + gt] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in += F[(kfIn + i) * kC + gt];
+    out *= F[kfBeta * kC + gt];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float up = __shfl_up_sync(0xffffffffu, out, o), down = __shfl_down_sync(0xffffffffu, in, o);
+      if (lane >= o) out += up;
+      if (lane + o < 32) in += down;
+      if (o < 16) {
+        const float u = __shfl_up_sync(0xffffffffu, cs, o, 16), w = __shfl_down_sync(0xffffffffu, rs, o, 16);
+        if (l16 >= o) cs += u;
+        if (l16 + o < 16) rs += w;
+      }
+    }
+    if (gt == 31) tot[9] = out;
+    if (gt == 32) tot[8] = in;
+    out = __shfl_up_sync(0xffffffffu, out, 1);  // the tokens before this one
+    cs = __shfl_up_sync(0xffffffffu, cs, 1);
+    if (lane == 0) out = 0.f;
+    if (l16 == 0) cs = 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    double* R = reinterpret_cast<double*>(F + kfRow * kC);
+    float dg = suffix_sum(so, sv, end, R, gt);
+    if (gt < valid && delta_step_size(raw, d.softplus) * A < kStrongDecay) {
+      float s = (F[kfOwn * kC + gt] + rs) + (cs + (in + out));
+      if (K == 1) s += tot[4] + tot[6];  // rows of blocks behind, columns of blocks before
+      if (K == 2) s += tot[6] + tot[7];
+      s += K < 2 ? tot[8] : tot[9];
+      float ss = 0.f;
+      for (int i = 0; i < kThreads / 32; ++i) ss += red[i];
+      dg = gt == 0 ? before : s + sc[kScEnd * kC] * ss;
+    }
+    write_gates(p, R, dg, gt, gate_at, bch, t0 + gt == 0, gt < valid, raw, A);
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_constant__ DeltaChunkParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -97,6 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   const int r0 = mi * 16 + (lane >> 2), r1 = r0 + 8;
   chain_go();
   chain_wait();
+
+  if (tid == 0) reinterpret_cast<double*>(F + kfRow * kC)[6] = 0.0;
 
   // ---- raw k and q
   constexpr int LPR = N / 8;
@@ -197,38 +546,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     // ---- the gates, one token per thread of two warps that have no weights below
     if (gate) {
       const float* dots = reinterpret_cast<const float*>(smem + g.dots) + gt;
+      double* R = reinterpret_cast<double*>(F + kfRow * kC);
       float so = 0.f, sv = 0.f;
       for (int i = 0; i < sl; ++i) {
         so += dots[(sl + i) * kC];
         sv += dots[(2 * sl + i) * kC];
       }
-      // suffix sums over the chunk's 64 tokens, in 64 bits: their terms cancel
-      double sum = (double)so - (double)sv, all = end;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += up;
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-      }
-      double* R = reinterpret_cast<double*>(F + kfRow * kC);
-      if (gt == 32) R[0] = sum;
-      asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (gt < 32) sum += R[0];
-      float dg = (float)(sum + all);
-      // the first token's decay has nothing to act on without an initial state
-      if (!d.h0 && t0 + gt == 0) dg = 0.f;
-      double dA = 0.0, dbias = 0.0;
+      const float dg = suffix_sum(so, sv, end, R, gt);
       if (gt < valid) {
-        const float raw = bf16_to_f32(dt_raw) + bias_h;
-        const float step = delta_step_size(raw, d.softplus);
-        // dg = a <S_before, dS'>: after a decay below e^-20 it is less than the
-        // rounding of the sum above (2^-22 of its terms), so it is taken as 0
-        if (step * A_h < -20.f) dg = 0.f;
-        const float sig = (d.softplus && raw <= kSoftplusCut) ? 1.f / (1.f + expf(-raw)) : 1.f;
-        const float ddt = dg * A_h * sig;
-        dA = (double)dg * step;
-        dbias = ddt;
-        p.ddt[gate_at] = f32_to_bf16(ddt);
         float db = 0.f;
         for (int i = 0; i < sl; ++i) db += dots[i * kC];
         db /= delta_beta_floor(F[kfBeta * kC + gt]);
@@ -238,17 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         }
         p.dbeta[gate_at] = f32_to_bf16(db);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        dA += __shfl_xor_sync(0xffffffffu, dA, o);
-        dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
-      }
-      if (lane == 0) {
-        R[2 + 2 * (gt >> 5)] = dA;
-        R[2 + 2 * (gt >> 5) + 1] = dbias;
-      }
-      asm volatile("bar.sync 1, 64;" ::: "memory");
-      if (gt < 2) p.ws_part[bch * 2 + gt] = R[2 + gt] + R[4 + gt];
+      write_gates(p, R, dg, gt, gate_at, bch, t0 + gt == 0, gt < valid, bf16_to_f32(dt_raw) + bias_h, A_h);
     }
 
     // ---- dy r^T and dv r^T -> W, N + N^T: rows of block mi, columns of block `part`
@@ -393,22 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const unsigned char* x = smem + (w ? g.q : g.k);
-    float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-      const int at = (part * T + j) * 16 + (lane & 3) * 4;
-      const uint32_t x0 = *reinterpret_cast<const uint32_t*>(x + r0 * g.xs + at);
-      const uint32_t x1 = *reinterpret_cast<const uint32_t*>(x + r1 * g.xs + at);
-      const float(&t)[4] = w ? tq[j] : tk[j];
-      d0 = fmaf(bf16_lo(x0), t[0], fmaf(bf16_hi(x0), t[1], d0));
-      d1 = fmaf(bf16_lo(x1), t[2], fmaf(bf16_hi(x1), t[3], d1));
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      d0 += __shfl_xor_sync(0xffffffffu, d0, o);
-      d1 += __shfl_xor_sync(0xffffffffu, d1, o);
-    }
+    float d0, d1;
+    rows_dot<T>(w ? tq : tk, smem + (w ? g.q : g.k), g.xs, r0, part, lane, d0, d1);
     if ((lane & 3) == 0) {  // over the weights' tiles, which are free
       float* D = reinterpret_cast<float*>(smem + g.w1) + (4 * w + part) * kC;
       D[r0] = d0;
@@ -440,6 +741,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
             pack_bf16x2(n1 * (t[2] - bf16_lo(x1) * e1), n1 * (t[3] - bf16_hi(x1) * e1));
     }
   }
+
+  // ---- the heads with strong decays
+  double* const R = reinterpret_cast<double*>(F + kfRow * kC);
+  if (R[6] == 0.0) return;
+  __syncthreads();
+  for (int hx = 0; hx < rep; ++hx)
+    if (strong_head(p, bc * d.nheads + kh * rep + hx)) {
+      strong_gates<N>(p, smem, kh * rep + hx);
+      __syncthreads();
+    }
 }
 
 // dA, ddt_bias: the chunks' sums of one head, in a fixed order.

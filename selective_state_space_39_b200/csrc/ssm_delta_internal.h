@@ -54,7 +54,8 @@ enum DeltaScal {       // arrays of 64 floats in a head block; the forward pass 
   kScK = 3,            // kmul: k = kmul k16
   kScSq = 4,           // e^G qmul: S q16 -> y
   kScP = 5,            // qmul 2^-p: (P16 u) -> y
-  kScEnd = 6,          // [0]: e^G_end; [1], [2]: the largest e^(G_end - G) of either half, at least 1
+  kScEnd = 6,          // [0]: e^G_end; [1], [2]: the largest e^(G_end - G) of either half, at least 1;
+                       // [3], [4]: 1 where a half has a log decay below kStrongDecay
   kScT = 7,            // 2^-t: (T16 R) -> r
   kScBeta = 8,
   kScGhi = 9,          // the running log decay, high and low part
@@ -68,6 +69,13 @@ enum DeltaScal {       // arrays of 64 floats in a head block; the forward pass 
 // meet a beta of at least 2^-26 (r is then off by less than its own rounding), and dv
 // is scaled back afterwards.
 constexpr float kBetaFloor = 1.f / 67108864.f;
+// From here on a decay's gradient, about e^g of the terms that suffix sums make it
+// of (2^-24 each), comes from the pairs of tokens on either side (ssm_delta_grad.cu).
+// Suffix sums leave a head's dA off by 5e-4 at e^-5, 4e-3 at e^-8 and all of it at
+// e^-16, the pairs 1e-6 at any decay (and 3e-3 of a single token where a state given
+// or asked for meets it). A head and chunk with such a decay takes about 11 us more of
+// an SM: from e^-4 on, ordinary layers would pay 15 us of 450 for a few of them.
+constexpr float kStrongDecay = -5.f;
 // A lower triangular 64 x 64 fp16 tile: its ten 16 x 16 blocks (i, j <= i),
 // column of blocks by column, 512 bytes each, as 2 x 2 core matrices of eight
 // rows of 16 bytes (the tensor cores' layout without a swizzle; any eight rows
@@ -102,9 +110,13 @@ struct DeltaChunkParams {
   uint16_t* ws_state16;  // (..., headdim, dstate): before each chunk, bf16
   uint16_t* ws_dstate16; // ... its adjoint after each chunk, bf16
   float* ws_end;         // (batch, nchunks, nheads, headdim/16, 2): <state, adjoint> after each chunk
+  float* ws_first;       // (batch, nheads, headdim/16, 2): ... before the first, with an initial state
   uint16_t* ws_r;        // (batch, seqlen, nheads, headdim): v minus the state's prediction
+  uint16_t* ws_rlo;      // what r's rounding leaves, in chunks with a strong decay (either half)
+  uint16_t* ws_dvlo;     // ... dv's
   float* ws_doto;        // (batch, nchunks, nheads, headdim/16, 64): dy.y over 16 rows
   float* ws_dotv;        //   ... dv.v
+  float* ws_doth;        //   ... e^(G_end - G) r . dS k, in chunks with a strong decay
   float* ws_dotb;        //   ... dv.r, before dv is scaled back to the token's own beta
   double* ws_part;       // (batch, nchunks, nheads, 2): partial dA, ddt_bias
   uint16_t *dq, *dk, *dv, *ddt, *dbeta;

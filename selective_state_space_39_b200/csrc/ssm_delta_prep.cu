@@ -238,12 +238,14 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       const int xg = x + (warp >> 1), i = tid & 63;
       double g = 0.0;
       float beta = 0.f;
+      bool strong = false;
       if (xg < nh && i < valid) {
         const int h = kh * rep + sub * heads + xg;
         const size_t at = ((size_t)b * d_.seqlen + t0 + i) * d_.nheads + h;
         const float raw = bf16_to_f32(static_cast<const uint16_t*>(d_.dt)[at]) +
                           (d_.dt_bias ? d_.dt_bias[h] : 0.f);
         float gf = delta_step_size(raw, d_.softplus) * d_.A[h];
+        strong = gf < kStrongDecay;
         gf = gf < kMinLogDecay ? kMinLogDecay : gf;
         g = (double)gf * 1.4426950408889634;  // log2 units
         beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d_.beta)[at]), d_.beta_sigmoid);
@@ -259,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       float* sc = scal + (warp >> 1) * (kDeltaScalBwd / 4);
       const float hi = (float)g;
       if (BWD) {
+        strong = __any_sync(0xffffffffu, strong);
+        if (xg < nh && lane == 0) sc[kScEnd * kC + 3 + (warp & 1)] = strong ? 1.f : 0.f;
         const float use = delta_beta_floor(beta);
         if (xg < nh) sc[kScRatio * kC + i] = use == beta ? 1.f : beta / use;
         beta = use;

@@ -139,6 +139,19 @@ __device__ __forceinline__ void store_rows(uint32_t tile, int t0, uint16_t* out,
   }
 }
 
+// What rounding to bf16 leaves of the values.
+template <int T>
+__device__ __forceinline__ void rest_of(float (&x)[T][4]) {
+#pragma unroll
+  for (int j = 0; j < T; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      const uint32_t r = pack_bf16x2(x[j][q], x[j][q + 1]);
+      x[j][q] -= bf16_lo(r);
+      x[j][q + 1] -= bf16_hi(r);
+    }
+}
+
 // Asynchronous copy of tokens t0 .. t0 + 8 T - 1 of 16 columns into a column
 // tile; tokens from `valid` on become zero. src: the chunk's first token.
 template <int T>

@@ -458,6 +458,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (BWD) {  // r leaves by the rows of v
           scale_cols(x, sc + kScT * kC + tk, lane);
           stage_rows(x, vrow, tk, lc);
+          if (sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f) {  // and its rest, by the state's rows
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) u[j][q] = x[j][q];
+            rest_of(u);
+            __syncwarp();
+            stage_rows(u, out16 - tk * 32, tk, lc);
+            store_rows<TT>(out16 - tk * 32, tk, p.ws_rlo + col_at0 + t0 * vs, vs, valid, lane);
+          }
         }
         scale_cols(x, sc + (BWD ? kScBeta : kScU) * kC + tk, lane);
 #pragma unroll
@@ -707,7 +717,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         wrote(&bars[kPutS]);
         return true;
       };
-      bool ok = put_state(true);
+      bool ok = put_state(true), strong = false;  // a strong decay in the chunk
       int st = 0;
       uint32_t fpar = 0;
       for (int s = 0; ok && s < p.nchunks; ++s) {
@@ -732,12 +742,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         RowScale r0 = row_scale(exponent_of(m0)), r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
         wrote(&bars[kPutP]);
+        strong = sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
+        if (strong) {
+          fetch_rows<TT>(out16 - tk * 32, p.ws_rlo + col_at0 + t0 * vs, vs, tk, valid, lane);
+          cp_async_commit_group();
+        }
 
         // ---- dU = P^T dY + e^(G_end - G) K dS^T
         ok = wait_warp(&bars[kBarK], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmX + tcol, x);
         scale_rows(x, inv0, inv1);
         scale_cols(x, sc + kScKend * kC + tk, lane);
+        if (strong) {
+#pragma unroll
+          for (int j = 0; j < TT; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[j][q] = x[j][q];
+        }
         ok = wait_warp(&bars[kBarQ], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmU + hcol, u);
         scale_rows(u, r0.inv, r1.inv);
@@ -758,6 +779,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- meanwhile: the next chunk's rows, dS for the gradients, <S, dS>
         const float dot = tiles_dot<NS>(S, after, lane);
         if (lane == 0) p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
+        if (strong) {  // r . e^(G_end - G) dS k
+          cp_async_wait_group<0>();
+          __syncwarp();
+          load_rows(x, vrow + 2 * kCol, tk, lc);
+          load_rows(u, out16 - tk * 32, tk, lc);
+          add_tiles(x, u);
+          row_dots(x, y, p.ws_doth + dot_at, lane);
+        }
         __syncwarp();
         if (c > 0) fetch(c - 1);
         store_state16<N, NS>(S, out16, p.ws_dstate16 + st_at, lane);
@@ -792,6 +821,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         stage_rows(x, vrow, tk, lc);
         store_rows<TT>(vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane);
+        if (strong) {
+          rest_of(x);
+          __syncwarp();
+          stage_rows(x, vrow, tk, lc);
+          store_rows<TT>(vrow, tk, p.ws_dvlo + col_at0 + t0 * vs, vs, valid, lane);
+        }
         // ---- dS <- e^G_end dS + dY^T (e^G Q) - dR^T (e^G K), and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
         ok = wait_warp(&bars[kBarU], par, ok ? p.wait_limit_ns : 0) && ok;
@@ -823,6 +858,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) atomicExch(&g_delta_timeout, 1);
       } else if (p.dh0) {
         store_state<N, NS>(S, p.dh0 + state_at, lane);
+      }
+      if (ok && d.h0 && strong) {  // <S, dS> before the first token
+        float s[NS / 8][4], dot = 0.f;
+        load_state<N, NS>(s, d.h0 + state_at, lane);
+#pragma unroll
+        for (int j = 0; j < NS / 8; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dot = fmaf(s[j][q], S[j][q], dot);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) p.ws_first[(((size_t)t.b * d.nheads + h) * pb + pw / 16) * 2 + hf] = dot;
       }
     }
   }

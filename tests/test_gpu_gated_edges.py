@@ -12,6 +12,56 @@ from tests.test_gpu_gated_delta import BF, F32Y, G, S32, Y, bwd, check_fwd, cu, 
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------ the gates' gradients -------
+# Per head, of the root of the sum of squares of the tokens' parts. A decay's
+# gradient is about e^g of the row products that suffix sums take it from
+# (fp32, 64 terms: 8 * 2^-24 of a term, e^5 * 10 times that of the value), or a
+# sum over pairs of two bf16 pieces each (2^-16): below 1e-3. With a state
+# before or after the call, one token per sequence end meets it as bf16 (two
+# roundings of 2^-9, the token up to all of the sum): 4e-3.
+@pytest.mark.parametrize("states", [False, True], ids=["bare", "states"])
+@pytest.mark.parametrize("L", [64, 130, 300])
+@pytest.mark.parametrize("logs", [(0.5, 2.0, 3.0, 4.0), (4.4, 5.7, 8.0, 10.0), (12.0, 16.0, 19.0, 24.0)],
+                         ids=str)
+def test_gates_of_heads_that_decay_at_every_token(logs, L, states):
+    d = R.make_delta(1, L, 4, 2, 64, 128, BF, 91, h0=states)
+    d["A"] = -torch.tensor(logs)
+    steps = torch.tensor([0.875, 1.0, 1.125]).repeat(L)[:L]
+    d["dt"] = steps.to(BF).reshape(1, L, 1).repeat(1, 1, 4)
+    d["dt_bias"] = None
+    g = bwd(d, softplus=False)
+    ref = R.delta_grads(d, softplus=False)
+    for h in range(4):
+        near(g["ddt"][:, :, h], ref["ddt"][:, :, h], G, f"ddt e^-{logs[h]}")
+        part = ref["ddt"][0, :, h] / d["A"][h].double()  # each token's part of dA / step
+        scale = (part * steps.double()).norm().item()
+        off = abs(g["dA"][h].item() - ref["dA"][h].item()) / scale
+        print(f"dA e^-{logs[h]}: {off:.2e}")
+        assert off <= (4e-3 if states else 1e-3), (logs[h], off)
+
+
+@pytest.mark.parametrize("P,N,H,Hk", [(16, 64, 2, 1), (128, 64, 2, 2), (80, 128, 3, 1), (128, 128, 2, 1)])
+def test_gates_of_single_strong_decays(P, N, H, Hk):
+    """A few tokens with decays of e^-4.5 .. e^-40 among weak ones, at every place
+    of a chunk and of its blocks of 16: each token's gradient for itself, of the
+    products (of a value with two bf16 roundings, G) that make it."""
+    L = 200
+    d = R.make_delta(2, L, H, Hk, P, N, BF, 92)
+    d["A"] = -torch.ones(H)
+    d["dt"] = torch.full((2, L, H), 0.0625, dtype=BF)
+    at = [0, 1, 15, 16, 17, 31, 40, 63, 64, 65, 100, 127, 128, 150, 191, 192, 199]
+    for i, t in enumerate(at):
+        d["dt"][:, t] = (4.5, 7.0, 11.0, 16.0, 22.0, 40.0)[i % 6]
+    d["dt_bias"] = None
+    g = bwd(d, softplus=False)
+    ref = R.delta_grads(d, softplus=False)
+    got, want = g["ddt"].double().cpu(), ref["ddt"]
+    for i in range(6):  # the tokens of one strength together
+        near(got[:, at[i::6]], want[:, at[i::6]], (2 * G[0], 2 * G[1]), f"strength {i}")
+    weak = [t for t in range(L) if t not in at]
+    near(got[:, weak], want[:, weak], G, "weak")
+
+
 @pytest.mark.parametrize("raw", [None, 5.0, -12.0, -40.0])
 def test_beta_gradient_of_repeated_keys(raw):
     """Equal keys and hardly any decay: a token's write is undone by the next
