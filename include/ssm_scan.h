@@ -452,7 +452,11 @@ int ssm_ssd_state_update(int64_t batch, int64_t nheads, int64_t headdim, int64_t
  * chunk (64 tokens) on the tensor cores,
  * every product on the state's path in two fp16 pieces per fp32 operand, so
  * that h_last is as exact as fp32 arithmetic; other calls run token by token
- * in fp32. y may be NULL when h_last is given; h_last may be h0.
+ * in fp32. So do, inside a chunked call, 16 rows of a state through a chunk in
+ * which one of them meets a value that is not finite, or one 2^24 times that of
+ * two neighbouring tokens (2^32 times that of a single one), about 1 us a token:
+ * no value changes the results of the tokens before it, whatever its size. y
+ * may be NULL when h_last is given; h_last may be h0.
  * workspace: at least ssm_gated_delta_workspace_bytes(...) bytes of device
  * memory, 16-byte aligned (may be NULL when that is 0), used as scratch only;
  * not by two calls that can run at the same time. seqlen == 0 writes only

@@ -102,19 +102,27 @@ __device__ __forceinline__ RowScale row_scale(uint32_t e) {
   return r;
 }
 __device__ __forceinline__ uint32_t exponent_of(float m) { return __float_as_uint(m) >> 23; }
-// Largest magnitude of fragment rows g (m0) and g + 8 (m1), over the quad.
+// The larger one, or NaN where either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ bool not_finite(float m) { return (__float_as_uint(m) & 0x7FFFFFFFu) >= 0x7F800000u; }
+// Largest magnitude of fragment rows g (m0) and g + 8 (m1), over the quad; NaN where
+// one of them is.
 template <int T>
 __device__ __forceinline__ void row_max(const float (&x)[T][4], float& m0, float& m1) {
   m0 = m1 = 0.f;
 #pragma unroll
   for (int j = 0; j < T; ++j) {
-    m0 = fmaxf(m0, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
-    m1 = fmaxf(m1, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+    m0 = max_nan(m0, max_nan(fabsf(x[j][0]), fabsf(x[j][1])));
+    m1 = max_nan(m1, max_nan(fabsf(x[j][2]), fabsf(x[j][3])));
   }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    m0 = max_nan(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = max_nan(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
 }
 // The transpose of the warp's 8 x 8 matrix of 16-bit values.

@@ -159,14 +159,16 @@ __device__ __forceinline__ void write_gates(const DeltaChunkParams& p, double* R
   if (gt < 2) p.ws_part[bch * 2 + gt] = R[2 + gt] + R[4 + gt];
 }
 
-// Whether head h has a strong decay in the chunk.
+// Whether a head has a strong decay in the chunk, or rows that went token by token.
 __device__ __forceinline__ bool strong_head(const DeltaChunkParams& p, size_t bch) {
   const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri);
-  return sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
+  return sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] + sc[kScEnd * kC + 5] != 0.f;
 }
 
-// The gates of a head with a strong decay in the chunk, over what write_gates left: dg of
-// the tokens behind one from the pairs on either side. All threads of the CTA, k and q in
+// The gates of such a head, over what write_gates left: dg of the tokens behind a strong
+// decay, or of all where a value's size took the rows out of the pieces (the suffix sums
+// of the tokens before it would be lost in it; r and dv then are one bf16 piece), from the
+// pairs on either side. All threads of the CTA, k and q in
 // place; its own function at the kernel's end, so that neither its registers nor its
 // instructions meet the others' products (inside the loop over the heads: 138 us in
 // place of 131 for the kernel where no decay is strong).
@@ -192,6 +194,7 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
   const size_t gate_at = (row0 + gt) * d.nheads + h;
   float* const red = F + kfSum * kC;
   const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri);
+  const bool whole = sc[kScEnd * kC + 5] == 0.f;
   if (tid < 5 * kC) {
     const int w = tid / kC, i = tid % kC;
     const int from = w == 0 ? kScGhi : (w == 1 ? kScGlo : (w == 2 ? kScBeta : (w == 3 ? kScKn : kScQn)));
@@ -204,8 +207,8 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
     copy16(to + g.dy, p.dy + from, row < valid);
     copy16(to + g.r, p.ws_r + from, row < valid);
     copy16(to + g.dr, p.dv + from, row < valid);
-    copy16(to + g.w1, p.ws_rlo + from, row < valid);
-    copy16(to + g.w1 + kC * g.ps, p.ws_dvlo + from, row < valid);
+    copy16(to + g.w1, p.ws_rlo + from, row < valid && whole);
+    copy16(to + g.w1 + kC * g.ps, p.ws_dvlo + from, row < valid && whole);
   }
   for (int j = tid; j < P * LPR; j += kThreads) {
     const uint32_t to = sm + (j / LPR) * g.xs + (j % LPR) * 16;
@@ -407,7 +410,7 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     double* R = reinterpret_cast<double*>(F + kfRow * kC);
     float dg = suffix_sum(so, sv, end, R, gt);
-    if (gt < valid && delta_step_size(raw, d.softplus) * A < kStrongDecay) {
+    if (gt < valid && (!whole || delta_step_size(raw, d.softplus) * A < kStrongDecay)) {
       float s = (F[kfOwn * kC + gt] + rs) + (cs + (in + out));
       if (K == 1) s += tot[4] + tot[6];  // rows of blocks behind, columns of blocks before
       if (K == 2) s += tot[6] + tot[7];
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   const bool gate = gt >= 0 && gt < kC;
   const int sl = P / 16;  // at most 8
   uint16_t dt_raw = 0, beta_raw = 0;
-  float A_h = 0.f, bias_h = 0.f, end = 0.f;
+  float A_h = 0.f, bias_h = 0.f, end = 0.f, alone = 0.f;
   auto load = [&](int hx) {
     const int h = kh * rep + hx;
     const size_t bch = bc * d.nheads + h;
@@ -508,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
       end = lane < 2 * sl ? p.ws_end[bch * 2 * sl + lane] : 0.f;
       A_h = d.A[h];
       bias_h = d.dt_bias ? d.dt_bias[h] : 0.f;
+      alone = sc[kScEnd * kC + 5];
       if (gt < valid) {
         dt_raw = static_cast<const uint16_t*>(d.dt)[(row0 + gt) * d.nheads + h];
         beta_raw = static_cast<const uint16_t*>(d.beta)[(row0 + gt) * d.nheads + h];
@@ -553,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         sv += dots[(2 * sl + i) * kC];
       }
       const float dg = suffix_sum(so, sv, end, R, gt);
+      if (alone != 0.f) R[6] = 1.0;
       if (gt < valid) {
         float db = 0.f;
         for (int i = 0; i < sl; ++i) db += dots[i * kC];

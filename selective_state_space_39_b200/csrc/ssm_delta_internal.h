@@ -55,7 +55,8 @@ enum DeltaScal {       // arrays of 64 floats in a head block; the forward pass 
   kScSq = 4,           // e^G qmul: S q16 -> y
   kScP = 5,            // qmul 2^-p: (P16 u) -> y
   kScEnd = 6,          // [0]: e^G_end; [1], [2]: the largest e^(G_end - G) of either half, at least 1;
-                       // [3], [4]: 1 where a half has a log decay below kStrongDecay
+                       // [3], [4]: 1 where a half has a log decay below kStrongDecay;
+                       // [5]: 1 where rows went token by token (set by the walk)
   kScT = 7,            // 2^-t: (T16 R) -> r
   kScBeta = 8,
   kScGhi = 9,          // the running log decay, high and low part

@@ -262,7 +262,10 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       const float hi = (float)g;
       if (BWD) {
         strong = __any_sync(0xffffffffu, strong);
-        if (xg < nh && lane == 0) sc[kScEnd * kC + 3 + (warp & 1)] = strong ? 1.f : 0.f;
+        if (xg < nh && lane == 0) {
+          sc[kScEnd * kC + 3 + (warp & 1)] = strong ? 1.f : 0.f;
+          sc[kScEnd * kC + 5] = 0.f;
+        }
         const float use = delta_beta_floor(beta);
         if (xg < nh) sc[kScRatio * kC + i] = use == beta ? 1.f : beta / use;
         beta = use;

@@ -310,11 +310,164 @@ __device__ __forceinline__ void put_max(float m0, float m1, float* mine, int lan
   }
 }
 __device__ __forceinline__ void get_max(float& m0, float& m1, const float* other, int lane) {
-  m0 = fmaxf(m0, other[lane >> 2]);
-  m1 = fmaxf(m1, other[8 + (lane >> 2)]);
+  m0 = max_nan(m0, other[lane >> 2]);
+  m1 = max_nan(m1, other[8 + (lane >> 2)]);
 }
 
 constexpr int kRowWarps = 8, kTcThreads = kRowWarps * 32 + 128;
+
+// ---- rows that the pieces do not hold --------------------------------------
+// A row's pieces stand under one scale for the chunk's 64 tokens and hold 2^-40 of the
+// largest. A value that is not finite, or one so large that it leaves the others too few
+// bits, must not reach the tokens before it, nor those behind a decay that forgets it: the
+// 16 rows then take the chunk token by token in fp32, in the fragments they hold the
+// state in. (A row whose state has a NaN is NaN from there on either way.)
+//
+// Whether a row has values too small beside its largest m: neighbours both below 2^-24
+// of it (16 bits left), or a single one below 2^-32. Exact zeros need no bits.
+__device__ __forceinline__ bool too_small(float a, float b, float m) {
+  const float both = fmaxf(a, b), pair = m * 0x1p-24f, one = m * 0x1p-32f;
+  return (both < pair && both > 0.f) || (a < one && a > 0.f) || (b < one && b > 0.f);
+}
+// What a residual x = v - (its decayed prediction) stands for: it may well be small where
+// v is not, and where v is zero (a masked token) and the prediction decayed, it is the
+// state, of largest magnitude s.
+__device__ __forceinline__ float size_of(float x, float v, float s) {
+  return v != 0.f ? fmaxf(fabsf(x), fabsf(v)) : (x != 0.f ? s : 0.f);
+}
+template <int T>
+__device__ __forceinline__ bool wide_rows(const float (&x)[T][4], const float (&v)[T][4], float m0, float m1,
+                                          float s0, float s1) {
+  // by the residuals alone first, a third of the instructions: hardly a chunk has one
+  float both0 = m0, both1 = m1, one0 = m0, one1 = m1;
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    both0 = fminf(both0, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
+    both1 = fminf(both1, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+    one0 = fminf(one0, fminf(fabsf(x[j][0]), fabsf(x[j][1])));
+    one1 = fminf(one1, fminf(fabsf(x[j][2]), fabsf(x[j][3])));
+  }
+  bool wide = both0 < m0 * 0x1p-24f || both1 < m1 * 0x1p-24f || one0 < m0 * 0x1p-32f || one1 < m1 * 0x1p-32f;
+  if (!__any_sync(0xffffffffu, wide)) return false;
+  wide = false;
+#pragma unroll
+  for (int j = 0; j < T; ++j) {
+    wide |= too_small(size_of(x[j][0], v[j][0], s0), size_of(x[j][1], v[j][1], s0), m0);
+    wide |= too_small(size_of(x[j][2], v[j][2], s1), size_of(x[j][3], v[j][3], s1), m1);
+  }
+  return __any_sync(0xffffffffu, wide);
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+// The sums of both warps of a pair, six values a lane (mine, other: their places for 16
+// floats in three buffers, kRowWarps * 16 apart): two of rows g and g + 8, four of all.
+template <int SP>
+__device__ __forceinline__ void pair_sum(float (&r)[8], float* mine, const float* other, int id, int lane) {
+  if (SP == 1) return;
+  constexpr int kNext = kRowWarps * 16;
+  pair_sync(id);  // the buffers' last readers are done
+  if ((lane & 3) == 0) {
+    mine[lane >> 2] = r[0];
+    mine[8 + (lane >> 2)] = r[1];
+    mine[kNext + (lane >> 2)] = r[2];
+    mine[kNext + 8 + (lane >> 2)] = r[3];
+  }
+  if (lane < 4) mine[2 * kNext + lane] = lane == 0 ? r[4] : (lane == 1 ? r[5] : (lane == 2 ? r[6] : r[7]));
+  pair_sync(id);
+  r[0] += other[lane >> 2];
+  r[1] += other[8 + (lane >> 2)];
+  r[2] += other[kNext + (lane >> 2)];
+  r[3] += other[kNext + 8 + (lane >> 2)];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[4 + i] += other[2 * kNext + i];
+}
+
+// Rows g and g + 8 of 16 (pw: the first) and the warp's columns, through chunk c: y (BWD:
+// r and dy . y), and the state S [NS / 8][4] from before the chunk to after it. Both
+// warps of a pair.
+template <int N, int SP, bool BWD>
+__device__ __noinline__ void walk_tokens(const DeltaChunkParams& p, int b, int h, int pw, int c, int id,
+                                         float* mine, const float* other, float* state) {
+  constexpr int NS = N / SP;
+  const DeltaParams& d = p.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hf = SP == 2 ? (warp >> 2) & 1 : 0, kh = h / (d.nheads / d.nkheads);
+  const int64_t t0 = (int64_t)c * kC;
+  const int valid = (int)min((int64_t)kC, d.seqlen - t0);
+  const size_t bch = ((size_t)b * p.nchunks + c) * d.nheads + h;
+  const float A = d.A[h], bias = d.dt_bias ? d.dt_bias[h] : 0.f;
+  float s[NS / 8][4];
+#pragma unroll
+  for (int j = 0; j < NS / 8; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[j][q] = state[4 * j + q];
+  if (BWD && lane == 0)
+    reinterpret_cast<float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri)[kScEnd * kC + 5] = 1.f;
+#pragma unroll 1
+  for (int t = 0; t < valid; ++t) {
+    const size_t row = (size_t)b * d.seqlen + t0 + t;
+    const uint16_t* kr = static_cast<const uint16_t*>(d.k) + (row * d.nkheads + kh) * N + hf * NS + 2 * (lane & 3);
+    const uint16_t* qr = static_cast<const uint16_t*>(d.q) + (row * d.nkheads + kh) * N + hf * NS + 2 * (lane & 3);
+    float r[8] = {};  // S k, S q of both rows; k.k, q.q, k.q
+    uint32_t kv[NS / 8];
+#pragma unroll
+    for (int j = 0; j < NS / 8; ++j) {
+      kv[j] = *reinterpret_cast<const uint32_t*>(kr + 8 * j);
+      const uint32_t qv = *reinterpret_cast<const uint32_t*>(qr + 8 * j);
+      const float k0 = bf16_lo(kv[j]), k1 = bf16_hi(kv[j]), q0 = bf16_lo(qv), q1 = bf16_hi(qv);
+      r[0] = fmaf(s[j][0], k0, fmaf(s[j][1], k1, r[0]));
+      r[1] = fmaf(s[j][2], k0, fmaf(s[j][3], k1, r[1]));
+      r[2] = fmaf(s[j][0], q0, fmaf(s[j][1], q1, r[2]));
+      r[3] = fmaf(s[j][2], q0, fmaf(s[j][3], q1, r[3]));
+      r[4] = fmaf(k0, k0, fmaf(k1, k1, r[4]));
+      r[5] = fmaf(q0, q0, fmaf(q1, q1, r[5]));
+      r[6] = fmaf(k0, q0, fmaf(k1, q1, r[6]));
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i) r[i] = quad_sum(r[i]);
+    pair_sum<SP>(r, mine, other, id, lane);
+    const float kn = d.qk_norm ? rsqrtf(r[4] + kDeltaQkEps) : 1.f;
+    const float qn = (d.qk_norm ? rsqrtf(r[5] + kDeltaQkEps) : 1.f) * d.scale;
+    const float step = delta_step_size(bf16_to_f32(static_cast<const uint16_t*>(d.dt)[row * d.nheads + h]) + bias,
+                                       d.softplus);
+    const float a = expf(step * A);
+    const float beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d.beta)[row * d.nheads + h]),
+                                  d.beta_sigmoid);
+    const size_t at = (row * d.nheads + h) * d.headdim + pw + (lane >> 2);
+    const uint16_t* v = static_cast<const uint16_t*>(d.v) + at;
+    const float r0 = bf16_to_f32(v[0]) - a * kn * r[0], r1 = bf16_to_f32(v[8]) - a * kn * r[1];
+    const float w0 = beta * r0 * kn, w1 = beta * r1 * kn;
+    const float y0 = qn * fmaf(a, r[2], w0 * r[6]), y1 = qn * fmaf(a, r[3], w1 * r[6]);
+#pragma unroll
+    for (int j = 0; j < NS / 8; ++j) {
+      const float k0 = bf16_lo(kv[j]), k1 = bf16_hi(kv[j]);
+      s[j][0] = fmaf(w0, k0, a * s[j][0]);
+      s[j][1] = fmaf(w0, k1, a * s[j][1]);
+      s[j][2] = fmaf(w1, k0, a * s[j][2]);
+      s[j][3] = fmaf(w1, k1, a * s[j][3]);
+    }
+    if (BWD) {
+      float dot = fmaf(bf16_to_f32(p.dy[at]), y0, bf16_to_f32(p.dy[at + 8]) * y1);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (hf == 0 && lane == 0) p.ws_doto[(bch * (d.headdim / 16) + pw / 16) * kC + t] = dot;
+    }
+    uint16_t* out = BWD ? p.ws_r : static_cast<uint16_t*>(d.y);
+    if (hf == 0 && (lane & 3) == 0 && out) {
+      out[at] = f32_to_bf16(BWD ? r0 : y0);
+      out[at + 8] = f32_to_bf16(BWD ? r1 : y1);
+    }
+  }
+  if (BWD && hf == 0)
+    for (int t = valid + lane; t < kC; t += 32) p.ws_doto[(bch * (d.headdim / 16) + pw / 16) * kC + t] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NS / 8; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) state[4 * j + q] = s[j][q];
+  if (SP == 2) pair_sync(id);  // the buffers are free
+}
 
 // SP warps share a block of 16 rows (BWD: two).
 template <int N, int SP, bool BWD>
@@ -386,6 +539,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       fetch(0);
       float S[NS / 8][4], inv0 = 1.f, inv1 = 1.f;  // the state's rows, the inverse of its pieces' scale
+      float big0 = 0.f, big1 = 0.f;  // its largest magnitudes, NaN where it has one
       load_state<N, NS>(S, d.h0 ? d.h0 + state_at : nullptr, lane);
       auto meet = [&](float& m0, float& m1, int use) {
         if (SP == 1) return;
@@ -403,6 +557,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           get_max(m0, m1, ox, lane);
         }
         if (!ok) return false;
+        big0 = m0;
+        big1 = m1;
         const RowScale a = row_scale(exponent_of(m0)), b = row_scale(exponent_of(m1));
         inv0 = a.inv;
         inv1 = b.inv;
@@ -443,6 +599,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_pieces<true, TT>(x, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
         wrote(&bars[kPutR]);
 
+        // (the backward pass has no registers to keep R and V longer: 483 us for 456; the
+        // forward pass alone gains by it: 8192 tokens of 32 heads 393 us, not 397)
+        bool wide = BWD && wide_rows(x, u, m0, m1, big0, big1);
+
         // ---- meanwhile the next chunk's v, and the readout of the entering state
         if (c + 1 < p.nchunks) fetch(c + 1);
         ok = wait_warp(&bars[kBarQ], par, ok ? p.wait_limit_ns : 0) && ok;
@@ -452,6 +612,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (BWD) store_state16<N, NS>(S, out16, p.ws_state16 + st_at, lane);
 
         // ---- u = beta T R; K^T (e^(G_end - G) u)
+        if (!BWD) wide = wide_rows(x, u, m0, m1, big0, big1);
         ok = wait_warp(&bars[kBarT], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmU + hcol, x);
         scale_rows(x, r0.inv, r1.inv);
@@ -480,9 +641,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float most = fmaxf(sc[kScEnd * kC + 1], sc[kScEnd * kC + 2]);
         scale_cols(x, sc + kScK * kC + tk, lane);
         row_max(x, m0, m1);
-        m0 *= most;
-        m1 *= most;
+        m0 = wide ? __uint_as_float(0x7FFFFFFFu) : m0 * most;
+        m1 = wide ? m0 : m1 * most;
         meet(m0, m1, 2);
+        const bool alone = __any_sync(0xffffffffu, (not_finite(m0) && big0 == big0) || (not_finite(m1) && big1 == big1));
         r0 = row_scale(exponent_of(m0));
         r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(u, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
@@ -491,24 +653,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- P u
         tm_pieces<BWD, TT>(x, r0.s, r1.s, row + kTmS + tcol / 2, row + kTmS + 32 + tcol / 2);
         wrote(&bars[kPutP]);
-        if (BWD) store_rows<TT>(vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane);
+        if (BWD && !alone) store_rows<TT>(vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane);
 
         // ---- S <- e^G_end S + K^T u, and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
         ok = wait_warp(&bars[kBarU], par, ok ? p.wait_limit_ns : 0) && ok;
         constexpr int G = NS / 8 < 8 ? NS / 8 : 8;  // tiles per load
+        if (alone) {
+          float s[NS / 2];
 #pragma unroll
-        for (int i = 0; i < NS / 8; i += G) {
-          float ds[G][4];
-          tm_load(row + kTmU + hf * NS + 8 * i, ds);
+          for (int i = 0; i < NS / 2; ++i) s[i] = S[i / 4][i % 4];
+          walk_tokens<N, SP, BWD>(p, t.b, h, pw, c, 1 + (warp & 3), mx, ox, s);
 #pragma unroll
-          for (int j = 0; j < G; ++j) {
-            float(&s)[4] = S[i + j];
-            const float2 a = fma2(make_float2(s[0], s[1]), make_float2(end, end),
-                                  mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
-            const float2 b = fma2(make_float2(s[2], s[3]), make_float2(end, end),
-                                  mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
-            s[0] = a.x; s[1] = a.y; s[2] = b.x; s[3] = b.y;
+          for (int i = 0; i < NS / 2; ++i) S[i / 4][i % 4] = s[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < NS / 8; i += G) {
+            float ds[G][4];
+            tm_load(row + kTmU + hf * NS + 8 * i, ds);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              float(&s)[4] = S[i + j];
+              const float2 a = fma2(make_float2(s[0], s[1]), make_float2(end, end),
+                                    mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
+              const float2 b = fma2(make_float2(s[2], s[3]), make_float2(end, end),
+                                    mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
+              s[0] = a.x; s[1] = a.y; s[2] = b.x; s[3] = b.y;
+            }
           }
         }
         ok = wait_warp(&bars[kBarP], par, ok ? p.wait_limit_ns : 0) && ok;  // the columns of the pieces are free
@@ -519,16 +690,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (BWD) store_tiles<NS>(S, p.ws_state + (st_at - part) + (size_t)pw * N + hf * 16 * NS, lane);
 
         // ---- Y
-        tm_load(ycol, x);
-        scale_rows(x, w0.inv, w1.inv);
-        scale_cols(x, sc + kScP * kC + tk, lane);
-        add_tiles(y, x);
-        if (BWD) {
-          load_rows(x, vrow + kCol, tk, lc);
-          row_dots(x, y, p.ws_doto + (bch * pb + pw / 16) * kC + tk, lane);
-        } else if (d.y) {
-          stage_rows(y, vrow, tk, lc);
-          store_rows<TT>(vrow, tk, static_cast<uint16_t*>(d.y) + col_at0 + t0 * vs, vs, valid, lane);
+        if (!alone) {
+          tm_load(ycol, x);
+          scale_rows(x, w0.inv, w1.inv);
+          scale_cols(x, sc + kScP * kC + tk, lane);
+          add_tiles(y, x);
+          if (BWD) {
+            load_rows(x, vrow + kCol, tk, lc);
+            row_dots(x, y, p.ws_doto + (bch * pb + pw / 16) * kC + tk, lane);
+          } else if (d.y) {
+            stage_rows(y, vrow, tk, lc);
+            store_rows<TT>(vrow, tk, static_cast<uint16_t*>(d.y) + col_at0 + t0 * vs, vs, valid, lane);
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&freed[st]);
@@ -742,8 +915,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         RowScale r0 = row_scale(exponent_of(m0)), r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
         wrote(&bars[kPutP]);
-        strong = sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
-        if (strong) {
+        const bool whole = sc[kScEnd * kC + 5] == 0.f;  // r has a rest in every row
+        strong = !whole || sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
+        if (strong && whole) {
           fetch_rows<TT>(out16 - tk * 32, p.ws_rlo + col_at0 + t0 * vs, vs, tk, valid, lane);
           cp_async_commit_group();
         }
@@ -783,8 +957,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           cp_async_wait_group<0>();
           __syncwarp();
           load_rows(x, vrow + 2 * kCol, tk, lc);
-          load_rows(u, out16 - tk * 32, tk, lc);
-          add_tiles(x, u);
+          if (whole) {
+            load_rows(u, out16 - tk * 32, tk, lc);
+            add_tiles(x, u);
+          }
           row_dots(x, y, p.ws_doth + dot_at, lane);
         }
         __syncwarp();

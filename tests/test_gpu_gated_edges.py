@@ -90,3 +90,124 @@ def test_beta_gradient_beside_tokens_that_write_nothing():
         near(g["dbeta"][:, i::5], ref["dbeta"][:, i::5], G, f"dbeta {i}")
         near(g["dv"][:, i::5], ref["dv"][:, i::5], G, f"dv {i}")
     assert not g["dv"][:, 0::5].any()
+
+
+# ------------------------------------------ values far above the others ------
+SHAPES = [(1, 130, 4, 2, 64, 128), (5, 70, 32, 16, 64, 64), (1, 130, 2, 1, 48, 64)]
+
+
+def refer(d, **kw):
+    return R.delta(**{k: d[k] for k in ("q", "k", "v", "dt", "A", "beta", "dt_bias", "h0")}, **kw)
+
+
+def near_where_finite(got, ref, tol, what):
+    """Finite exactly where the reference is, and near it there."""
+    ok = torch.isfinite(ref)
+    assert torch.equal(torch.isfinite(got.float().cpu()), ok), what
+    near(got.cpu()[ok], ref[ok], tol, what)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")], ids=str)
+def test_an_infinite_value_reaches_only_later_tokens(shape, value):
+    d = R.make_delta(*shape, BF, 21)
+    d["v"][0, 40, 1, 5] = value
+    y, S = fwd(d)
+    yr, Sr = refer(d)
+    near_where_finite(y, yr, Y, "y")
+    near_where_finite(S, Sr, S32, "h_last")
+
+
+@pytest.mark.parametrize("name", ["k", "dt", "beta", "q"])
+def test_a_nan_of_a_token_reaches_only_later_tokens(name):
+    d = R.make_delta(1, 130, 4, 2, 64, 128, BF, 22)
+    d[name][0, 37, 1] = float("nan")
+    y, S = fwd(d)
+    yr, Sr = refer(d)
+    near_where_finite(y, yr, Y, "y")
+    near_where_finite(S, Sr, S32, "h_last")
+
+
+@pytest.mark.parametrize("L0", [36, 50, 64, 100])
+def test_padding_that_holds_anything(L0):
+    """Tokens behind a sequence's last one, of NaN in every tensor: the ones
+    before them are the call without padding."""
+    d = R.make_delta(2, 130, 4, 2, 64, 64, BF, 23)
+    cut = {k: (d[k][:, :L0].contiguous() if k in ("q", "k", "v", "dt", "beta") else d[k])
+           for k in ("q", "k", "v", "dt", "A", "beta", "dt_bias", "h0")}
+    yr, _ = refer(cut)
+    for k in ("q", "k", "v", "dt", "beta"):
+        d[k][:, L0:] = float("nan")
+    y, S = fwd(d)
+    near(y[:, :L0], yr, Y, "y")
+    assert torch.isnan(S).all() and torch.isnan(y[:, L0:].float()).all()
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=str)
+def test_a_state_that_is_not_finite(shape, value):
+    """In one row of one head: that row only."""
+    d = R.make_delta(*shape, BF, 24)
+    d["h0"][0, 1, 7, 3] = value
+    y, S = fwd(d)
+    yr, Sr = refer(d)
+    near_where_finite(y, yr, Y, "y")
+    near_where_finite(S, Sr, S32, "h_last")
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("power", [20, 24, 30, 36, 60, 100])
+@pytest.mark.parametrize("late", [False, True], ids=["token", "from"])
+def test_a_large_value_leaves_earlier_tokens_alone(shape, power, late):
+    """One token's v (or every one from it on) 2^power times the others'."""
+    d = R.make_delta(*shape, BF, 25)
+    if late:
+        d["v"][:, 40:] *= 2.0 ** power
+    else:
+        d["v"][:, 40] *= 2.0 ** power
+    y, S = fwd(d)
+    yr, Sr = refer(d)
+    near(y[:, :40], yr[:, :40], Y, "before")
+    near(y[:, 40:], yr[:, 40:], Y, "behind")
+    near(S, Sr, S32, "h_last")
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("power", [20, 24, 30, 36, 60])
+def test_a_large_value_that_is_forgotten(shape, power):
+    """A decay of e^-60 or more behind a large token, in its chunk: what follows
+    does not remember it."""
+    d = R.make_delta(*shape, BF, 26)
+    d["v"][:, 20] *= 2.0 ** power
+    d["dt"][:, 30] = 60
+    y, S = fwd(d)
+    yr, Sr = refer(d)
+    near(y[:, :20], yr[:, :20], Y, "before")
+    near(y[:, 30:], yr[:, 30:], Y, "behind")
+    near(S, Sr, S32, "h_last")
+
+
+@pytest.mark.parametrize("what", ["v"])
+@pytest.mark.parametrize("value", [2.0 ** 24, 2.0 ** 36, float("inf"), float("nan")], ids=str)
+def test_gradients_beside_a_large_value(what, value):
+    """A token's v reaches the gradients of no earlier token but through y, which
+    dy does not see; a token's dy reaches those of no later token."""
+    L, at = 130, 40
+    d = R.make_delta(1, L, 4, 2, 64, 128, BF, 27)
+    if value > 1 and value < float("inf"):
+        d[what][:, at] *= value
+    else:
+        d[what][0, at, :, 5] = value
+    g = bwd(d)
+    ref = R.delta_grads(d)
+    if what == "v":
+        near(g["dv"], ref["dv"], G, "dv")
+        near(g["dh0"], ref["dh0"], S32, "dh0")
+        for n, end in (("dq", at), ("dk", at), ("dbeta", at), ("ddt", at + 1)):
+            near(g[n][:, :end], ref[n][:, :end], G, n + " before")
+    else:
+        for n in ("dq", "dk", "dv", "dbeta", "ddt"):
+            near(g[n][:, at + 1:], ref[n][:, at + 1:], G, n + " behind")
+    for n in ("dq", "dk", "dv", "dbeta", "ddt"):  # nothing that is not finite turns finite
+        bad = ~torch.isfinite(ref[n])
+        assert not torch.isfinite(g[n].float().cpu()[bad]).any(), n
