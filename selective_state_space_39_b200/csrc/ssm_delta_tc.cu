@@ -335,10 +335,10 @@ __device__ __forceinline__ bool too_small(float a, float b, float m) {
 __device__ __forceinline__ float size_of(float x, float v, float s) {
   return v != 0.f ? fmaxf(fabsf(x), fabsf(v)) : (x != 0.f ? s : 0.f);
 }
+// By the residuals alone first (of this lane), a third of the instructions: hardly a
+// chunk has one.
 template <int T>
-__device__ __forceinline__ bool wide_rows(const float (&x)[T][4], const float (&v)[T][4], float m0, float m1,
-                                          float s0, float s1) {
-  // by the residuals alone first, a third of the instructions: hardly a chunk has one
+__device__ __forceinline__ bool maybe_wide(const float (&x)[T][4], float m0, float m1) {
   float both0 = m0, both1 = m1, one0 = m0, one1 = m1;
 #pragma unroll
   for (int j = 0; j < T; ++j) {
@@ -347,9 +347,13 @@ __device__ __forceinline__ bool wide_rows(const float (&x)[T][4], const float (&
     one0 = fminf(one0, fminf(fabsf(x[j][0]), fabsf(x[j][1])));
     one1 = fminf(one1, fminf(fabsf(x[j][2]), fabsf(x[j][3])));
   }
-  bool wide = both0 < m0 * 0x1p-24f || both1 < m1 * 0x1p-24f || one0 < m0 * 0x1p-32f || one1 < m1 * 0x1p-32f;
-  if (!__any_sync(0xffffffffu, wide)) return false;
-  wide = false;
+  return both0 < m0 * 0x1p-24f || both1 < m1 * 0x1p-24f || one0 < m0 * 0x1p-32f || one1 < m1 * 0x1p-32f;
+}
+template <int T>
+__device__ __forceinline__ bool wide_rows(bool maybe, const float (&x)[T][4], const float (&v)[T][4], float m0,
+                                          float m1, float s0, float s1) {
+  if (!__any_sync(0xffffffffu, maybe)) return false;
+  bool wide = false;
 #pragma unroll
   for (int j = 0; j < T; ++j) {
     wide |= too_small(size_of(x[j][0], v[j][0], s0), size_of(x[j][1], v[j][1], s0), m0);
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
         // (the backward pass has no registers to keep R and V longer: 483 us for 456; the
         // forward pass alone gains by it: 8192 tokens of 32 heads 393 us, not 397)
-        bool wide = BWD && wide_rows(x, u, m0, m1, big0, big1);
+        bool wide = BWD && wide_rows(maybe_wide(x, m0, m1), x, u, m0, m1, big0, big1);
 
         // ---- meanwhile the next chunk's v, and the readout of the entering state
         if (c + 1 < p.nchunks) fetch(c + 1);
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (BWD) store_state16<N, NS>(S, out16, p.ws_state16 + st_at, lane);
 
         // ---- u = beta T R; K^T (e^(G_end - G) u)
-        if (!BWD) wide = wide_rows(x, u, m0, m1, big0, big1);
+        if (!BWD) wide = wide_rows(maybe_wide(x, m0, m1), x, u, m0, m1, big0, big1);
         ok = wait_warp(&bars[kBarT], par, ok ? p.wait_limit_ns : 0) && ok;
         tm_load(row + kTmU + hcol, x);
         scale_rows(x, r0.inv, r1.inv);
@@ -796,6 +800,96 @@ __device__ __forceinline__ void issue_back(const DeltaChunkParams& p, const Cta&
   }
 }
 
+// The same back: dS [NS / 8][4] from after the chunk to before it, dv (and its rest where
+// `rest`), dv . r and dv . v, both of the products as the walk back leaves them.
+template <int N>
+__device__ __noinline__ void walk_back_tokens(const DeltaChunkParams& p, int b, int h, int pw, int c, bool rest,
+                                              int id, float* mine, const float* other, float* state) {
+  constexpr int NS = N / 2;
+  const DeltaParams& d = p.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hf = (warp >> 2) & 1, kh = h / (d.nheads / d.nkheads);
+  const int64_t t0 = (int64_t)c * kC;
+  const int valid = (int)min((int64_t)kC, d.seqlen - t0);
+  const size_t dot_at = ((((size_t)b * p.nchunks + c) * d.nheads + h) * (d.headdim / 16) + pw / 16) * kC;
+  const float A = d.A[h], bias = d.dt_bias ? d.dt_bias[h] : 0.f;
+  float s[NS / 8][4];
+#pragma unroll
+  for (int j = 0; j < NS / 8; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[j][q] = state[4 * j + q];
+  if (hf == 0)
+    for (int t = valid + lane; t < kC; t += 32) p.ws_dotb[dot_at + t] = p.ws_dotv[dot_at + t] = 0.f;
+#pragma unroll 1
+  for (int t = valid - 1; t >= 0; --t) {
+    const size_t row = (size_t)b * d.seqlen + t0 + t;
+    const size_t from = (row * d.nkheads + kh) * N + hf * NS + 2 * (lane & 3);
+    const uint16_t *kr = static_cast<const uint16_t*>(d.k) + from, *qr = static_cast<const uint16_t*>(d.q) + from;
+    float r[8] = {};  // dS k of both rows; k.k, q.q, k.q
+    uint32_t kv[NS / 8], qv[NS / 8];
+#pragma unroll
+    for (int j = 0; j < NS / 8; ++j) {
+      kv[j] = *reinterpret_cast<const uint32_t*>(kr + 8 * j);
+      qv[j] = *reinterpret_cast<const uint32_t*>(qr + 8 * j);
+      const float k0 = bf16_lo(kv[j]), k1 = bf16_hi(kv[j]), q0 = bf16_lo(qv[j]), q1 = bf16_hi(qv[j]);
+      r[0] = fmaf(s[j][0], k0, fmaf(s[j][1], k1, r[0]));
+      r[1] = fmaf(s[j][2], k0, fmaf(s[j][3], k1, r[1]));
+      r[4] = fmaf(k0, k0, fmaf(k1, k1, r[4]));
+      r[5] = fmaf(q0, q0, fmaf(q1, q1, r[5]));
+      r[6] = fmaf(k0, q0, fmaf(k1, q1, r[6]));
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i) r[i] = quad_sum(r[i]);
+    pair_sum<2>(r, mine, other, id, lane);
+    const float kn = d.qk_norm ? rsqrtf(r[4] + kDeltaQkEps) : 1.f;
+    const float qn = (d.qk_norm ? rsqrtf(r[5] + kDeltaQkEps) : 1.f) * d.scale;
+    const float step = delta_step_size(bf16_to_f32(static_cast<const uint16_t*>(d.dt)[row * d.nheads + h]) + bias,
+                                       d.softplus);
+    const float a = expf(step * A);
+    const float beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d.beta)[row * d.nheads + h]),
+                                  d.beta_sigmoid);
+    const size_t at = (row * d.nheads + h) * d.headdim + pw + (lane >> 2);
+    const uint16_t* v = static_cast<const uint16_t*>(d.v) + at;
+    const float y0 = bf16_to_f32(p.dy[at]) * qn, y1 = bf16_to_f32(p.dy[at + 8]) * qn;
+    const float u0 = kn * fmaf(y0, r[6], r[0]), u1 = kn * fmaf(y1, r[6], r[1]);  // the adjoint of u
+    const float v0 = beta * u0, v1 = beta * u1;
+    float db = fmaf(u0, bf16_to_f32(p.ws_r[at]), u1 * bf16_to_f32(p.ws_r[at + 8])) * delta_beta_floor(beta);
+    float dv = fmaf(v0, bf16_to_f32(v[0]), v1 * bf16_to_f32(v[8]));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      db += __shfl_xor_sync(0xffffffffu, db, o);
+      dv += __shfl_xor_sync(0xffffffffu, dv, o);
+    }
+    if (hf == 0 && lane == 0) {
+      p.ws_dotb[dot_at + t] = db;
+      p.ws_dotv[dot_at + t] = dv;
+    }
+    if (hf == 0 && (lane & 3) == 0) {
+      const uint16_t h0 = f32_to_bf16(v0), h1 = f32_to_bf16(v1);
+      p.dv[at] = h0;
+      p.dv[at + 8] = h1;
+      if (rest) {
+        p.ws_dvlo[at] = f32_to_bf16(v0 - bf16_to_f32(h0));
+        p.ws_dvlo[at + 8] = f32_to_bf16(v1 - bf16_to_f32(h1));
+      }
+    }
+    const float w0 = v0 * kn, w1 = v1 * kn;
+#pragma unroll
+    for (int j = 0; j < NS / 8; ++j) {
+      const float k0 = bf16_lo(kv[j]), k1 = bf16_hi(kv[j]), q0 = bf16_lo(qv[j]), q1 = bf16_hi(qv[j]);
+      s[j][0] = a * fmaf(-w0, k0, fmaf(y0, q0, s[j][0]));
+      s[j][1] = a * fmaf(-w0, k1, fmaf(y0, q1, s[j][1]));
+      s[j][2] = a * fmaf(-w1, k0, fmaf(y1, q0, s[j][2]));
+      s[j][3] = a * fmaf(-w1, k1, fmaf(y1, q1, s[j][3]));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NS / 8; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) state[4 * j + q] = s[j][q];
+  pair_sync(id);  // the buffers are free
+}
+
 // Two warps share a block of 16 rows; up to four blocks.
 template <int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -866,6 +960,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       fetch(p.nchunks - 1);
       float S[NS / 8][4], inv0 = 1.f, inv1 = 1.f;  // the rows of dS
+      bool gone0 = false, gone1 = false;           // rows that have a NaN
       load_state<N, NS>(S, p.dh_last ? p.dh_last + state_at : nullptr, lane);
       auto meet = [&](float& m0, float& m1, int use) {
         put_max(m0, m1, mx + use * kRowWarps * 16, lane);
@@ -879,6 +974,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = pair_and(1 + blk, ok);
         get_max(m0, m1, ox, lane);
         if (!ok) return false;
+        gone0 = m0 != m0;
+        gone1 = m1 != m1;
         const RowScale a = row_scale(exponent_of(m0)), b = row_scale(exponent_of(m1));
         inv0 = a.inv;
         inv1 = b.inv;
@@ -915,6 +1012,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         RowScale r0 = row_scale(exponent_of(m0)), r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
         wrote(&bars[kPutP]);
+        const float top0 = m0, top1 = m1;
+        const bool maybe = maybe_wide(y, m0, m1);
         const bool whole = sc[kScEnd * kC + 5] == 0.f;  // r has a rest in every row
         strong = !whole || sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
         if (strong && whole) {
@@ -945,6 +1044,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         scale_cols(x, sc + kScU * kC + tk, lane);
         row_max(x, m0, m1);
         meet(m0, m1, 2);
+        bool bad0 = not_finite(m0), bad1 = not_finite(m1);
         r0 = row_scale(exponent_of(m0));
         r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(x, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
@@ -966,6 +1066,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (c > 0) fetch(c - 1);
         store_state16<N, NS>(S, out16, p.ws_dstate16 + st_at, lane);
+        bool wide = false;
+        if (__any_sync(0xffffffffu, maybe)) {
+          load_rows(y, vrow + kCol, tk, lc);
+          scale_cols(y, sc + kScP * kC + tk, lane);
+          wide = wide_rows(true, y, y, top0, top1, 0.f, 0.f);
+        }
         load_rows(y, vrow + kCol, tk, lc);
         scale_cols(y, sc + kScSq * kC + tk, lane);
 
@@ -981,44 +1087,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         float n0, n1;
         row_max(y, n0, n1);
         row_max(u, m0, m1);
-        m0 = fmaxf(m0, n0);
-        m1 = fmaxf(m1, n1);
+        m0 = wide ? __uint_as_float(0x7FFFFFFFu) : max_nan(m0, n0);
+        m1 = wide ? m0 : max_nan(m1, n1);
         meet(m0, m1, 3);
+        bad0 |= not_finite(m0);
+        bad1 |= not_finite(m1);
+        const bool alone = __any_sync(0xffffffffu, (bad0 && !gone0) || (bad1 && !gone1));
         r0 = row_scale(exponent_of(m0));
         r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
         tm_pieces<true, TT>(u, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
         wrote(&bars[kPutR]);
-        load_rows(u, vrow + 2 * kCol, tk, lc);
-        row_dots(x, u, p.ws_dotb + dot_at, lane);
-        scale_cols(x, sc + kScRatio * kC + tk, lane);
-        load_rows(u, vrow, tk, lc);
-        row_dots(x, u, p.ws_dotv + dot_at, lane);
-        __syncwarp();
-        stage_rows(x, vrow, tk, lc);
-        store_rows<TT>(vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane);
-        if (strong) {
-          rest_of(x);
+        if (!alone) {
+          load_rows(u, vrow + 2 * kCol, tk, lc);
+          row_dots(x, u, p.ws_dotb + dot_at, lane);
+          scale_cols(x, sc + kScRatio * kC + tk, lane);
+          load_rows(u, vrow, tk, lc);
+          row_dots(x, u, p.ws_dotv + dot_at, lane);
           __syncwarp();
           stage_rows(x, vrow, tk, lc);
-          store_rows<TT>(vrow, tk, p.ws_dvlo + col_at0 + t0 * vs, vs, valid, lane);
+          store_rows<TT>(vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane);
+          if (strong) {
+            rest_of(x);
+            __syncwarp();
+            stage_rows(x, vrow, tk, lc);
+            store_rows<TT>(vrow, tk, p.ws_dvlo + col_at0 + t0 * vs, vs, valid, lane);
+          }
         }
         // ---- dS <- e^G_end dS + dY^T (e^G Q) - dR^T (e^G K), and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
         ok = wait_warp(&bars[kBarU], par, ok ? p.wait_limit_ns : 0) && ok;
         constexpr int G = NS / 8 < 8 ? NS / 8 : 8;
+        if (alone) {
+          float q[NS / 2];
 #pragma unroll
-        for (int i = 0; i < NS / 8; i += G) {
-          float ds[G][4];
-          tm_load(row + kTmU + hf * NS + 8 * i, ds);
+          for (int i = 0; i < NS / 2; ++i) q[i] = S[i / 4][i % 4];
+          walk_back_tokens<N>(p, t.b, h, pw, c, strong, 1 + blk, mx, ox, q);
 #pragma unroll
-          for (int j = 0; j < G; ++j) {
-            float(&q)[4] = S[i + j];
-            const float2 a = fma2(make_float2(q[0], q[1]), make_float2(end, end),
-                                  mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
-            const float2 b = fma2(make_float2(q[2], q[3]), make_float2(end, end),
-                                  mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
-            q[0] = a.x; q[1] = a.y; q[2] = b.x; q[3] = b.y;
+          for (int i = 0; i < NS / 2; ++i) S[i / 4][i % 4] = q[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < NS / 8; i += G) {
+            float ds[G][4];
+            tm_load(row + kTmU + hf * NS + 8 * i, ds);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              float(&q)[4] = S[i + j];
+              const float2 a = fma2(make_float2(q[0], q[1]), make_float2(end, end),
+                                    mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
+              const float2 b = fma2(make_float2(q[2], q[3]), make_float2(end, end),
+                                    mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
+              q[0] = a.x; q[1] = a.y; q[2] = b.x; q[3] = b.y;
+            }
           }
         }
         if (c > 0) ok = put_state(ok);

@@ -187,13 +187,17 @@ def test_a_large_value_that_is_forgotten(shape, power):
     near(S, Sr, S32, "h_last")
 
 
-@pytest.mark.parametrize("what", ["v"])
+@pytest.mark.parametrize("what", ["v", "dy"])
 @pytest.mark.parametrize("value", [2.0 ** 24, 2.0 ** 36, float("inf"), float("nan")], ids=str)
-def test_gradients_beside_a_large_value(what, value):
+@pytest.mark.parametrize("strong", [False, True], ids=["", "strong"])
+def test_gradients_beside_a_large_value(what, value, strong):
     """A token's v reaches the gradients of no earlier token but through y, which
     dy does not see; a token's dy reaches those of no later token."""
     L, at = 130, 40
     d = R.make_delta(1, L, 4, 2, 64, 128, BF, 27)
+    if strong:  # decays of e^-5 .. e^-40 on either side
+        d["dt"][:, 30:32] = 2.5
+        d["dt"][:, 50:53] = 2.5
     if value > 1 and value < float("inf"):
         d[what][:, at] *= value
     else:
@@ -211,3 +215,30 @@ def test_gradients_beside_a_large_value(what, value):
     for n in ("dq", "dk", "dv", "dbeta", "ddt"):  # nothing that is not finite turns finite
         bad = ~torch.isfinite(ref[n])
         assert not torch.isfinite(g[n].float().cpu()[bad]).any(), n
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=str)
+def test_an_adjoint_that_is_not_finite(shape, value):
+    """dh_last in one row of one head: no other row's dv and dh0, and no dq."""
+    d = R.make_delta(*shape, BF, 28)
+    d["dh_last"][0, 1, 7, 3] = value
+    g = bwd(d)
+    ref = R.delta_grads(d)
+    near(g["dq"], ref["dq"], G, "dq")
+    near_where_finite(g["dv"], ref["dv"], G, "dv")
+    near_where_finite(g["dh0"], ref["dh0"], S32, "dh0")
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("power", [20, 28, 36, 60])
+def test_a_large_gradient_leaves_later_tokens_alone(shape, power):
+    """The tokens up to 30 with a dy of 2^power times the others'."""
+    d = R.make_delta(*shape, BF, 29)
+    d["dy"][:, :30] *= 2.0 ** power
+    g = bwd(d)
+    ref = R.delta_grads(d)
+    for n in ("dq", "dk", "dv", "dbeta", "ddt"):
+        near(g[n][:, 30:], ref[n][:, 30:], G, n + " behind")
+        near(g[n][:, :30], ref[n][:, :30], G, n + " before")
+    near(g["dh0"], ref["dh0"], S32, "dh0")
