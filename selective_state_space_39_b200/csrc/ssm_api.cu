@@ -1258,7 +1258,7 @@ static int norm_status(int64_t rows, int64_t dim, int64_t groups, int io, int h)
     return fail(SSM_ERR_UNSUPPORTED, "gated norm: fp32 io needs an fp32 residual");
   if (dim % groups != 0)
     return fail(SSM_ERR_INVALID_ARG, "gated norm: dim must be a multiple of groups");
-  if (groups > 65535 || dim > (1 << 24) || dim / groups > 49152 ||
+  if (groups > 65535 || dim > (1 << 24) || dim / groups > kNormMaxWidth ||
       (double)rows * (double)groups > 2147483647.0 || too_large({rows, dim}))
     return SSM_ERR_UNSUPPORTED;
   return SSM_OK;

@@ -36,6 +36,9 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
+// Shared memory of the widest group's dw sums: the limit of every launch that needs more
+// than 48 KB, so that calls from several threads cannot lower it under one another.
+constexpr int kMaxNormShared = (kNormMaxWidth + 1) * 4;
 
 // V values of type T as they lie in memory: 16-byte units, or (V = 2) two values
 // loaded one by one, the second only where `left`, the values up to the row's
@@ -473,7 +476,7 @@ cudaError_t run_bwd(K* kern, NormParams p, const Shape& s, cudaStream_t stream) 
   const size_t bytes = p.dw ? ((size_t)(s.M ? s.threads / s.T : 1) * p.width + 1) * 4 : 0;
   if (bytes > 48 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxNormShared);
     if (e != cudaSuccess) return e;
   }
   kern<<<dim3(p.slices, p.groups), s.threads, bytes, stream>>>(p, s.T);

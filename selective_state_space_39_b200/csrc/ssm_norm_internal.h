@@ -7,6 +7,8 @@
 
 namespace ssm {
 
+constexpr int kNormMaxWidth = 49152;  // values per group
+
 enum NormGate { kGateNone = 0, kGateFirst = 1, kGateLast = 2 };
 
 struct NormParams {

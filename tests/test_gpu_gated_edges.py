@@ -242,3 +242,44 @@ def test_a_large_gradient_leaves_later_tokens_alone(shape, power):
         near(g[n][:, 30:], ref[n][:, 30:], G, n + " behind")
         near(g[n][:, :30], ref[n][:, :30], G, n + " before")
     near(g["dh0"], ref["dh0"], S32, "dh0")
+
+
+# ------------------------------------------------ calls from two threads -----
+def test_norm_gradients_of_several_widths_from_several_threads():
+    """Rows that are read twice take shared memory for their width: a narrow
+    call's limit must not stand in a wide one's way. The C calls themselves, so
+    that little else is between them."""
+    import threading
+
+    from selective_state_space_39_b200 import gated_norm_bwd_workspace_bytes, lib, ssm_gated_norm_bwd
+    fn, failed, keep = lib().ssm_gated_norm_bwd, [], []
+
+    def calls(args):
+        for _ in range(4000):
+            rc = fn(*args)
+            if rc != 0:
+                failed.append((args[1], rc))
+                return
+
+    threads = []
+    for width in (49152, 16384, 49151, 12416):
+        h, dy = torch.randn(2, 2, width, device="cuda")
+        w = torch.ones(width, device="cuda")
+        dx, dw = torch.zeros_like(dy), torch.zeros_like(w)
+        need = gated_norm_bwd_workspace_bytes(2, width, 1, torch.float32)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        stream = torch.cuda.Stream()
+        keep.append((ssm_gated_norm_bwd(h, w, dy), dx, dw, h, dy, w, ws, stream))
+        p = [t.data_ptr() for t in (h, w, dy, dx, dw, ws)]
+        threads.append(threading.Thread(target=calls, args=((
+            2, width, 1, 0, 0, p[0], 1.0, None, 0, p[1], 1e-5, p[2], None, p[3], None, None, p[4], p[5], need,
+            stream.cuda_stream),)))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for want, dx, dw, *_ in keep:
+        assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"])
