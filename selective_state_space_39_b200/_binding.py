@@ -623,13 +623,21 @@ def _stream_of(stream, dev):
 
 def _streamed(fn):
     """Runs a call given a stream with that stream current, so that its results
-    and its workspace are allocated there too."""
+    and its workspace are allocated there too. The stream is one of the tensors'
+    device: any object's pointer (cuda_stream) is taken as that, a torch stream
+    of another device is refused."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
+        dev = next((t.device for t in (*args, *kw.values())
+                    if isinstance(t, torch.Tensor) and t.is_cuda), None)
+        if dev is None:  # refused by the call itself
+            return fn(*args, **kw)
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream.cuda_stream)
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+        elif stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call

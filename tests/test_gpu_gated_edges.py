@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import delta_ref as R
-from tests.test_gpu_gated_delta import BF, F32Y, G, S32, Y, bwd, check_fwd, cu, fwd, near
+from tests.test_gpu_gated_delta import BF, G, S32, Y, bwd, check_fwd, cu, fwd, near
 
 pytestmark = pytest.mark.gpu
 
@@ -283,3 +283,21 @@ def test_norm_gradients_of_several_widths_from_several_threads():
     assert not failed, failed
     for want, dx, dw, *_ in keep:
         assert torch.equal(dx, want["dx"]) and torch.equal(dw, want["dw"])
+
+
+def test_another_library_s_stream():
+    """An object that has a stream's pointer only."""
+    from selective_state_space_39_b200 import ssm_gated_delta_fwd
+
+    class Foreign:
+        pass
+
+    d = R.make_delta(1, 100, 4, 2, 64, 64, BF, 30)
+    g = [cu(d[k]) for k in ("q", "k", "v", "dt", "A", "beta")]
+    want, S = ssm_gated_delta_fwd(*g)
+    side, f = torch.cuda.Stream(), Foreign()
+    f.cuda_stream = side.cuda_stream
+    side.wait_stream(torch.cuda.current_stream())
+    y, S2 = ssm_gated_delta_fwd(*g, stream=f)
+    side.synchronize()
+    assert torch.equal(y, want) and torch.equal(S, S2)
