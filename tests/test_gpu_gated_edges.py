@@ -301,3 +301,37 @@ def test_another_library_s_stream():
     y, S2 = ssm_gated_delta_fwd(*g, stream=f)
     side.synchronize()
     assert torch.equal(y, want) and torch.equal(S, S2)
+
+
+# ------------------------------------------------ the edges of the dispatch --
+# Chunks from 36 tokens on, or from 6 where tokens times state rows reach 2^17.
+@pytest.mark.parametrize("shape,chunks", [((1, 35, 4, 2, 64, 64), False), ((1, 36, 4, 2, 64, 64), True),
+                                          ((2, 5, 256, 16, 64, 64), False), ((2, 6, 256, 16, 64, 64), True),
+                                          ((1, 7, 128, 16, 128, 128), False), ((1, 8, 128, 16, 128, 128), True),
+                                          ((1, 31, 64, 16, 64, 128), False), ((1, 32, 64, 16, 64, 128), True)],
+                         ids=str)
+def test_both_sides_of_the_dispatch(shape, chunks):
+    from selective_state_space_39_b200 import gated_delta_workspace_bytes
+    assert (gated_delta_workspace_bytes(*shape) > 0) == chunks
+    check_fwd(R.make_delta(*shape, BF, 31), BF, str(shape))
+
+
+@pytest.mark.parametrize("which,by", [("y", 1), ("q", 4), ("k", 4), ("v", 1)])
+def test_a_base_off_16_bytes_goes_token_by_token(which, by):
+    """By `by` bf16 values: the results of the aligned call, to rounding, and
+    nothing written beside y."""
+    d = R.make_delta(1, 100, 2, 1, 32, 64, BF, 13)
+    n = d["v" if which == "y" else which].numel()
+    flat = torch.full((n + 2 * by,), 7.0, dtype=BF, device="cuda")
+    at = flat[by:by + n].view(d["v" if which == "y" else which].shape)
+    if which == "y":
+        y, S = fwd(d, y=at)
+        assert y is at
+    else:
+        at.copy_(d[which])
+        y, S = fwd(dict(d, **{which: at}))
+    yr, Sr = refer(d)
+    near(y, yr, Y, "y")
+    near(S, Sr, S32, "h_last")
+    assert (flat[:by] == 7).all() and (flat[by + n:] == 7).all()
+
