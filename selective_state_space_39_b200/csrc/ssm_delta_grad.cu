@@ -56,10 +56,10 @@ struct GradLayout {
 };
 enum {
   kfGhi, kfGlo, kfBeta, kfKn, kfQn, kfLk, kfLq, kfRow,
-  // of a chunk with a strong decay: the tokens' parts with the entering state (a quarter
-  // of dstate each) and with dS, row sums by column block, column sums by row block,
+  // of strong_gates: the tokens' parts with the entering state and with dS (a quarter of
+  // dstate each), row sums by column block, column sums by row block,
   // the pairs inside a token's own block; the warps' parts of <S, dS>
-  kfIn, kfOut = kfIn + 4, kfRows, kfCols = kfRows + 3, kfOwn = kfCols + 4, kfSum, kfCount
+  kfIn, kfOut = kfIn + 4, kfRows = kfOut + 4, kfCols = kfRows + 3, kfOwn = kfCols + 4, kfSum, kfCount
 };
 
 __host__ __device__ inline GradLayout grad_layout(int N, int P) {
@@ -110,21 +110,49 @@ __device__ __forceinline__ void rows_dot(const float (&t)[T][4], const unsigned 
 }
 
 // The 64 gate threads: dg of the thread's token as a suffix sum over the chunk. so, sv:
-// the token's dy.y and dv.v; end: a part of <S_end, dS_end> per lane.
-__device__ __forceinline__ float suffix_sum(float so, float sv, float end, double* R, int gt) {
+// the token's dy.y and dv.v; end, prev: a lane's part of <S, dS> after and before the
+// chunk, which is the first token's dg (`first`: there is no prev). lost: the sum is small
+// beside its terms, and they are 2^11 times those of the tokens before this one, whose
+// size dg is of (a value far above theirs stands at this one or behind it). terms: the
+// sum of their magnitudes.
+__device__ __forceinline__ float suffix_sum(float so, float sv, float end, float prev, bool first, double* R,
+                                            int gt, float& terms, bool& lost) {
   const int lane = gt & 31;
+  float* const f = reinterpret_cast<float*>(R + 1);
+  float before = terms = fabsf(so) + fabsf(sv);
   // in 64 bits: the terms cancel
   double sum = (double)so - (double)sv, all = end;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const double up = __shfl_down_sync(0xffffffffu, sum, o);
-    if (lane + o < 32) sum += up;
+    const float t = __shfl_down_sync(0xffffffffu, terms, o), b = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane + o < 32) {
+      sum += up;
+      terms += t;
+    }
+    if (lane >= o) before = fmaxf(before, b);
     all += __shfl_xor_sync(0xffffffffu, all, o);
+    prev += __shfl_xor_sync(0xffffffffu, prev, o);
   }
-  if (gt == 32) R[0] = sum;
+  if (gt == 32) {
+    R[0] = sum;
+    f[0] = terms;
+  }
+  if (gt == 31) f[1] = before;
+  before = __shfl_up_sync(0xffffffffu, before, 1);
   asm volatile("bar.sync 1, 64;" ::: "memory");
-  if (gt < 32) sum += R[0];
-  return (float)(sum + all);
+  if (gt < 32) {
+    sum += R[0];
+    terms += f[0];
+  } else {
+    before = lane ? fmaxf(before, f[1]) : f[1];
+  }
+  float dg = (float)(sum + all);
+  // (so written that NaN counts)
+  lost = gt > 0 ? !(terms <= before * 0x1p11f) && !(fabsf(dg) >= terms * 0x1p-11f)
+                : first && !(fabsf(dg) >= terms * 0x1p-11f);
+  if (gt == 0 && !first) dg = prev;
+  return dg;
 }
 
 // The 64 gate threads: ddt of the thread's token from dg, and the chunk's parts of dA
@@ -159,17 +187,16 @@ __device__ __forceinline__ void write_gates(const DeltaChunkParams& p, double* R
   if (gt < 2) p.ws_part[bch * 2 + gt] = R[2 + gt] + R[4 + gt];
 }
 
-// Whether a head has a strong decay in the chunk, or rows that went token by token.
+// Whether a head has a strong decay in the chunk.
 __device__ __forceinline__ bool strong_head(const DeltaChunkParams& p, size_t bch) {
   const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri);
-  return sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] + sc[kScEnd * kC + 5] != 0.f;
+  return sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
 }
 
-// The gates of such a head, over what write_gates left: dg of the tokens behind a strong
-// decay, or of all where a value's size took the rows out of the pieces (the suffix sums
-// of the tokens before it would be lost in it; r and dv then are one bf16 piece), from the
-// pairs on either side. All threads of the CTA, k and q in
-// place; its own function at the kernel's end, so that neither its registers nor its
+// The gates of such a head, or of one with lost suffix sums, over what write_gates left:
+// dg of the tokens behind a strong decay, or lost, from the pairs on either side. (Without
+// a strong decay r and dv are one bf16 piece: 3e-3 of the pairs' sum.) All threads of the
+// CTA, k and q in place; its own function at the kernel's end, so that neither its registers nor its
 // instructions meet the others' products (inside the loop over the heads: 138 us in
 // place of 131 for the kernel where no decay is strong).
 template <int N>
@@ -194,7 +221,7 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
   const size_t gate_at = (row0 + gt) * d.nheads + h;
   float* const red = F + kfSum * kC;
   const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri);
-  const bool whole = sc[kScEnd * kC + 5] == 0.f;
+  const bool strong = strong_head(p, bch), whole = strong && sc[kScEnd * kC + 5] == 0.f;  // r, dv in two pieces
   if (tid < 5 * kC) {
     const int w = tid / kC, i = tid % kC;
     const int from = w == 0 ? kScGhi : (w == 1 ? kScGlo : (w == 2 ? kScBeta : (w == 3 ? kScKn : kScQn)));
@@ -227,13 +254,13 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
       const size_t at = (bch * sl + i) * kC + gt;
       so += p.ws_doto[at];
       sv += p.ws_dotv[at];
-      out += p.ws_doth[at];
+      if (strong) out += p.ws_doth[at];
     }
     const float* prev = c > 0 ? p.ws_end + (bch - d.nheads) * 2 * sl
                               : p.ws_first + ((size_t)b * d.nheads + h) * 2 * sl;
     if (lane < 2 * sl) {
       end = p.ws_end[bch * 2 * sl + lane];
-      if (c > 0 || d.h0) before = prev[lane];
+      if (c > 0 || (d.h0 && strong)) before = prev[lane];
     }
   }
   cp_async_wait_group<0>();
@@ -264,6 +291,31 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
                                    (F[kfQn * kC + r0] * i0 - F[kfKn * kC + r0] * v0);
       F[(kfIn + part) * kC + r1] = ex2_approx(F[kfGhi * kC + r1] + F[kfGlo * kC + r1]) *
                                    (F[kfQn * kC + r1] * i1 - F[kfKn * kC + r1] * v1);
+    }
+  }
+  if (!strong) {  // e^(G_end - G) u . dS k, a quarter of dstate (else the walk back took it)
+    constexpr int T = N / 32;
+    const int tr_row = (lane & 7) + (lane & 8), tr_u = lane >> 4;
+    float t[T][4] = {};
+    for (int kt = 0; kt < P / 16; ++kt) {
+      uint32_t a[4];
+      ldsm4(a, sm + g.r + (mi * 16 + a_row) * g.ps + (2 * kt + a_u) * 16);
+#pragma unroll
+      for (int j = 0; j < T / 2; ++j) {
+        uint32_t bb[4];
+        ldsm4t(bb, sm + g.ds + (16 * kt + tr_row) * g.xs + (part * T + 2 * j + tr_u) * 16);
+        mma_bf16(t[2 * j], a, bb[0], bb[1]);
+        mma_bf16(t[2 * j + 1], a, bb[2], bb[3]);
+      }
+    }
+    float o0, o1;
+    rows_dot<T>(t, smem + g.k, g.xs, r0, part, lane, o0, o1);
+    if ((lane & 3) == 0) {
+      const float gh = F[kfGhi * kC + kC - 1], gl = F[kfGlo * kC + kC - 1];
+      F[(kfOut + part) * kC + r0] = ex2_approx((gh - F[kfGhi * kC + r0]) + (gl - F[kfGlo * kC + r0])) *
+                                    F[kfBeta * kC + r0] * F[kfKn * kC + r0] * o0;
+      F[(kfOut + part) * kC + r1] = ex2_approx((gh - F[kfGhi * kC + r1]) + (gl - F[kfGlo * kC + r1])) *
+                                    F[kfBeta * kC + r1] * F[kfKn * kC + r1] * o1;
     }
   }
   {  // <S, dS>
@@ -372,7 +424,7 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
     // sums over rows from the token on and over columns before it, in its block of 16
     // and, of the parts with the states, in the chunk; totals of whole blocks
     const int K = gt >> 4, l16 = gt & 15;
-    float* const tot = red + kThreads / 32;  // [2 K + J]: rows of block K by column block J; in, out
+    float* const tot = red + kThreads / 32;  // [2 K + J]: rows of block K by column block J; in, out, sizes
     float rs = 0.f, cs = 0.f, in = 0.f;
 #pragma unroll
     for (int J = 0; J < 3; ++J) {
@@ -389,35 +441,61 @@ __device__ __noinline__ void strong_gates(const DeltaChunkParams& p, unsigned ch
 #pragma unroll
     for (int i = 0; i < 4; ++i) in += F[(kfIn + i) * kC + gt];
     out *= F[kfBeta * kC + gt];
+    if (!strong) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out += F[(kfOut + i) * kC + gt];
+    }
+    float size_in = fabsf(in), size_out = fabsf(out);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const float up = __shfl_up_sync(0xffffffffu, out, o), down = __shfl_down_sync(0xffffffffu, in, o);
-      if (lane >= o) out += up;
-      if (lane + o < 32) in += down;
+      const float up2 = __shfl_up_sync(0xffffffffu, size_out, o);
+      const float down2 = __shfl_down_sync(0xffffffffu, size_in, o);
+      if (lane >= o) {
+        out += up;
+        size_out += up2;
+      }
+      if (lane + o < 32) {
+        in += down;
+        size_in += down2;
+      }
       if (o < 16) {
         const float u = __shfl_up_sync(0xffffffffu, cs, o, 16), w = __shfl_down_sync(0xffffffffu, rs, o, 16);
         if (l16 >= o) cs += u;
         if (l16 + o < 16) rs += w;
       }
     }
-    if (gt == 31) tot[9] = out;
-    if (gt == 32) tot[8] = in;
+    if (gt == 31) {
+      tot[9] = out;
+      tot[11] = size_out;
+    }
+    if (gt == 32) {
+      tot[8] = in;
+      tot[10] = size_in;
+    }
     out = __shfl_up_sync(0xffffffffu, out, 1);  // the tokens before this one
+    size_out = __shfl_up_sync(0xffffffffu, size_out, 1);
     cs = __shfl_up_sync(0xffffffffu, cs, 1);
-    if (lane == 0) out = 0.f;
+    if (lane == 0) out = size_out = 0.f;
     if (l16 == 0) cs = 0.f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     double* R = reinterpret_cast<double*>(F + kfRow * kC);
-    float dg = suffix_sum(so, sv, end, R, gt);
-    if (gt < valid && (!whole || delta_step_size(raw, d.softplus) * A < kStrongDecay)) {
+    float terms;
+    bool lost;
+    float dg = suffix_sum(so, sv, end, before, c == 0 && !strong, R, gt, terms, lost);
+    const bool behind = delta_step_size(raw, d.softplus) * A < kStrongDecay;
+    if (gt < valid && (lost || behind)) {
       float s = (F[kfOwn * kC + gt] + rs) + (cs + (in + out));
+      float size = fabsf(F[kfOwn * kC + gt]) + fabsf(rs) + fabsf(cs) + size_in + size_out;
       if (K == 1) s += tot[4] + tot[6];  // rows of blocks behind, columns of blocks before
       if (K == 2) s += tot[6] + tot[7];
       s += K < 2 ? tot[8] : tot[9];
+      size += K < 2 ? tot[10] : tot[11];
       float ss = 0.f;
       for (int i = 0; i < kThreads / 32; ++i) ss += red[i];
-      dg = gt == 0 ? before : s + sc[kScEnd * kC] * ss;
+      ss *= sc[kScEnd * kC];
+      // a lost sum only where the pairs are better: 2^-9 of their terms, it 2^-20 of its
+      if (!behind && size + fabsf(ss) >= terms * 0x1p-11f) lost = false;
+      if ((lost || behind) && (gt > 0 || (c == 0 && !strong))) dg = s + ss;
     }
     write_gates(p, R, dg, gt, gate_at, bch, t0 + gt == 0, gt < valid, raw, A);
   }
@@ -448,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   chain_go();
   chain_wait();
 
-  if (tid == 0) reinterpret_cast<double*>(F + kfRow * kC)[6] = 0.0;
+  if (tid < 2) reinterpret_cast<double*>(F + kfRow * kC)[6 + tid] = 0.0;
 
   // ---- raw k and q
   constexpr int LPR = N / 8;
@@ -466,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
   const bool gate = gt >= 0 && gt < kC;
   const int sl = P / 16;  // at most 8
   uint16_t dt_raw = 0, beta_raw = 0;
-  float A_h = 0.f, bias_h = 0.f, end = 0.f, alone = 0.f;
+  float A_h = 0.f, bias_h = 0.f, end = 0.f, prev = 0.f;
   auto load = [&](int hx) {
     const int h = kh * rep + hx;
     const size_t bch = bc * d.nheads + h;
@@ -509,9 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
     if (gate) {
       // <S_end, dS_end>, over the reverse pass's warps
       end = lane < 2 * sl ? p.ws_end[bch * 2 * sl + lane] : 0.f;
+      prev = c > 0 && lane < 2 * sl ? p.ws_end[(bch - d.nheads) * 2 * sl + lane] : 0.f;
       A_h = d.A[h];
       bias_h = d.dt_bias ? d.dt_bias[h] : 0.f;
-      alone = sc[kScEnd * kC + 5];
       if (gt < valid) {
         dt_raw = static_cast<const uint16_t*>(d.dt)[(row0 + gt) * d.nheads + h];
         beta_raw = static_cast<const uint16_t*>(d.beta)[(row0 + gt) * d.nheads + h];
@@ -556,8 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
         so += dots[(sl + i) * kC];
         sv += dots[(2 * sl + i) * kC];
       }
-      const float dg = suffix_sum(so, sv, end, R, gt);
-      if (alone != 0.f) R[6] = 1.0;
+      float terms;
+      bool lost;
+      const float dg = suffix_sum(so, sv, end, prev, c == 0, R, gt, terms, lost);
+      if (lost && gt < valid && (d.h0 || t0 + gt > 0)) R[7] = 1.0;  // ... of every head
       if (gt < valid) {
         float db = 0.f;
         for (int i = 0; i < sl; ++i) db += dots[i * kC];
@@ -749,10 +829,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_grad_kernel(const __grid_co
 
   // ---- the heads with strong decays
   double* const R = reinterpret_cast<double*>(F + kfRow * kC);
-  if (R[6] == 0.0) return;
+  const bool lost = R[7] != 0.0;
+  if (R[6] == 0.0 && !lost) return;
   __syncthreads();
   for (int hx = 0; hx < rep; ++hx)
-    if (strong_head(p, bc * d.nheads + kh * rep + hx)) {
+    if (lost || strong_head(p, bc * d.nheads + kh * rep + hx)) {
       strong_gates<N>(p, smem, kh * rep + hx);
       __syncthreads();
     }

@@ -1015,7 +1015,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float top0 = m0, top1 = m1;
         const bool maybe = maybe_wide(y, m0, m1);
         const bool whole = sc[kScEnd * kC + 5] == 0.f;  // r has a rest in every row
-        strong = !whole || sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
+        strong = sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
         if (strong && whole) {
           fetch_rows<TT>(out16 - tk * 32, p.ws_rlo + col_at0 + t0 * vs, vs, tk, valid, lane);
           cp_async_commit_group();

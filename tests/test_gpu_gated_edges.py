@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import delta_ref as R
-from tests.test_gpu_gated_delta import BF, G, S32, Y, bwd, check_fwd, cu, fwd, near
+from tests.test_gpu_gated_delta import BF, G, G32, S32, Y, bwd, check_fwd, cu, fwd, near
 
 pytestmark = pytest.mark.gpu
 
@@ -242,6 +242,43 @@ def test_a_large_gradient_leaves_later_tokens_alone(shape, power):
         near(g[n][:, 30:], ref[n][:, 30:], G, n + " behind")
         near(g[n][:, :30], ref[n][:, :30], G, n + " before")
     near(g["dh0"], ref["dh0"], S32, "dh0")
+
+
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("power", [8, 12, 14, 16, 18, 20, 30, 60])
+@pytest.mark.parametrize("late", [False, True], ids=["token", "from"])
+def test_gates_before_a_large_value(N, power, late):
+    """The decays' gradients of the tokens before it, and the heads' sums, which
+    the large ones make up (suffix sums of fp32 row products: G32)."""
+    d = R.make_delta(1, 130, 4, 2, 64, N, BF, 25)
+    if late:
+        d["v"][:, 40:] *= 2.0 ** power
+    else:
+        d["v"][:, 40] *= 2.0 ** power
+    g = bwd(d)
+    ref = R.delta_grads(d)
+    near(g["ddt"][:, :41], ref["ddt"][:, :41], G, "before")
+    near(g["ddt"][:, 41:], ref["ddt"][:, 41:], G, "behind")
+    for n in ("dA", "ddt_bias"):
+        near(g[n], ref[n], G32, n)
+
+
+def test_gates_around_tokens_of_zeros():
+    """Sequences that begin, pause and end with tokens of zeros (padding): their
+    decays act on the state alone, or on nothing."""
+    d = R.make_delta(1, 200, 4, 2, 64, 64, BF, 32, h0=False)
+    for k in ("q", "k", "v", "dy"):
+        d[k][:, :80] = 0
+        d[k][:, 110:125] = 0
+        d[k][:, 180:] = 0
+    g = bwd(d)
+    ref = R.delta_grads(d)
+    assert not g["ddt"][:, :81].any() and not g["ddt"][:, 180:].any()
+    for n in ("dq", "dk", "dv", "dbeta", "ddt"):
+        near(g[n], ref[n], G, n)
+    near(g["ddt"][:, 110:125], ref["ddt"][:, 110:125], G, "ddt of the pause")
+    for n in ("dA", "ddt_bias"):
+        near(g[n], ref[n], G32, n)
 
 
 # ------------------------------------------------ calls from two threads -----
