@@ -501,9 +501,10 @@ int ssm_gated_delta_update(int64_t batch, int64_t nheads, int64_t nkheads, int64
  * headdim axis 16-byte aligned. workspace: ssm_gated_delta_bwd_workspace_bytes
  * (about 8 * headdim * dstate / 64 bytes per token and head), 16-byte aligned.
  * Sums run in a fixed order. As in the forward call, 16 rows that meet a value
- * (of v, dy or a state) that is not finite or far above the others go through
- * that chunk token by token, so that it reaches no gradient that does not
- * depend on it. No output may overlap an input, another output or the
+ * (of v, dy or a state) that is not finite or far above the others go token by
+ * token, through that chunk or, from dy or dh_last, back through the sequence
+ * (about 1 us a token): it reaches no gradient that does not depend on it. No
+ * output may overlap an input, another output or the
  * workspace.
  */
 size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,

@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- P u
         tm_pieces<BWD, TT>(x, r0.s, r1.s, row + kTmS + tcol / 2, row + kTmS + 32 + tcol / 2);
         wrote(&bars[kPutP]);
-        if (BWD && !alone) store_rows<TT>(vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane);
+        if (BWD) store_rows<TT>(vrow, tk, p.ws_r + col_at0 + t0 * vs, vs, valid, lane);
 
         // ---- S <- e^G_end S + K^T u, and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
@@ -800,33 +800,28 @@ __device__ __forceinline__ void issue_back(const DeltaChunkParams& p, const Cta&
   }
 }
 
-// The same back: dS [NS / 8][4] from after the chunk to before it, dv (and its rest where
-// `rest`), dv . r and dv . v, both of the products as the walk back leaves them.
+// The same back, for the 16 rows' whole sequence over what the walk left of it: everything
+// that the walk writes, from dh_last on. (Chunk by chunk inside the walk, as forward, it
+// cost the walk 8 % where no row needs it: 158 us for 2 x 2048 tokens of 32 heads of 128.)
 template <int N>
-__device__ __noinline__ void walk_back_tokens(const DeltaChunkParams& p, int b, int h, int pw, int c, bool rest,
-                                              int id, float* mine, const float* other, float* state) {
+__device__ __noinline__ void walk_back_tokens(const DeltaChunkParams& p, int b, int h, int pw, int id, float* mine,
+                                              const float* other) {
   constexpr int NS = N / 2;
   const DeltaParams& d = p.d;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hf = (warp >> 2) & 1, kh = h / (d.nheads / d.nkheads);
-  const int64_t t0 = (int64_t)c * kC;
-  const int valid = (int)min((int64_t)kC, d.seqlen - t0);
-  const size_t dot_at = ((((size_t)b * p.nchunks + c) * d.nheads + h) * (d.headdim / 16) + pw / 16) * kC;
+  const int hf = (warp >> 2) & 1, kh = h / (d.nheads / d.nkheads), pb = d.headdim / 16;
   const float A = d.A[h], bias = d.dt_bias ? d.dt_bias[h] : 0.f;
+  const size_t state_at = ((size_t)b * d.nheads + h) * ((size_t)d.headdim * N) + (size_t)pw * N + hf * NS;
   float s[NS / 8][4];
-#pragma unroll
-  for (int j = 0; j < NS / 8; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) s[j][q] = state[4 * j + q];
-  if (hf == 0)
-    for (int t = valid + lane; t < kC; t += 32) p.ws_dotb[dot_at + t] = p.ws_dotv[dot_at + t] = 0.f;
-#pragma unroll 1
-  for (int t = valid - 1; t >= 0; --t) {
-    const size_t row = (size_t)b * d.seqlen + t0 + t;
+  load_state<N, NS>(s, p.dh_last ? p.dh_last + state_at : nullptr, lane);
+  // a token's columns of k and q, its S k (of both rows; here dS k), k.k, q.q, k.q, and gates
+  uint32_t kv[NS / 8], qv[NS / 8];
+  float r[8], kn, qn, a, beta;
+  auto token = [&](size_t row) {
     const size_t from = (row * d.nkheads + kh) * N + hf * NS + 2 * (lane & 3);
     const uint16_t *kr = static_cast<const uint16_t*>(d.k) + from, *qr = static_cast<const uint16_t*>(d.q) + from;
-    float r[8] = {};  // dS k of both rows; k.k, q.q, k.q
-    uint32_t kv[NS / 8], qv[NS / 8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < NS / 8; ++j) {
       kv[j] = *reinterpret_cast<const uint32_t*>(kr + 8 * j);
@@ -841,53 +836,101 @@ __device__ __noinline__ void walk_back_tokens(const DeltaChunkParams& p, int b, 
 #pragma unroll
     for (int i = 0; i < 7; ++i) r[i] = quad_sum(r[i]);
     pair_sum<2>(r, mine, other, id, lane);
-    const float kn = d.qk_norm ? rsqrtf(r[4] + kDeltaQkEps) : 1.f;
-    const float qn = (d.qk_norm ? rsqrtf(r[5] + kDeltaQkEps) : 1.f) * d.scale;
-    const float step = delta_step_size(bf16_to_f32(static_cast<const uint16_t*>(d.dt)[row * d.nheads + h]) + bias,
-                                       d.softplus);
-    const float a = expf(step * A);
-    const float beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d.beta)[row * d.nheads + h]),
-                                  d.beta_sigmoid);
-    const size_t at = (row * d.nheads + h) * d.headdim + pw + (lane >> 2);
-    const uint16_t* v = static_cast<const uint16_t*>(d.v) + at;
-    const float y0 = bf16_to_f32(p.dy[at]) * qn, y1 = bf16_to_f32(p.dy[at + 8]) * qn;
-    const float u0 = kn * fmaf(y0, r[6], r[0]), u1 = kn * fmaf(y1, r[6], r[1]);  // the adjoint of u
-    const float v0 = beta * u0, v1 = beta * u1;
-    float db = fmaf(u0, bf16_to_f32(p.ws_r[at]), u1 * bf16_to_f32(p.ws_r[at + 8])) * delta_beta_floor(beta);
-    float dv = fmaf(v0, bf16_to_f32(v[0]), v1 * bf16_to_f32(v[8]));
+    kn = d.qk_norm ? rsqrtf(r[4] + kDeltaQkEps) : 1.f;
+    qn = (d.qk_norm ? rsqrtf(r[5] + kDeltaQkEps) : 1.f) * d.scale;
+    const size_t at = row * d.nheads + h;
+    a = expf(delta_step_size(bf16_to_f32(static_cast<const uint16_t*>(d.dt)[at]) + bias, d.softplus) * A);
+    beta = delta_beta(bf16_to_f32(static_cast<const uint16_t*>(d.beta)[at]), d.beta_sigmoid);
+  };
+  auto rows_sum = [&](float x) {  // over the 16 rows
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      db += __shfl_xor_sync(0xffffffffu, db, o);
-      dv += __shfl_xor_sync(0xffffffffu, dv, o);
-    }
-    if (hf == 0 && lane == 0) {
-      p.ws_dotb[dot_at + t] = db;
-      p.ws_dotv[dot_at + t] = dv;
-    }
-    if (hf == 0 && (lane & 3) == 0) {
-      const uint16_t h0 = f32_to_bf16(v0), h1 = f32_to_bf16(v1);
-      p.dv[at] = h0;
-      p.dv[at + 8] = h1;
-      if (rest) {
-        p.ws_dvlo[at] = f32_to_bf16(v0 - bf16_to_f32(h0));
-        p.ws_dvlo[at + 8] = f32_to_bf16(v1 - bf16_to_f32(h1));
+    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+#pragma unroll 1
+  for (int c = p.nchunks - 1; c >= 0; --c) {
+    const int64_t t0 = (int64_t)c * kC;
+    const int valid = (int)min((int64_t)kC, d.seqlen - t0);
+    const size_t bch = ((size_t)b * p.nchunks + c) * d.nheads + h, dot_at = (bch * pb + pw / 16) * kC;
+    const float* sc = reinterpret_cast<const float*>(p.ws_head + bch * (size_t)p.head_bytes + 4 * kDeltaTri);
+    const bool strong = sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f, whole = sc[kScEnd * kC + 5] == 0.f;
+    {  // dS after the chunk, its product with the state
+      const float* after = p.ws_state + bch * ((size_t)d.headdim * N) + (size_t)pw * N + hf * 16 * NS;
+      uint16_t* out = p.ws_dstate16 + bch * ((size_t)d.headdim * N) + (size_t)(pw + (lane >> 2)) * N + hf * NS +
+                      2 * (lane & 3);
+      const float dot = tiles_dot<NS>(s, after, lane);
+      if (lane == 0) p.ws_end[(bch * pb + pw / 16) * 2 + hf] = dot;
+#pragma unroll
+      for (int j = 0; j < NS / 8; ++j) {
+        *reinterpret_cast<uint32_t*>(out + 8 * j) = pack_bf16x2(s[j][0], s[j][1]);
+        *reinterpret_cast<uint32_t*>(out + 8 * N + 8 * j) = pack_bf16x2(s[j][2], s[j][3]);
       }
     }
-    const float w0 = v0 * kn, w1 = v1 * kn;
+    if (strong) {  // r . e^(G_end - G) dS k
+      float e = 1.f;
+#pragma unroll 1
+      for (int t = valid - 1; t >= 0; --t) {
+        const size_t row = (size_t)b * d.seqlen + t0 + t, at = (row * d.nheads + h) * d.headdim + pw + (lane >> 2);
+        token(row);
+        float r0 = bf16_to_f32(p.ws_r[at]), r1 = bf16_to_f32(p.ws_r[at + 8]);
+        if (whole) {
+          r0 += bf16_to_f32(p.ws_rlo[at]);
+          r1 += bf16_to_f32(p.ws_rlo[at + 8]);
+        }
+        const float dot = rows_sum(e * kn * fmaf(r[0], r0, r[1] * r1));
+        if (hf == 0 && lane == 0) p.ws_doth[dot_at + t] = dot;
+        e *= a;
+      }
+    }
+    if (hf == 0)
+      for (int t = valid + lane; t < kC; t += 32) p.ws_doth[dot_at + t] = p.ws_dotb[dot_at + t] = p.ws_dotv[dot_at + t] = 0.f;
+#pragma unroll 1
+    for (int t = valid - 1; t >= 0; --t) {
+      const size_t row = (size_t)b * d.seqlen + t0 + t, at = (row * d.nheads + h) * d.headdim + pw + (lane >> 2);
+      token(row);
+      const uint16_t* v = static_cast<const uint16_t*>(d.v) + at;
+      const float y0 = bf16_to_f32(p.dy[at]) * qn, y1 = bf16_to_f32(p.dy[at + 8]) * qn;
+      const float u0 = kn * fmaf(y0, r[6], r[0]), u1 = kn * fmaf(y1, r[6], r[1]);  // the adjoint of u
+      const float v0 = beta * u0, v1 = beta * u1;
+      const float db = rows_sum(fmaf(u0, bf16_to_f32(p.ws_r[at]), u1 * bf16_to_f32(p.ws_r[at + 8]))) *
+                       delta_beta_floor(beta);
+      const float dv = rows_sum(fmaf(v0, bf16_to_f32(v[0]), v1 * bf16_to_f32(v[8])));
+      if (hf == 0 && lane == 0) {
+        p.ws_dotb[dot_at + t] = db;
+        p.ws_dotv[dot_at + t] = dv;
+      }
+      if (hf == 0 && (lane & 3) == 0) {
+        const uint16_t h0 = f32_to_bf16(v0), h1 = f32_to_bf16(v1);
+        p.dv[at] = h0;
+        p.dv[at + 8] = h1;
+        if (strong) {
+          p.ws_dvlo[at] = f32_to_bf16(v0 - bf16_to_f32(h0));
+          p.ws_dvlo[at + 8] = f32_to_bf16(v1 - bf16_to_f32(h1));
+        }
+      }
+      const float w0 = v0 * kn, w1 = v1 * kn;
 #pragma unroll
-    for (int j = 0; j < NS / 8; ++j) {
-      const float k0 = bf16_lo(kv[j]), k1 = bf16_hi(kv[j]), q0 = bf16_lo(qv[j]), q1 = bf16_hi(qv[j]);
-      s[j][0] = a * fmaf(-w0, k0, fmaf(y0, q0, s[j][0]));
-      s[j][1] = a * fmaf(-w0, k1, fmaf(y0, q1, s[j][1]));
-      s[j][2] = a * fmaf(-w1, k0, fmaf(y1, q0, s[j][2]));
-      s[j][3] = a * fmaf(-w1, k1, fmaf(y1, q1, s[j][3]));
+      for (int j = 0; j < NS / 8; ++j) {
+        const float k0 = bf16_lo(kv[j]), k1 = bf16_hi(kv[j]), q0 = bf16_lo(qv[j]), q1 = bf16_hi(qv[j]);
+        s[j][0] = a * fmaf(-w0, k0, fmaf(y0, q0, s[j][0]));
+        s[j][1] = a * fmaf(-w0, k1, fmaf(y0, q1, s[j][1]));
+        s[j][2] = a * fmaf(-w1, k0, fmaf(y1, q0, s[j][2]));
+        s[j][3] = a * fmaf(-w1, k1, fmaf(y1, q1, s[j][3]));
+      }
     }
   }
+  if (p.dh0) store_state<N, NS>(s, p.dh0 + state_at, lane);
+  if (d.h0) {
+    float z[NS / 8][4], dot = 0.f;
+    load_state<N, NS>(z, d.h0 + state_at, lane);
 #pragma unroll
-  for (int j = 0; j < NS / 8; ++j)
+    for (int j = 0; j < NS / 8; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) state[4 * j + q] = s[j][q];
-  pair_sync(id);  // the buffers are free
+      for (int q = 0; q < 4; ++q) dot = fmaf(z[j][q], s[j][q], dot);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) p.ws_first[(((size_t)b * d.nheads + h) * pb + pw / 16) * 2 + hf] = dot;
+  }
 }
 
 // Two warps share a block of 16 rows; up to four blocks.
@@ -960,7 +1003,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       fetch(p.nchunks - 1);
       float S[NS / 8][4], inv0 = 1.f, inv1 = 1.f;  // the rows of dS
-      bool gone0 = false, gone1 = false;           // rows that have a NaN
       load_state<N, NS>(S, p.dh_last ? p.dh_last + state_at : nullptr, lane);
       auto meet = [&](float& m0, float& m1, int use) {
         put_max(m0, m1, mx + use * kRowWarps * 16, lane);
@@ -974,8 +1016,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = pair_and(1 + blk, ok);
         get_max(m0, m1, ox, lane);
         if (!ok) return false;
-        gone0 = m0 != m0;
-        gone1 = m1 != m1;
         const RowScale a = row_scale(exponent_of(m0)), b = row_scale(exponent_of(m1));
         inv0 = a.inv;
         inv1 = b.inv;
@@ -988,6 +1028,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return true;
       };
       bool ok = put_state(true), strong = false;  // a strong decay in the chunk
+      bool alone = false;  // a row has met a value that the pieces do not hold
       int st = 0;
       uint32_t fpar = 0;
       for (int s = 0; ok && s < p.nchunks; ++s) {
@@ -1013,7 +1054,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
         wrote(&bars[kPutP]);
         const float top0 = m0, top1 = m1;
-        const bool maybe = maybe_wide(y, m0, m1);
         const bool whole = sc[kScEnd * kC + 5] == 0.f;  // r has a rest in every row
         strong = sc[kScEnd * kC + 3] + sc[kScEnd * kC + 4] != 0.f;
         if (strong && whole) {
@@ -1026,6 +1066,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tm_load(row + kTmX + tcol, x);
         scale_rows(x, inv0, inv1);
         scale_cols(x, sc + kScKend * kC + tk, lane);
+        const bool maybe = maybe_wide(y, top0, top1);
         if (strong) {
 #pragma unroll
           for (int j = 0; j < TT; ++j)
@@ -1044,7 +1085,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         scale_cols(x, sc + kScU * kC + tk, lane);
         row_max(x, m0, m1);
         meet(m0, m1, 2);
-        bool bad0 = not_finite(m0), bad1 = not_finite(m1);
+        alone |= not_finite(m0) || not_finite(m1);
         r0 = row_scale(exponent_of(m0));
         r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(x, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
@@ -1090,55 +1131,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         m0 = wide ? __uint_as_float(0x7FFFFFFFu) : max_nan(m0, n0);
         m1 = wide ? m0 : max_nan(m1, n1);
         meet(m0, m1, 3);
-        bad0 |= not_finite(m0);
-        bad1 |= not_finite(m1);
-        const bool alone = __any_sync(0xffffffffu, (bad0 && !gone0) || (bad1 && !gone1));
+        alone |= not_finite(m0) || not_finite(m1);
         r0 = row_scale(exponent_of(m0));
         r1 = row_scale(exponent_of(m1));
         tm_pieces<true, TT>(y, r0.s, r1.s, row + kTmO + tcol / 2, row + kTmO + 32 + tcol / 2);
         tm_pieces<true, TT>(u, r0.s, r1.s, row + kTmX + tcol / 2, row + kTmX + 32 + tcol / 2);
         wrote(&bars[kPutR]);
-        if (!alone) {
-          load_rows(u, vrow + 2 * kCol, tk, lc);
-          row_dots(x, u, p.ws_dotb + dot_at, lane);
-          scale_cols(x, sc + kScRatio * kC + tk, lane);
-          load_rows(u, vrow, tk, lc);
-          row_dots(x, u, p.ws_dotv + dot_at, lane);
+        load_rows(u, vrow + 2 * kCol, tk, lc);
+        row_dots(x, u, p.ws_dotb + dot_at, lane);
+        scale_cols(x, sc + kScRatio * kC + tk, lane);
+        load_rows(u, vrow, tk, lc);
+        row_dots(x, u, p.ws_dotv + dot_at, lane);
+        __syncwarp();
+        stage_rows(x, vrow, tk, lc);
+        store_rows<TT>(vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane);
+        if (strong) {
+          rest_of(x);
           __syncwarp();
           stage_rows(x, vrow, tk, lc);
-          store_rows<TT>(vrow, tk, p.dv + col_at0 + t0 * vs, vs, valid, lane);
-          if (strong) {
-            rest_of(x);
-            __syncwarp();
-            stage_rows(x, vrow, tk, lc);
-            store_rows<TT>(vrow, tk, p.ws_dvlo + col_at0 + t0 * vs, vs, valid, lane);
-          }
+          store_rows<TT>(vrow, tk, p.ws_dvlo + col_at0 + t0 * vs, vs, valid, lane);
         }
         // ---- dS <- e^G_end dS + dY^T (e^G Q) - dR^T (e^G K), and its pieces for the next chunk
         const float end = sc[kScEnd * kC];
         ok = wait_warp(&bars[kBarU], par, ok ? p.wait_limit_ns : 0) && ok;
         constexpr int G = NS / 8 < 8 ? NS / 8 : 8;
-        if (alone) {
-          float q[NS / 2];
 #pragma unroll
-          for (int i = 0; i < NS / 2; ++i) q[i] = S[i / 4][i % 4];
-          walk_back_tokens<N>(p, t.b, h, pw, c, strong, 1 + blk, mx, ox, q);
+        for (int i = 0; i < NS / 8; i += G) {
+          float ds[G][4];
+          tm_load(row + kTmU + hf * NS + 8 * i, ds);
 #pragma unroll
-          for (int i = 0; i < NS / 2; ++i) S[i / 4][i % 4] = q[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < NS / 8; i += G) {
-            float ds[G][4];
-            tm_load(row + kTmU + hf * NS + 8 * i, ds);
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-              float(&q)[4] = S[i + j];
-              const float2 a = fma2(make_float2(q[0], q[1]), make_float2(end, end),
-                                    mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
-              const float2 b = fma2(make_float2(q[2], q[3]), make_float2(end, end),
-                                    mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
-              q[0] = a.x; q[1] = a.y; q[2] = b.x; q[3] = b.y;
-            }
+          for (int j = 0; j < G; ++j) {
+            float(&q)[4] = S[i + j];
+            const float2 a = fma2(make_float2(q[0], q[1]), make_float2(end, end),
+                                  mul2(make_float2(ds[j][0], ds[j][1]), make_float2(r0.inv, r0.inv)));
+            const float2 b = fma2(make_float2(q[2], q[3]), make_float2(end, end),
+                                  mul2(make_float2(ds[j][2], ds[j][3]), make_float2(r1.inv, r1.inv)));
+            q[0] = a.x; q[1] = a.y; q[2] = b.x; q[3] = b.y;
           }
         }
         if (c > 0) ok = put_state(ok);
@@ -1150,8 +1178,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fpar ^= 1u;
         }
       }
+      ok = pair_and(1 + blk, ok);  // the pair stays together
       if (!ok) {
         if (lane == 0) atomicExch(&g_delta_timeout, 1);
+      } else if (__any_sync(0xffffffffu, alone)) {
+        walk_back_tokens<N>(p, t.b, h, pw, 1 + blk, mx, ox);
+        strong = false;
       } else if (p.dh0) {
         store_state<N, NS>(S, p.dh0 + state_at, lane);
       }
