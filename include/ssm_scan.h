@@ -455,8 +455,12 @@ int ssm_ssd_state_update(int64_t batch, int64_t nheads, int64_t headdim, int64_t
  * in fp32. So do, inside a chunked call, 16 rows of a state through a chunk in
  * which one of them meets a value that is not finite, or one 2^24 times that of
  * two neighbouring tokens (2^32 times that of a single one), about 1 us a token:
- * no value changes the results of the tokens before it, whatever its size. y
- * may be NULL when h_last is given; h_last may be h0.
+ * no value changes the results of the tokens before it, whatever its size. All
+ * rows of a head do, where a chunk's keys as they are (no qk_norm) differ by
+ * 2^16 in length, a beta as it is reaches 2^10, or writes grow by 2^20. y's own
+ * products take one fp16 piece of S, of u and of q . k: where a token's y is what
+ * is left of larger terms (a large value overwritten, in its chunk or the next),
+ * it is off by up to 2^-12 of those, beside its rounding. y may be NULL when h_last is given; h_last may be h0.
  * workspace: at least ssm_gated_delta_workspace_bytes(...) bytes of device
  * memory, 16-byte aligned (may be NULL when that is 0), used as scratch only;
  * not by two calls that can run at the same time. seqlen == 0 writes only

@@ -77,6 +77,11 @@ constexpr float kBetaFloor = 1.f / 67108864.f;
 // or asked for meets it). A head and chunk with such a decay takes about 11 us more of
 // an SM: from e^-4 on, ordinary layers would pay 15 us of 450 for a few of them.
 constexpr float kStrongDecay = -5.f;
+// A row of T or P stands under one scale too. With unit-length keys and beta below 1 its
+// entries are alike; a chunk whose keys differ by 2^16 in length, or with a beta of 2^10,
+// or whose T grows to 2^20 goes token by token: its first kScSk is NaN, and the walks
+// find a value that is not finite in every row.
+constexpr float kOddKeys = 65536.f, kOddBeta = 1024.f, kOddT = 1048576.f;
 // A lower triangular 64 x 64 fp16 tile: its ten 16 x 16 blocks (i, j <= i),
 // column of blocks by column, 512 bytes each, as 2 x 2 core matrices of eight
 // rows of 16 bytes (the tensor cores' layout without a swizzle; any eight rows

@@ -278,6 +278,16 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
       __syncthreads();
       if (xg < nh) {
         const float ehi = sc[kScGhi * kC + kC - 1], elo = sc[kScGlo * kC + kC - 1];
+        if (!d_.qk_norm || !d_.beta_sigmoid) {
+          // the longest and the shortest key (those of zeros aside), and a large beta
+          const float len = tok[i], odd = fabsf(sc[kScBeta * kC + i]) >= kOddBeta ? INFINITY : len;
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(odd));
+          const uint32_t least = __reduce_min_sync(0xffffffffu, __float_as_uint(len > 0x1p-110f ? len : INFINITY));
+          if (lane == 0) {
+            sc[kScEnd * kC + 8 + (warp & 1)] = __uint_as_float(most);
+            sc[kScEnd * kC + 10 + (warp & 1)] = __uint_as_float(least);
+          }
+        }
         const float lo = sc[kScGlo * kC + i];
         const float D = ex2_approx(hi + lo), E = ex2_approx((ehi - hi) + (elo - lo));
         sc[kScSk * kC + i] = D * tok[i];
@@ -465,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
         }
       }
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if (m >= kOddT) sc[kScSk * kC] = __uint_as_float(0x7FFFFFFFu);
       const RowScale s = row_scale(exponent_of(m));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -484,6 +495,10 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(const DeltaChun
         if (BWD) sc[kScBeta * kC + row] *= sc[kScRatio * kC + row];
         rows_s[row] = s.s;
       }
+    }
+    if (tid == 0 && (!d_.qk_norm || !d_.beta_sigmoid)) {
+      const float* e = sc + kScEnd * kC + 8;
+      if (fmaxf(e[0], e[1]) > fminf(e[2], e[3]) * kOddKeys) sc[kScSk * kC] = __uint_as_float(0x7FFFFFFFu);
     }
     __syncthreads();
     if (BWD) {  // T^T: column `row` of T, eight rows of a block at a time

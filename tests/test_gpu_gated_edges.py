@@ -281,6 +281,76 @@ def test_gates_around_tokens_of_zeros():
         near(g[n], ref[n], G32, n)
 
 
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("power", [12, 18, 24, 40, 100])
+@pytest.mark.parametrize("at", [0, 40, 63])
+def test_a_long_key(shape, power, at):
+    """Keys as they are (qk_norm off), one 2^power times the others: at a token
+    that writes nothing (no state yet, v = 0) it changes nothing; at a later one
+    the tokens before it."""
+    d = R.make_delta(*shape, BF, 33, h0=at > 0)
+    d["k"] = (d["k"].float() / 12).to(BF)
+    d["k"][:, at] *= 2.0 ** power
+    if at == 0:
+        d["v"][:, 0] = 0
+    d["dh_last"] = None
+    y, S = fwd(d, qk_norm=False)
+    g = bwd(d, qk_norm=False)
+    yr, Sr = refer(d, qk_norm=False)
+    ref = R.delta_grads(d, qk_norm=False)
+    if at == 0:
+        near(y, yr, Y, "y")
+        near(S, Sr, S32, "h_last")
+        for n in ("dq", "dv", "dbeta", "ddt"):
+            near(g[n], ref[n], G, n)
+        near(g["dk"][:, 1:], ref["dk"][:, 1:], G, "dk")
+    else:
+        near(y[:, :at], yr[:, :at], Y, "y before")
+        near(g["dq"][:, :at], ref["dq"][:, :at], G, "dq before")
+
+
+@pytest.mark.parametrize("power", [9, 20, 40])
+@pytest.mark.parametrize("at", [0, 30, 63])
+def test_a_large_write_strength(power, at):
+    """beta as it is, one 2^power: nothing before it changes (and nothing at all
+    where there is nothing to write)."""
+    d = R.make_delta(1, 130, 4, 2, 64, 64, BF, 34, h0=at > 0)
+    d["beta"] = torch.sigmoid(d["beta"].float()).to(BF)
+    d["beta"][:, at] = 2.0 ** power
+    if at == 0:
+        d["v"][:, 0] = 0
+    d["dh_last"] = None
+    y, S = fwd(d, beta_sigmoid=False)
+    yr, Sr = refer(d, beta_sigmoid=False)
+    if at == 0:
+        near(y, yr, Y, "y")
+        near(S, Sr, S32, "h_last")
+    else:
+        near(y[:, :at], yr[:, :at], Y, "y before")
+
+
+def test_a_recurrence_that_grows():
+    """Steps beyond 2 / |k|^2: every write overshoots, the state grows by a factor
+    of two a token for a while, then falls. y's products take one fp16 piece
+    each of the state, u and P (2^-12, three of them), so a token's y is off by
+    that of the largest y that its sum went through, beside its rounding."""
+    d = R.make_delta(1, 100, 2, 1, 32, 64, BF, 35, h0=False)
+    d["k"][:] = d["k"][:, :1]
+    d["dt"][:] = -20
+    d["beta"] = torch.full_like(d["beta"], 0.5)
+    d["beta"][:, 20:34] = 3.0
+    y, S = fwd(d, beta_sigmoid=False)
+    yr, Sr = refer(d, beta_sigmoid=False)
+    y = y.double().cpu()
+    for t in range(100):
+        off, most = (y[:, t] - yr[:, t]).norm(), yr[:, :t + 1].abs().max() * yr[:, t].numel() ** 0.5
+        assert off <= Y[0] * yr[:, t].norm() + 3 * 2.0 ** -12 * most, t
+    # a rounding of the state at its peak stays where keys do not reach: fp32's 2^-24 of
+    # the peak, at each of the few steps that are near it
+    peak = refer(dict(d, **{k: d[k][:, :34] for k in ("q", "k", "v", "dt", "beta")}), beta_sigmoid=False)[1].norm()
+    assert (S.double().cpu() - Sr).norm() <= S32[0] * Sr.norm() + 4 * 2.0 ** -24 * peak
+
+
 # ------------------------------------------------ calls from two threads -----
 def test_norm_gradients_of_several_widths_from_several_threads():
     """Rows that are read twice take shared memory for their width: a narrow
