@@ -919,8 +919,7 @@ int ssm_compose_carries(int64_t rank, int64_t batch, int64_t dim, int64_t dstate
 
 // ---- gated delta rule ---------------------------------------------------------
 
-// The sizes of a call; `chunked`: whether the chunk kernels hold it (bf16 io and
-// the sizes of delta_chunk_supported).
+// The sizes of a call.
 struct DeltaDims {
   int64_t batch, seqlen, nheads, nkheads, headdim, dstate;
   int io;

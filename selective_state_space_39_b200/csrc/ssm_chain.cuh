@@ -27,9 +27,9 @@ inline cudaError_t launch_chained(void (*kern)(P), dim3 grid, int threads, int b
 
 // Before the first read of what the preceding kernel of the call wrote.
 __device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next kernel's blocks may take the places that this kernel's leave; only
-// called once a block holds its tensor memory, so that none of them can wait
-// for columns that a waiting successor has taken.
+// The next kernel's blocks may take the places that this kernel's leave. A kernel
+// that holds tensor memory calls it once a block has its columns, so that none of
+// them can wait for columns that a waiting successor has taken; the others at once.
 __device__ __forceinline__ void chain_go() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

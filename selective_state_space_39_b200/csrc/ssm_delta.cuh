@@ -82,19 +82,18 @@ __device__ __forceinline__ uint32_t col_at(int row, int half) {
 
 // ------------------------------------- fp32 operands as two pieces of fp16 --
 // x s = hi + lo with hi, lo fp16 and s a power of two that brings the largest
-// magnitude of the row to [2^14, 2^15) (the carried state: to about 2^6, with
-// room to grow): the two pieces carry 22 bits of every element within 2^16
-// (2^8) of the largest, and smaller ones to 2^-40 (2^-32) of the
-// largest, so products keep fp32's accuracy at two MMAs (three where both
-// operands have two pieces; the dropped lo lo is 2^-24 of the product).
+// magnitude of the row to [2^14, 2^15): the two pieces carry 22 bits of every
+// element within 2^16 of the largest, and smaller ones to 2^-40 of the largest
+// (what a row's scale must not hide goes token by token, ssm_delta_tc.cu), so
+// products keep fp32's accuracy at two MMAs (three where both operands have two
+// pieces; the dropped lo lo is 2^-24 of the product).
 // bf16 operands (k, q) are one exact fp16 piece under a row scale of their own.
 struct RowScale {
   float s, inv;
 };
-// s = 2^(top - e) for a largest magnitude of biased exponent e (top: the
-// exponent it is brought to)
-template <uint32_t top = 14>
+// s = 2^(14 - e) for a largest magnitude of biased exponent e
 __device__ __forceinline__ RowScale row_scale(uint32_t e) {
+  constexpr uint32_t top = 14;
   e = e < 1u + top ? 1u + top : (e > 253u ? 253u : e);
   RowScale r;
   r.s = __uint_as_float((254u + top - e) << 23);

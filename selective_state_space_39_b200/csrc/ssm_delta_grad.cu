@@ -21,7 +21,8 @@
 // pairs for the tokens of its rows, column sums for those of its columns. r and dv
 // then come as two bf16 pieces (2^-16); S and dS stay one, for they matter only to the
 // chunk's first and last tokens: the first one's dg is <S_end, dS_end> of the chunk
-// before, and the walk back takes the parts with dS in fp32. One CTA per chunk and key
+// before, and the walk back takes the parts with dS in fp32. The same serves tokens
+// whose suffix sum is lost in the products of far larger tokens behind them. One CTA per chunk and key
 // head adds its value heads in order, so dq and dk are written once, through
 // x / |x| when q and k were scaled to unit length. Operands are bf16 (q, k, dy
 // exactly; S, dS, r, dv and the weights rounded once), sums fp32: the outputs
@@ -33,12 +34,13 @@
 // the states' while the weights are computed, the next head's while the last
 // products run. Two warps without weights take the gates meanwhile.
 //
-// 2 x 2048 tokens, 32 heads of 128 on 16 key heads, dstate 128: 137 us for
-// 25.8 GFLOP and 300 MB. Bound: the phases of a head (copies, weights, products
-// with the states, products with the weights) follow one another with all warps:
-// tensor pipe 32 % busy, DRAM 34 %. It was 176 us with the gates after the
-// products, 148 with dy and dv meeting S one after the other and the weights
-// stored element by element.
+// 2 x 2048 tokens, 32 heads of 128 on 16 key heads, dstate 128: 132 us for
+// 25.8 GFLOP and 300 MB, and about 11 us for a round of heads with strong decays.
+// Bound: the phases of a head (copies, weights, products with the states,
+// products with the weights) follow one another with all warps: tensor pipe 32 %
+// busy, DRAM 34 %. It was 176 us with the gates after the products, 148 with dy
+// and dv meeting S one after the other and the weights stored element by element,
+// 137 with k k^T and its column sums for dbeta.
 #include "ssm_delta.cuh"
 
 namespace ssm {

@@ -73,8 +73,7 @@ constexpr float kBetaFloor = 1.f / 67108864.f;
 // From here on a decay's gradient, about e^g of the terms that suffix sums make it
 // of (2^-24 each), comes from the pairs of tokens on either side (ssm_delta_grad.cu).
 // Suffix sums leave a head's dA off by 5e-4 at e^-5, 4e-3 at e^-8 and all of it at
-// e^-16, the pairs 1e-6 at any decay (and 3e-3 of a single token where a state given
-// or asked for meets it). A head and chunk with such a decay takes about 11 us more of
+// e^-16, the pairs 1e-6 at any decay. A head and chunk with such a decay takes about 11 us more of
 // an SM: from e^-4 on, ordinary layers would pay 15 us of 450 for a few of them.
 constexpr float kStrongDecay = -5.f;
 // A row of T or P stands under one scale too. With unit-length keys and beta below 1 its

@@ -21,7 +21,7 @@
 // fp16 rows, k k^T and q k^T (fp16 MMAs) are shared by the heads. Below the
 // diagonal blocks the decay is a product of a row's and a column's factor
 // around the start of the row's block, e^(G_i - G_s) e^(G_s - G_j), neither
-// above 1; inside them it is taken from the difference itself.
+// above 1 where no decay is; inside them it is taken from the difference itself.
 //
 // Bound: the latencies of about 1900 instructions per warp and head, at four CTAs
 // per SM (issue slots 53 % busy, tensor pipe 20 %, DRAM 2.3 TB/s): 219 us for

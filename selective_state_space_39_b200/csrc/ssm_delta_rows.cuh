@@ -34,12 +34,12 @@ constexpr int kMaxBlocks = 8;  // 16-row blocks per CTA
 // buffers of `tiles` column tiles (64 tokens x 16 columns).
 constexpr int kCol = kC * 32;  // bytes of a column tile
 struct Layout {
-  int kq, head, head_off, heads, tiles, stage;  // bytes; heads of a CTA; column tiles
+  int kq, head, head_off, heads, stage;  // bytes; heads of a CTA
 };
 // `blocks` 16-row blocks per CTA out of heads of `per_head` blocks each; the
-// bytes from head_off of every head block.
-__host__ __device__ inline Layout layout(int dstate, int blocks, int per_head, int tiles,
-                                         int head_bytes, int head_off) {
+// bytes from head_off of every head block (the walk back starts at the factors).
+__host__ __device__ inline Layout layout(int dstate, int blocks, int per_head, int head_bytes,
+                                         int head_off) {
   Layout l;
   l.head_off = head_off;
   l.kq = 2 * kC * dstate * 2;
@@ -47,7 +47,6 @@ __host__ __device__ inline Layout layout(int dstate, int blocks, int per_head, i
   l.heads = per_head % blocks == 0 ? 1
             : blocks % per_head == 0 ? blocks / per_head
                                      : (blocks + per_head - 2) / per_head + 1;
-  l.tiles = tiles;
   l.stage = (l.kq + l.heads * l.head + 1023) / 1024 * 1024;  // the swizzle's period
   return l;
 }

@@ -36,13 +36,16 @@
 // Precision: everything on the state's path is a product of two pieces per
 // operand (k and q are exact in one; lo lo is left out), so the carried state,
 // dh0 and the gate gradients keep fp32's accuracy; for y, rounded to bf16, one
-// fp16 piece (2^-12) of S, u and P is taken.
+// fp16 piece (2^-12) of S, u and P is taken: beside its rounding y is off by
+// that of its terms, which shows where they cancel (a second piece of P is 5 KB
+// more per chunk and head; the backward pass, which sums dy . y, has it). Rows
+// whose values one scale does not hold go token by token (walk_tokens).
 //
 // Bound: the chain of a chunk (products, commits, tensor memory loads, row maxima,
 // splitting), in every head at once: 8192 tokens of 32 heads of 128, dstate 128
-// take 302 us, 2.4 us per chunk (128 CTAs of 32 rows); 4 x 4096 tokens of 64 heads of 64: 253 us, 4.0 us per
+// take 312 us, 2.4 us per chunk (128 CTAs of 32 rows); 4 x 4096 tokens of 64 heads of 64: 265 us, 4.1 us per
 // chunk (128 CTAs of 128 rows; tensor pipe 27 % busy, DRAM 2.4 TB/s). For the
-// backward pass, 2 x 2048 tokens of 32 heads of 128: 125 us, and 151 us back; both
+// backward pass, 2 x 2048 tokens of 32 heads of 128: 129 us, and 147 us back; both
 // move a state per chunk (2.6 TB/s).
 //
 // Tensor memory (512 columns), forward: 0 S pieces, then u's pieces for P; 128 K S, R's
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pb = d.headdim / 16;
   const Cta t = cta_of(p);
-  const Layout l = layout(N, p.blocks, pb, kTiles, BWD ? kDeltaLoadBwd : kDeltaHeadFwd, 0);
+  const Layout l = layout(N, p.blocks, pb, BWD ? kDeltaLoadBwd : kDeltaHeadFwd, 0);
   if (threadIdx.x == 0) {
     const uint32_t warps = (uint32_t)t.active * SP;
     for (int i = 0; i < p.stages; ++i) {
@@ -947,7 +950,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pb = d.headdim / 16;
   const Cta t = cta_of(p);
-  const Layout l = layout(N, p.blocks, pb, kTiles, kDeltaLoadBwd, 4 * kDeltaTri);
+  const Layout l = layout(N, p.blocks, pb, kDeltaLoadBwd, 4 * kDeltaTri);
   if (threadIdx.x == 0) {
     const uint32_t warps = (uint32_t)t.active * 2;
     for (int i = 0; i < p.stages; ++i) {
@@ -1219,7 +1222,7 @@ cudaError_t run(K* one, K* two, DeltaChunkParams p, int tiles, int head_bytes, i
                 cudaStream_t stream) {
   const int per_head = p.d.headdim / 16, group = p.d.nheads / p.d.nkheads * per_head;
   const int64_t groups = (int64_t)p.d.batch * p.d.nkheads;
-  auto lay = [&](int blocks) { return layout(N, blocks, per_head, tiles, head_bytes, 0); };
+  auto lay = [&](int blocks) { return layout(N, blocks, per_head, head_bytes, 0); };
   auto extra = [&](int blocks) { return blocks * (2 * tiles * kCol + block_bytes) + 1024; };
   auto stages_of = [&](int blocks) {
     return std::min(kMaxStages, (kMaxShared - extra(blocks)) / lay(blocks).stage);

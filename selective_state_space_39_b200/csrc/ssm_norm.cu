@@ -20,10 +20,11 @@
 // blocks by a second kernel, always in the same order.
 //
 // Bound: memory traffic (forward: x, z, residual in, y, h out; backward: h,
-// dy, z, dh in, dx, dz, dresidual out). Measured (CUDA graph): forward with an
-// fp32 residual, 16384 x 4096 bf16, 119 us = 6.8 TB/s; gated backward of
-// 131072 x 128 bf16, 39 us = 4.3 TB/s, the sigmoid and its derivative beside
-// the loads; 1000 x 1537 fp32 backward, 16 us, the latency of a few rows.
+// dy, z, dh in, dx, dz, dresidual out). Measured, calls in a row: forward with an
+// fp32 residual, 16384 x 4096 bf16, 124 us = 6.5 TB/s (119 us in a graph's
+// replay, whose last writes partly stay in L2); gated backward of 131072 x 128
+// bf16, 41 us = 4.1 TB/s, the sigmoid and its derivative beside the loads; 1000 x
+// 1537 fp32 backward, 19 us, 16 of it the latency of a few rows.
 #include <algorithm>
 #include <type_traits>
 
@@ -445,14 +446,14 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const NormParams p) {
 struct Shape {
   int V, T, M, threads;  // M units per thread; 0: the row is read twice
 };
-Shape shape(const NormParams& p, int types, bool vec, int max_m) {
+Shape shape(const NormParams& p, int types, bool vec) {
   Shape s;
   s.V = vec ? (types == 2 ? 4 : 8) : 2;
   const int units = (p.width + s.V - 1) / s.V;
   s.T = 8;
   while (s.T < 512 && s.T * 2 < units) s.T *= 2;
   const int m = (units + s.T - 1) / s.T;
-  s.M = m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 ? 4 : m <= max_m ? max_m : 0;
+  s.M = m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 ? 4 : 0;
   s.threads = std::max(s.T, kThreads);
   return s;
 }
@@ -516,7 +517,7 @@ cudaError_t gated(const NormParams& p, const Shape& s, cudaStream_t st) {
 }
 template <bool BWD>
 cudaError_t typed(const NormParams& p, int types, bool vec, cudaStream_t st) {
-  const Shape s = shape(p, types, vec, 4);
+  const Shape s = shape(p, types, vec);
   if (types == 2) return vec ? gated<BWD, float, float, 4>(p, s, st) : gated<BWD, float, float, 2>(p, s, st);
   if (types == 1)
     return vec ? gated<BWD, uint16_t, float, 8>(p, s, st) : gated<BWD, uint16_t, float, 2>(p, s, st);
