@@ -449,14 +449,17 @@ int ssm_ssd_state_update(int64_t batch, int64_t nheads, int64_t headdim, int64_t
  * ssm_gated_delta_fwd -- the gated delta rule over a sequence. bf16 io with
  * dstate 64 or 128, headdim a multiple of 16, at least 36 tokens (from 6 on
  * over a state of many rows) and 16-byte aligned q, k, v and y runs chunk by
- * chunk (64 tokens) on the tensor cores, every product on the state's path in two fp16 pieces per fp32 operand, so
- * that h_last is as exact as fp32 arithmetic; other calls run token by token
- * in fp32. So do, inside a chunked call, 16 rows of a state through a chunk in
- * which one of them meets a value that is not finite, or one 2^24 times that of
- * two neighbouring tokens (2^32 times that of a single one), about 1 us a token:
- * no value changes the results of the tokens before it, whatever its size. All
- * rows of a head do, where a chunk's keys as they are (no qk_norm) differ by
- * 2^16 in length, a beta as it is reaches 2^10, or writes grow by 2^20.
+ * chunk (64 tokens) on the tensor cores, every product on the state's path in
+ * two fp16 pieces per fp32 operand, so that h_last is as exact as fp32
+ * arithmetic; other calls run token by token in fp32. So do, inside a chunked
+ * call, 16 rows of a state through a chunk in which one of them meets a value
+ * that is not finite, or one 2^24 times that of two neighbouring tokens (2^32
+ * times that of a single one), about 1 us a token: no value changes the results
+ * of the tokens before it, whatever its size. All rows of a head do, where a
+ * chunk's keys as they are (no qk_norm) differ by 2^16 in length, a beta as it
+ * is reaches 2^10, or writes grow by 2^20. A row of the state has one scale for
+ * the products that read it: they see its columns to 2^-40 of the largest one,
+ * which only keys and queries that miss the large columns altogether can tell.
  * y's own products take one fp16 piece of S, of u and of q . k: where a token's
  * y is what is left of larger terms (a large value overwritten, in its chunk or
  * the next), it is off by up to 2^-12 of those, beside its rounding. y may be
@@ -509,8 +512,7 @@ int ssm_gated_delta_update(int64_t batch, int64_t nheads, int64_t nkheads, int64
  * (of v, dy or a state) that is not finite or far above the others go token by
  * token, through that chunk or, from dy or dh_last, back through the sequence
  * (about 1 us a token): it reaches no gradient that does not depend on it. No
- * output may overlap an input, another output or the
- * workspace.
+ * output may overlap an input, another output or the workspace.
  */
 size_t ssm_gated_delta_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,
                                            int64_t nkheads, int64_t headdim, int64_t dstate,

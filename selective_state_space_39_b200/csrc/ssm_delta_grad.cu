@@ -26,8 +26,8 @@
 // head adds its value heads in order, so dq and dk are written once, through
 // x / |x| when q and k were scaled to unit length. Operands are bf16 (q, k, dy
 // exactly; S, dS, r, dv and the weights rounded once), sums fp32: the outputs
-// are bf16 themselves (dq, dk: 3.0e-3 from the exact ones in the 2-norm, 1.7e-3
-// of it the last rounding). <S_end, dS_end> comes from the reverse pass, in fp32.
+// are bf16 themselves (dq, dk: 3.0e-3 from the exact ones in the 2-norm, dbeta,
+// whose r is rounded once, 2.3e-3; 1.7e-3 of it the last rounding). <S_end, dS_end> comes from the reverse pass, in fp32.
 //
 // One CTA of sixteen warps fills an SM's shared memory: a warp takes 16 tokens
 // by a quarter of the columns; the head's tiles come by asynchronous copies,

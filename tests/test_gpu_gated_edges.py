@@ -351,6 +351,30 @@ def test_a_recurrence_that_grows():
     assert (S.double().cpu() - Sr).norm() <= S32[0] * Sr.norm() + 4 * 2.0 ** -24 * peak
 
 
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("power", [12, 18])
+def test_state_columns_of_different_sizes(shape, power):
+    """Unit keys by turns of two columns, one column's values 2^power times the
+    other's: each column for itself. Two pieces see the small one to 2^-40 of the
+    large one's size, 2^-22 of its own at least; y's one piece of it has 2^-12."""
+    d = R.make_delta(*shape, BF, 36, h0=False)
+    L = shape[1]
+    d["k"].zero_()
+    d["k"][:, 0::2, :, 0] = 1
+    d["k"][:, 1::2, :, 1] = 1
+    d["q"].zero_()
+    g = torch.Generator().manual_seed(37)
+    at = torch.randint(0, 2, (L,), generator=g)
+    d["q"][:, torch.arange(L), :, at] = 1
+    d["v"][:, 0::2] *= 2.0 ** power
+    y, S = fwd(d)
+    yr, Sr = refer(d)
+    for c in range(2):
+        near(y[:, at == c], yr[:, at == c], Y, f"y of column {c}")
+        near(S[..., c], Sr[..., c], S32, f"column {c}")
+    assert not S[..., 2:].any()
+
+
 # ------------------------------------------------ calls from two threads -----
 def test_norm_gradients_of_several_widths_from_several_threads():
     """Rows that are read twice take shared memory for their width: a narrow
